@@ -548,6 +548,115 @@ moe_status moe_grouped_gemm_fp8_masked(const void* a, const float* a_scale, cons
                                        size_t ws_bytes, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Microscaled (MX) tensors (an addition; the pages' quantised expert op is
+ * another system's).  A row of K values is padded with zeros to Kp = K rounded
+ * up to a multiple of 128 and held as
+ *   codes   MOE_MX_E4M3: [rows, Kp] bytes, float8 e4m3;
+ *           MOE_MX_E2M1: [rows, Kp / 2] bytes, 4-bit floats (0, 0.5, 1, 1.5,
+ *           2, 3, 4, 6 and their negatives), the even column in the low half
+ *   scales  [rows, Kp / 32] bytes, one power of two per 32 columns: byte s
+ *           stands for 2^(s - 127), 255 for NaN (e8m0).
+ * The scale of a block with largest magnitude amax is 2^(floor(log2 amax) - 2)
+ * for e2m1 (magnitudes above 6 scales saturate) and the smallest power of two
+ * with amax / scale <= 448 for e4m3, both at least 2^-127; a block that holds
+ * an infinity or a NaN gets the NaN scale and zero codes.  Codes are rounded
+ * to nearest, ties to even. */
+typedef enum moe_mx_format { MOE_MX_E4M3 = 0, MOE_MX_E2M1 = 1 } moe_mx_format;
+
+/* x [rows, K] dtype, row_stride elements between rows (row_stride >= K), to
+ * codes and scales.  codes and scales 16-byte aligned (MOE_ERR_UNSUPPORTED
+ * otherwise); rows * Kp < 2^34. */
+moe_status moe_mx_quantize(const void* x, int64_t rows, int K, int64_t row_stride,
+                           moe_dtype dtype, int format, void* codes, void* scales,
+                           cudaStream_t stream);
+/* out [rows, K] dtype = codes * scales (exact in bf16 and f32; rounded, and
+ * infinite past its range, in f16).  codes and scales as above. */
+moe_status moe_mx_dequantize(const void* codes, const void* scales, int64_t rows, int K,
+                             int format, moe_dtype dtype, void* out, cudaStream_t stream);
+
+/* Residual addition, root-mean-square norm and the result in 8 bits, in one
+ * launch (an addition: the step in front of the layer, which makes the
+ * operands of the quantised products).  Per row t, in float32:
+ *   h = round(x[t] + residual[t]) to dtype, or x[t] without a residual
+ *   y = h * rsqrt(mean(h^2) + eps) * weight
+ *   residual_out[t] = h;  out[t] = round(y) to dtype
+ *   codes, scales: y (not its rounded copy) as
+ *     MOE_QUANT_MX_E4M3         an MX e4m3 row (above), or
+ *     MOE_QUANT_E4M3_BLOCK128   e4m3 codes [T, Hp] and one float32 scale per
+ *                               128 columns [T, Hp / 128], max(amax / 448,
+ *                               2^-126): the operand rows of
+ *                               moe_grouped_gemm_fp8_masked.  A block with an
+ *                               infinity or a NaN: NaN scale, zero codes.
+ *     MOE_QUANT_NONE            codes and scales NULL
+ *   x, residual, residual_out, out [T, H] dtype;  weight [H] dtype
+ *   residual and residual_out are passed together or not at all;
+ *   residual_out may be residual itself (an update in place; any other overlap
+ *   of an output with an input is MOE_ERR_OVERLAP).  out may be NULL.
+ * H <= 65536; codes and scales 16-byte aligned (MOE_ERR_UNSUPPORTED
+ * otherwise). */
+typedef enum moe_quant_kind {
+  MOE_QUANT_NONE = 0,
+  MOE_QUANT_MX_E4M3 = 1,
+  MOE_QUANT_E4M3_BLOCK128 = 2
+} moe_quant_kind;
+moe_status moe_add_rms_norm(const void* x, const void* residual, const void* weight, int T, int H,
+                            moe_dtype dtype, float eps, int quant, void* residual_out, void* out,
+                            void* codes, void* scales, cudaStream_t stream);
+
+/* Grouped GEMM of MX e4m3 rows by MX e2m1 weights over the tight layout (an
+ * addition next to moe_grouped_gemm_act / _down and the FP8 GEMM: 4-bit
+ * weights take a quarter of the bytes).  For each expert e and each row m in
+ * [seg_end[e-1], seg_end[e]):
+ *   p = a_row(m) . w[e, n, :] (+ bias[e, n])   in fp32, scales applied per block
+ *   out[m, j] = act(p)_j
+ * on the tensor cores (kind::mxf8f6f4, scales applied in the MMA).
+ *   a, a_scale   MX e4m3 rows [a_rows, Kp], [a_rows, Kp / 32]
+ *   row_to_route [M] i32: row m of the operand is a[row_to_route[m] / top_k]
+ *                (an entry outside [0, a_rows * top_k) gives a zero row); NULL:
+ *                row m is a[m], a_rows >= M, top_k ignored
+ *   w, w_scale   MX e2m1 rows [E, N1, Kp / 2], [E, N1, Kp / 32], N1 = 2N for a
+ *                gated act (rows as moe_grouped_gemm_act), N otherwise
+ *   bias         [E, N1] dtype or NULL;  act NULL for the plain product
+ *   out_scale    NULL: out [M, N] dtype (MOE_BF16 or MOE_F16).  Otherwise out
+ *                and out_scale are MX e4m3 rows [M, Np], [M, Np / 32] of the
+ *                unrounded act(p): the next product's operand
+ *   ws           >= moe_grouped_gemm_mx_workspace_size(M, N, K, E) bytes
+ * a 16-byte, w 32-byte, the scales 4-byte aligned, and out and out_scale
+ * 16-byte aligned when MX (MOE_ERR_UNSUPPORTED otherwise, and for MOE_F32).
+ * Rows past seg_end[E-1] are not written.  E <= 1024. */
+moe_status moe_grouped_gemm_mx(const void* a, const void* a_scale, int a_rows,
+                               const int32_t* row_to_route, int top_k, const void* w,
+                               const void* w_scale, const void* bias, const int32_t* seg_end,
+                               int M, int N, int K, int E, moe_dtype dtype,
+                               const moe_act_params* act, void* out, void* out_scale, void* ws,
+                               size_t ws_bytes, cudaStream_t stream);
+size_t moe_grouped_gemm_mx_workspace_size(int M, int N, int K, int E);
+
+/* The routed forward over microscaled operands: moe_ffn_forward with hidden as
+ * MX e4m3 rows (moe_add_rms_norm or moe_mx_quantize make them) and both weight
+ * stacks as MX e2m1.  Routing, index maps and combine as moe_ffn_forward; the
+ * gate_up product reads its rows through row_to_route and writes the gated
+ * activation as MX e4m3 rows, the down product writes dtype rows.  Four
+ * launches when E <= 512.
+ *   hidden, hidden_scale        [T, Hp], [T, Hp / 32]
+ *   w_gate_up, w_gate_up_scale  [E, N1, Hp / 2], [E, N1, Hp / 32]
+ *   w_down, w_down_scale        [E, H, Fp / 2], [E, H, Fp / 32]
+ *   b_gate_up [E, N1], b_down [E, H] dtype or NULL;  out [T, H] dtype (MOE_BF16
+ *   or MOE_F16);  the other arguments as moe_ffn_forward (no MoERouter slice:
+ *   p->local_expert_count must be 0);  alignment as moe_grouped_gemm_mx;
+ *   ws >= moe_workspace_size_mx(T, H, F, E, K). */
+moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, const void* logits,
+                              const void* w_gate_up, const void* w_gate_up_scale,
+                              const void* w_down, const void* w_down_scale,
+                              const float* correction_bias, const int32_t* expert_ids,
+                              const void* b_gate_up, const void* b_down, int T, int H, int F,
+                              int E, moe_dtype dtype, const moe_route_params* p,
+                              const moe_act_params* act, void* out, float* topk_weights_out,
+                              int32_t* topk_ids_out, void* ws, size_t ws_bytes,
+                              cudaStream_t stream);
+size_t moe_workspace_size_mx(int T, int H, int F, int E, int K);
+
+/* ------------------------------------------------------------------------ */
 /* Shared expert [TileOPs, SharedExpertMLPFwdOp]: the dense gated MLP applied
  * to every token,
  *     out = down(silu(hidden @ gate^T) * (hidden @ up^T)),

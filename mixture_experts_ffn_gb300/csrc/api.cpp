@@ -927,6 +927,208 @@ moe_status moe_ffn_forward_shared(const void* hidden, const void* logits, const 
                         stream);
 }
 
+// ---------------------------------------------------------------- microscaled operands
+namespace {
+size_t mx_pad(int K) { return ((size_t)K + 127) / 128 * 128; }
+bool mx_format_ok(int f) { return f == MOE_MX_E4M3 || f == MOE_MX_E2M1; }
+size_t mx_code_bytes(size_t rows, int K, int format) {
+  return format == MOE_MX_E2M1 ? rows * mx_pad(K) / 2 : rows * mx_pad(K);
+}
+bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+// rows and columns of an MX tensor whose 8-column groups a kernel counts in 31 bits
+bool mx_extent_ok(int64_t rows, int K) {
+  return rows >= 0 && K >= 1 && K <= (1 << 24) && rows < (1LL << 31) &&
+         (double)rows * (double)mx_pad(K) < 17179869184.0;
+}
+// extents of a grouped product over MX operands
+bool mx_gemm_extent_ok(long long M, int N, int K, int E) {
+  return M >= 0 && M < (1LL << 30) && N >= 1 && N <= (1 << 24) && K >= 1 && K <= (1 << 24) &&
+         E >= 1 && E <= kMaxExperts;
+}
+}  // namespace
+
+moe_status moe_mx_quantize(const void* x, int64_t rows, int K, int64_t row_stride,
+                           moe_dtype dtype, int format, void* codes, void* scales,
+                           cudaStream_t stream) {
+  if (!dtype_ok(dtype) || !mx_format_ok(format) || !mx_extent_ok(rows, K) || row_stride < K ||
+      row_stride > (1LL << 40))
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!x || !codes || !scales || !aligned(x, esize(dtype))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales)) return MOE_ERR_UNSUPPORTED;
+  Span outs[] = {{codes, mx_code_bytes((size_t)rows, K, format)},
+                 {scales, (size_t)rows * mx_pad(K) / 32}};
+  Span ins[] = {{x, ((size_t)(rows - 1) * row_stride + K) * esize(dtype)}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  return cuda_status(
+      launch_mx_quantize(x, rows, K, row_stride, dtype, format, codes, scales, stream));
+}
+
+moe_status moe_mx_dequantize(const void* codes, const void* scales, int64_t rows, int K,
+                             int format, moe_dtype dtype, void* out, cudaStream_t stream) {
+  if (!dtype_ok(dtype) || !mx_format_ok(format) || !mx_extent_ok(rows, K))
+    return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!codes || !scales || !out || !aligned(out, esize(dtype))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales)) return MOE_ERR_UNSUPPORTED;
+  Span outs[] = {{out, (size_t)rows * K * esize(dtype)}};
+  Span ins[] = {{codes, mx_code_bytes((size_t)rows, K, format)},
+                {scales, (size_t)rows * mx_pad(K) / 32}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  return cuda_status(launch_mx_dequantize(codes, scales, rows, K, format, dtype, out, stream));
+}
+
+moe_status moe_add_rms_norm(const void* x, const void* residual, const void* weight, int T, int H,
+                            moe_dtype dtype, float eps, int quant, void* residual_out, void* out,
+                            void* codes, void* scales, cudaStream_t stream) {
+  if (!dtype_ok(dtype) || T < 0 || H < 1 || H > 65536 || !(eps >= 0.f) || !std::isfinite(eps) ||
+      quant < MOE_QUANT_NONE || quant > MOE_QUANT_E4M3_BLOCK128)
+    return MOE_ERR_INVALID_ARG;
+  const bool q = quant != MOE_QUANT_NONE;
+  if (!residual != !residual_out || !codes == q || !scales == q) {
+    // an empty batch needs no buffers
+    if (T != 0) return MOE_ERR_INVALID_ARG;
+  }
+  if (T == 0) return MOE_OK;
+  if (!x || !weight) return MOE_ERR_INVALID_ARG;
+  const size_t esz = esize(dtype), n = (size_t)T * H * esz, Hp = mx_pad(H);
+  for (const void* ptr : {x, residual, weight, (const void*)residual_out, (const void*)out})
+    if (!aligned(ptr, esz)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales)) return MOE_ERR_UNSUPPORTED;
+  const size_t sb = quant == MOE_QUANT_MX_E4M3 ? (size_t)T * (Hp / 32) : (size_t)T * (Hp / 128) * 4;
+  Span outs[] = {{residual_out, n}, {out, n}, {codes, q ? (size_t)T * Hp : 0}, {scales, q ? sb : 0}};
+  Span ins[] = {{x, n}, {residual == residual_out ? nullptr : residual, n},
+                {weight, (size_t)H * esz}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  return cuda_status(launch_rms_norm(x, residual, weight, T, H, dtype, eps, quant, residual_out,
+                                     out, codes, scales, stream));
+}
+
+size_t moe_grouped_gemm_mx_workspace_size(int M, int N, int K, int E) {
+  if (!mx_gemm_extent_ok(M, N, K, E)) return 0;
+  return MOE_STATUS_BYTES;
+}
+
+moe_status moe_grouped_gemm_mx(const void* a, const void* a_scale, int a_rows,
+                               const int32_t* row_to_route, int top_k, const void* w,
+                               const void* w_scale, const void* bias, const int32_t* seg_end,
+                               int M, int N, int K, int E, moe_dtype dtype,
+                               const moe_act_params* act, void* out, void* out_scale, void* ws,
+                               size_t ws_bytes, cudaStream_t stream) {
+  if (!mx_gemm_extent_ok(M, N, K, E) || !dtype_ok(dtype) || (act && !act_ok(act)) || a_rows < 0 ||
+      (row_to_route ? top_k < 1 : a_rows < M))
+    return MOE_ERR_INVALID_ARG;
+  if (dtype == MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (!w || !w_scale || !seg_end || (M > 0 && (!out || (a_rows > 0 && (!a || !a_scale)))))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned(a_scale, 4) || !aligned(w, 32) || !aligned(w_scale, 4) ||
+      !aligned(out, out_scale ? 16 : 2) || !aligned16(out_scale))
+    return MOE_ERR_UNSUPPORTED;
+  const size_t need = moe_grouped_gemm_mx_workspace_size(M, N, K, E);
+  if (!ws_ok(ws, ws_bytes, need)) return MOE_ERR_WORKSPACE;
+  const size_t N1 = act && gated_kind(act->kind) ? 2 * (size_t)N : (size_t)N;
+  const size_t Kp = mx_pad(K), Np = mx_pad(N), rows = (size_t)E * N1;
+  Span outs[] = {{out, out_scale ? (size_t)M * Np : (size_t)M * N * 2},
+                 {out_scale, (size_t)M * (Np / 32)},
+                 {ws, need}};
+  Span ins[] = {{a, (size_t)a_rows * Kp},     {a_scale, (size_t)a_rows * (Kp / 32)},
+                {w, rows * (Kp / 2)},         {w_scale, rows * (Kp / 32)},
+                {bias, bias ? rows * 2 : 0},  {seg_end, (size_t)E * 4},
+                {row_to_route, row_to_route ? (size_t)M * 4 : 0}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  if (M == 0) return MOE_OK;
+  return cuda_status(launch_gemm_mx(a, a_scale, a_rows, row_to_route, row_to_route ? top_k : 1, w,
+                                    w_scale, bias, seg_end, M, N, K, E, act, dtype == MOE_F16, out,
+                                    out_scale, static_cast<int*>(ws), stream));
+}
+
+size_t moe_workspace_size_mx(int T, int H, int F, int E, int K) {
+  if (T < 0 || H < 1 || F < 1 || E < 1 || K < 1 || (long long)T * K >= (1LL << 30)) return 0;
+  return MxForwardWs(T, H, F, E, K).total;
+}
+
+moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, const void* logits,
+                              const void* w_gate_up, const void* w_gate_up_scale,
+                              const void* w_down, const void* w_down_scale,
+                              const float* correction_bias, const int32_t* expert_ids,
+                              const void* b_gate_up, const void* b_down, int T, int H, int F,
+                              int E, moe_dtype dtype, const moe_route_params* p,
+                              const moe_act_params* act, void* out, float* topk_weights_out,
+                              int32_t* topk_ids_out, void* ws, size_t ws_bytes,
+                              cudaStream_t stream) {
+  if (!dtype_ok(dtype) || !act_ok(act)) return MOE_ERR_INVALID_ARG;
+  float dummy_w = 0.f;
+  int32_t dummy_i = 0;
+  moe_status st = check_route(logits, correction_bias, T, E, p, &dummy_w, &dummy_i, nullptr, nullptr);
+  if (st != MOE_OK) return st;
+  const int K = p->top_k;
+  const long long Ml = (long long)T * K;
+  if (p->local_expert_count != 0 || !mx_gemm_extent_ok(Ml, H, F, E) || !mx_gemm_extent_ok(Ml, F, H, E))
+    return MOE_ERR_INVALID_ARG;
+  if (dtype == MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (!w_gate_up || !w_gate_up_scale || !w_down || !w_down_scale ||
+      (T > 0 && (!hidden || !hidden_scale || !out)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(hidden) || !aligned(hidden_scale, 4) || !aligned(w_gate_up, 32) ||
+      !aligned(w_gate_up_scale, 4) || !aligned(w_down, 32) || !aligned(w_down_scale, 4) ||
+      !aligned(out, 2))
+    return MOE_ERR_UNSUPPORTED;
+  const MxForwardWs L(T, H, F, E, K);
+  if (!ws_ok(ws, ws_bytes, L.total)) return MOE_ERR_WORKSPACE;
+  const size_t M = (size_t)Ml, N1 = gated_kind(act->kind) ? 2 * (size_t)F : (size_t)F;
+  const size_t Hp = mx_pad(H), Fp = mx_pad(F);
+  Span outs[] = {{out, (size_t)T * H * 2}, {topk_weights_out, M * 4}, {topk_ids_out, M * 4},
+                 {ws, L.total}};
+  Span ins[] = {{hidden, (size_t)T * Hp},
+                {hidden_scale, (size_t)T * (Hp / 32)},
+                {logits, (size_t)T * E * rsz(p)},
+                {w_gate_up, (size_t)E * N1 * (Hp / 2)},
+                {w_gate_up_scale, (size_t)E * N1 * (Hp / 32)},
+                {w_down, (size_t)E * H * (Fp / 2)},
+                {w_down_scale, (size_t)E * H * (Fp / 32)},
+                {correction_bias, correction_bias ? (size_t)E * 4 : 0},
+                {expert_ids, expert_ids ? M * 4 : 0},
+                {b_gate_up, b_gate_up ? (size_t)E * N1 * 2 : 0},
+                {b_down, b_down ? (size_t)E * H * 2 : 0}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  if (T == 0) return MOE_OK;
+
+  char* base = static_cast<char*>(ws);
+  float* tw = topk_weights_out ? topk_weights_out : reinterpret_cast<float*>(base + L.topk_w);
+  int32_t* ti = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(base + L.topk_ids);
+  int32_t* seg_end = reinterpret_cast<int32_t*>(base + L.seg_end);
+  int32_t* r2r = reinterpret_cast<int32_t*>(base + L.row_to_route);
+  int32_t* route_to_row = reinterpret_cast<int32_t*>(base + L.route_to_row);
+  int* status = reinterpret_cast<int*>(base);
+  const bool fused_maps = route_permute_ok(E), f16 = dtype == MOE_F16;
+  StageTimer t_route(fused_maps ? "route_permute" : "route", stream);
+  cudaError_t err =
+      fused_maps ? launch_route_permute(logits, correction_bias, expert_ids, T, E, *p, tw, ti,
+                                        nullptr, nullptr, seg_end, r2r, route_to_row, ws, stream)
+                 : launch_route(logits, correction_bias, expert_ids, T, E, *p, tw, ti, nullptr,
+                                nullptr, stream);
+  if (err == cudaSuccess && !fused_maps)
+    err = launch_permute(nullptr, 1, ti, T, H, E, K, nullptr, seg_end, r2r, route_to_row, ws, stream);
+  if (err != cudaSuccess) return MOE_ERR_CUDA;
+  t_route.done();
+  StageTimer t_gu("gate_up", stream);
+  err = launch_gemm_mx(hidden, hidden_scale, T, r2r, K, w_gate_up, w_gate_up_scale, b_gate_up,
+                       seg_end, (int)M, F, H, E, act, f16, base + L.act, base + L.act_scale, status,
+                       stream);
+  if (err != cudaSuccess) return MOE_ERR_CUDA;
+  t_gu.done();
+  StageTimer t_down("down", stream);
+  err = launch_gemm_mx(base + L.act, base + L.act_scale, (int)M, nullptr, 1, w_down, w_down_scale,
+                       b_down, seg_end, (int)M, H, F, E, nullptr, f16, base + L.y, nullptr, status,
+                       stream);
+  if (err != cudaSuccess) return MOE_ERR_CUDA;
+  t_down.done();
+  StageTimer t_comb("combine", stream);
+  err = launch_combine(base + L.y, tw, route_to_row, T, K, H, dtype, 1.0f, out, stream);
+  t_comb.done();
+  return cuda_status(err);
+}
+
 size_t moe_workspace_size_host(int T, int H, int F, int E, int K, moe_dtype dtype) {
   size_t base = moe_workspace_size(T, H, F, E, K, dtype);
   if (base == 0) return 0;

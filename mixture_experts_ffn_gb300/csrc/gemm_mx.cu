@@ -1,0 +1,577 @@
+// Grouped GEMM over microscaled operands (mx_dev.cuh): rows of activations in
+// MX e4m3 times expert weights in MX e2m1, over the expert-segmented row
+// layout, with bias, activation and the output rounding (16-bit, or MX e4m3
+// for the next product) in the epilogue.
+//
+// Mathematics: p[m, n] = sum over blocks b of 2^(sa[m, b] + sw[n, b]) *
+// (codes of a, block b . codes of w, block b).  tcgen05.mma kind::mxf8f6f4
+// applies both scales inside the tensor core and accumulates in float32, so
+// neither operand is expanded in memory: weights cross HBM at 17/32 byte a
+// value.
+//
+// Layout: the expert's weight rows are the MMA's M operand (128 rows a half),
+// the tokens of a chunk of its segment the N operand (a multiple of 16), so a
+// segment pads to 16 rows.  Two halves share each token slice: gate and up
+// rows of the same 128 outputs (gated kinds), or 256 consecutive output
+// columns (plain).  TMEM lane = output column, TMEM column = token; a warp's
+// 32 lanes are one MX block of a token's output, so its scale is one
+// redux.sync.
+//
+// Roles (320 threads, one CTA per SM, persistent)
+//   warp 0 lane 0 : TMA producer of the weight codes.  The map's type expands
+//                   each 16 packed values (8 bytes) into a 16-byte chunk of
+//                   shared memory, the form the MMA reads 4-bit values in.
+//   warp 1        : TMEM; lane 0 copies each stage's scales from shared
+//                   memory into TMEM (tcgen05.cp) and issues the MMAs
+//   warps 2..5    : epilogue
+//   warps 6..9    : cp.async loaders of the token rows (gathered through
+//                   row_to_route when given) and of both operands' scales
+// Stage: 128 columns of K, i.e. four K32 MMA steps; the 4 scale bytes of a
+// row and stage are one 32-bit TMEM cell, step j using byte j of it.
+// Every wait is bounded (tc_ptx.cuh).
+#include <cuda.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.cuh"
+#include "gemm_epilogue.cuh"
+#include "mx_dev.cuh"
+#include "tc_ptx.cuh"
+#include "tmap.h"
+
+namespace moe {
+namespace {
+
+using namespace tc;
+
+constexpr int BK = 128;                    // columns of K per stage
+constexpr int W_BYTES = 128 * BK;          // one half's weights, expanded: 16 KB
+constexpr int W_TX = W_BYTES / 2;          // bytes its copy counts: the packed ones (the gaps of
+                                           // the expanded form are not written)
+constexpr int SF_ATOM = 512;               // scales of 128 rows and one stage
+constexpr int NUM_THREADS = 320;
+constexpr int kEpiWarp0 = 2, kLoadWarp0 = 6;
+constexpr size_t kSmemLimit = 227 * 1024;
+
+// Token columns of a tile and what follows from them: ring depth and TMEM.
+template <int NMAX_>
+struct Cfg {
+  static constexpr int NMAX = NMAX_;
+  static constexpr int kAccs = NMAX <= 112 ? 2 : 1;  // accumulators (512 TMEM columns in all)
+  static constexpr int B_BYTES = NMAX * BK;
+  static constexpr int SFB_ATOMS = (NMAX + 127) / 128;
+  static constexpr int SF_BYTES = (2 + SFB_ATOMS) * SF_ATOM;
+  static constexpr int STAGE_BYTES = 2 * W_BYTES + B_BYTES;
+  static constexpr int kFixed = 8 * 1024;  // barriers, tile prefix, alignment
+  static constexpr int STAGES = (int)((kSmemLimit - kFixed) / (STAGE_BYTES + SF_BYTES));
+  static constexpr int SF_COLS = 4 * (2 + SFB_ATOMS);  // TMEM columns of a stage's scales
+  static constexpr int ACC_COLS = 2 * NMAX;
+  static constexpr int kSf0 = kAccs * ACC_COLS;
+  static_assert(kSf0 + STAGES * SF_COLS <= 512, "TMEM columns");
+  static_assert(NMAX % 16 == 0 && NMAX <= 256, "N");
+};
+
+template <int STAGES>
+struct MxShared {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int prefix[kMaxExperts + 1];
+  int scan_tmp[33];
+};
+
+struct MxArgs {
+  const uint8_t* a;        // [a_rows, Kp] e4m3 codes
+  const uint8_t* a_scale;  // [a_rows, Kp / 32]
+  const uint8_t* w_scale;  // [E, N1, Kp / 32]
+  const void* bias;        // [E, N1] or null
+  const int32_t* seg_end;
+  const int32_t* grows;    // row_to_route, or null (row m is row m of a)
+  void* out;               // 16-bit [M, Nout], or e4m3 codes [M, Np]
+  uint8_t* out_scale;      // [M, Np / 32]
+  int* status;
+  int M, Nout, N1, Kp, E, a_rows, gdiv;
+  int row_step, half_step;  // weight row of output f, half h: f * row_step + h * half_step
+  float limit, alpha, beta;
+};
+
+// Shared-memory descriptor of a 32-row x 16-byte scale matrix: no swizzle,
+// 8-row core matrices 128 bytes apart.
+__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(128 >> 4) << 32;  // stride byte offset
+  d |= (uint64_t)1 << 46;           // descriptor version
+  return d;
+}
+// 128 rows' scales (32 rows x 16 bytes) to four TMEM columns, repeated in all
+// four lane quarters
+__device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                       uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], "
+      "[%6], p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+__device__ __forceinline__ void mx_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+// Instruction descriptor, kind::mxf8f6f4: A e2m1 (format 5 at bit 7), B e4m3
+// (format 0 at bit 10), both K-major, N / 8 at bit 17, e8m0 scales (bit 23),
+// M = 128 (bit 27); the scale byte of K step j at bits 4 (B) and 29 (A).
+__device__ __forceinline__ uint32_t idesc_mx(int N) {
+  return (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok, uint64_t pol) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+               "l"(src), "r"(ok ? 16 : 0), "l"(pol)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 4 : 0)
+               : "memory");
+}
+// byte offset of row r's four scales in its 128-row scale matrix
+__device__ __forceinline__ uint32_t sf_off(int r) { return (uint32_t)((r & 31) * 16 + (r >> 5) * 4); }
+
+struct MxTile {
+  int e, ft, m0, nv, N;  // expert, output tile, first row, rows, MMA columns
+};
+template <int NMAX>
+__device__ __forceinline__ MxTile mx_decode(int t, const int* prefix, const int32_t* seg_end, int E,
+                                            int M) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {  // last e with prefix[e] <= t (skips empty experts)
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  int s, u;
+  seg_bounds(seg_end, lo, M, 0, s, u);
+  const int n = u - s;
+  const int ce = (n + NMAX - 1) / NMAX;  // chunks of equal size, rounded up to 16
+  const int local = t - prefix[lo];
+  MxTile r;
+  r.e = lo;
+  r.ft = local / ce;
+  const int per = (((n + ce - 1) / ce) + 15) & ~15;
+  const int start = min((local % ce) * per, n);
+  r.m0 = s + start;
+  r.nv = min(per, n - start);  // 0 for a chunk that rounding left empty
+  r.N = max(16, (r.nv + 15) & ~15);
+  return r;
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_one(float x) {
+  if constexpr (ACT == MOE_ACT_RELU) return fmaxf(x, 0.0f);
+  else if constexpr (ACT == MOE_ACT_GELU) return gelu_f(x);
+  else if constexpr (ACT == MOE_ACT_SILU) return x * fast_sigmoid(x);
+  else return x;
+}
+
+// The calling warp's 32 output columns f0 + lane for 16 tokens m0 .. (nval of
+// them): 16-bit rows, or MX e4m3 codes with one scale per token.
+template <bool MXOUT, bool F16>
+__device__ __forceinline__ void emit16(const float (&v)[16], const MxArgs& p, int m0, int nval,
+                                       int f0, int lane) {
+  const int f = f0 + lane;
+  if constexpr (MXOUT) {
+    const int Np = mx::padded(p.Nout);
+    uint8_t* o = static_cast<uint8_t*>(p.out) + (size_t)m0 * Np + f;
+    uint8_t* so = p.out_scale + (size_t)m0 * (Np / 32) + (f0 >> 5);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i >= nval) break;
+      const uint32_t amax = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[i]));
+      const uint32_t byte = mx::scale_byte<false>(amax);
+      o[(size_t)i * Np] = (uint8_t)mx::e4m3x2(mx::scaled(v[i], mx::inv_scale(byte)), 0.0f);
+      if (lane == 0) so[(size_t)i * (Np / 32)] = (uint8_t)byte;
+    }
+  } else if (f < p.Nout) {
+    uint16_t* o = static_cast<uint16_t*>(p.out) + (size_t)m0 * p.Nout + f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < nval) o[(size_t)i * p.Nout] = (uint16_t)pack2<F16>(v[i], 0.0f);
+  }
+}
+
+template <int NMAX, bool GATED, int ACT, bool MXOUT, bool F16>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    gemm_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ MxArgs p) {
+  using C = Cfg<NMAX>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sf = smem + (size_t)STAGES * C::STAGE_BYTES;
+  auto* sh = reinterpret_cast<MxShared<STAGES>*>(sf + (size_t)STAGES * C::SF_BYTES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sh->abort;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&sh->full[s], 1 + 128);  // the producer's expect-tx and every loader thread
+      mbar_init(&sh->empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&sh->tfull[a], 1);
+      mbar_init(&sh->tempty[a], 128);
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     su32(&sh->tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  constexpr int FT = GATED ? 128 : 256;  // output columns of a tile
+  const int n_ftiles = (p.Nout + FT - 1) / FT;
+  const int nkb = p.Kp / BK;
+  pdl_wait();
+  const int total = build_tile_prefix(p.seg_end, p.E, p.M, NMAX, n_ftiles, sh->prefix, sh->scan_tmp);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------ TMA producer (weights)
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued[STAGES];
+      for (int s = 0; s < STAGES; ++s) issued[s] = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+        if (t.nv == 0) continue;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+          uint8_t* dst = smem + (size_t)stage * C::STAGE_BYTES;
+          mbar_expect_tx(&sh->full[stage], 2 * W_TX);
+          // rows past the operand read as zeros and count in full
+          if constexpr (GATED) {
+            tma_4d(dst, &tm_w, &sh->full[stage], kb * BK, t.ft * 128, 0, t.e);
+            tma_4d(dst + W_BYTES, &tm_w, &sh->full[stage], kb * BK, t.ft * 128, 1, t.e);
+          } else {
+            tma_4d(dst, &tm_w, &sh->full[stage], kb * BK, t.ft * 256, 0, t.e);
+            tma_4d(dst + W_BYTES, &tm_w, &sh->full[stage], kb * BK, t.ft * 256 + 128, 0, t.e);
+          }
+          ++issued[stage];
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok) {  // let every copy already in flight land before the block exits
+        for (int s = 0; s < STAGES; ++s)
+          if (issued[s]) drain_wait(&sh->full[s], (issued[s] - 1u) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------ MMA issuer
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, aphase = 0;
+      bool ok = true, any = false;
+      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+        const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+        if (t.nv == 0) continue;
+        if (!wait_fast(&sh->tempty[acc], aphase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
+        const uint32_t idesc = idesc_mx(t.N);
+        const bool two = t.N > 128;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!wait_fast(&sh->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+          // the loaders wrote through the generic proxy; tcgen05 reads through
+          // the async proxy
+          fence_proxy_async_smem();
+          tc_fence_after();
+          // the stage's scales go to TMEM columns of their own, free since the
+          // stage's last MMAs completed; copies and MMAs of one thread run in
+          // issue order
+          const uint32_t sfa = tmem + (uint32_t)(C::kSf0 + stage * C::SF_COLS), sfb = sfa + 8;
+          const uint64_t sd = sf_desc(su32(sf + (size_t)stage * C::SF_BYTES));
+          sf_copy(sfa, sd);
+          sf_copy(sfa + 4, sd + (SF_ATOM >> 4));
+          sf_copy(sfb, sd + 2 * (SF_ATOM >> 4));
+          if (C::SFB_ATOMS == 2 && two) sf_copy(sfb + 4, sd + 3 * (SF_ATOM >> 4));
+          const uint64_t ad = sw128_desc(su32(smem + (size_t)stage * C::STAGE_BYTES));
+          const uint64_t bd = ad + (2 * W_BYTES >> 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t id = idesc | ((uint32_t)j << 4) | ((uint32_t)j << 29);
+            const uint32_t go = (kb | j) != 0;
+            mma_mx(d, ad + 2 * j, bd + 2 * j, id, sfa, sfb, go);
+            mma_mx(d + NMAX, ad + (W_BYTES >> 4) + 2 * j, bd + 2 * j, id, sfa + 4, sfb, go);
+          }
+          mx_commit(su32(&sh->empty[stage]));
+          any = true;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        mx_commit(su32(&sh->tfull[acc]));
+        if (++acc == C::kAccs) { acc = 0; aphase ^= 1u; }
+      }
+      if (!ok && any) {  // every MMA issued so far done before TMEM is freed
+        mx_commit(su32(&sh->drain));
+        drain_wait(&sh->drain, 0);
+      }
+    }
+  } else if (warp >= kLoadWarp0) {
+    // ------------------------------------------------ loaders (tokens, scales)
+    // Token rows: thread lt owns 16-byte chunk lt % 8 of rows lt / 8 + 16 i, so
+    // eight lanes read one 128-byte row piece; chunk ch of row r lands at chunk
+    // ch ^ (r % 8), the 128-byte swizzle.  Scales: one 4-byte piece per row.
+    const int lt = threadIdx.x - kLoadWarp0 * 32;
+    const int ch = lt & 7, r0 = lt >> 3;
+    const uint32_t dst0 = (uint32_t)(2 * W_BYTES + r0 * 128 + ((ch ^ (r0 & 7)) << 4));
+    constexpr int RI = NMAX / 16, SI = C::SFB_ATOMS;
+    // the token rows are read again by every output tile of their expert:
+    // kept in L2 ahead of the weight stream
+    uint64_t keep;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    const int sp = p.Kp / 32;  // scale bytes of a row
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    // row of `a` for tile row r, or -1 (padding, or a map entry out of range)
+    auto source = [&](const MxTile& t, int r) {
+      if (r >= t.nv) return -1;
+      int m = t.m0 + r;
+      if (p.grows) {
+        m = p.grows[m];
+        m = m < 0 ? -1 : m / p.gdiv;
+      }
+      return m < p.a_rows ? m : -1;
+    };
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+      if (t.nv == 0) continue;
+      int src[RI], ssrc[SI];
+#pragma unroll
+      for (int i = 0; i < RI; ++i) src[i] = 16 * i < t.N ? source(t, r0 + 16 * i) : -1;
+#pragma unroll
+      for (int i = 0; i < SI; ++i) ssrc[i] = source(t, lt + 128 * i);
+      // weight rows of the two halves
+      const uint8_t* ws[2];
+      bool wok[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int f = GATED ? t.ft * 128 + lt : t.ft * 256 + h * 128 + lt;
+        wok[h] = f < p.Nout;
+        const int row = GATED ? f * p.row_step + h * p.half_step : f;
+        ws[h] = p.w_scale + ((size_t)t.e * p.N1 + (wok[h] ? row : 0)) * sp;
+      }
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+        const uint32_t sfs = su32(sf + (size_t)stage * C::SF_BYTES);
+        cp_async4(sfs + sf_off(lt), ws[0] + kb * 4, wok[0]);
+        cp_async4(sfs + SF_ATOM + sf_off(lt), ws[1] + kb * 4, wok[1]);
+#pragma unroll
+        for (int i = 0; i < SI; ++i)
+          if (lt + 128 * i < t.N)
+            cp_async4(sfs + (2 + i) * SF_ATOM + sf_off(lt),
+                      p.a_scale + (size_t)max(ssrc[i], 0) * sp + kb * 4, ssrc[i] >= 0);
+        const uint32_t dst = su32(smem + (size_t)stage * C::STAGE_BYTES) + dst0;
+        const uint8_t* a = p.a + kb * BK + ch * 16;
+#pragma unroll
+        for (int i = 0; i < RI; ++i)
+          if (16 * i < t.N)
+            cp_async16(dst + i * 16 * 128, a + (size_t)max(src[i], 0) * p.Kp, src[i] >= 0, keep);
+        // arrives on the stage's full barrier once this thread's copies land
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         su32(&sh->full[stage]))
+                     : "memory");
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight at exit
+  } else {
+    // ------------------------------------------------ epilogue (warps 2..5)
+    const int quad = warp & 3;  // TMEM lanes 32 * quad ..
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    int acc = 0;
+    uint32_t aphase = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+      if (t.nv == 0) continue;
+      // the lane's biases, loaded before the accumulator is ready
+      float b[2] = {0.0f, 0.0f};
+      const int f0 = t.ft * FT + quad * 32, f = f0 + lane;
+      if (p.bias) {
+        const __nv_bfloat16* be = static_cast<const __nv_bfloat16*>(p.bias) + (size_t)t.e * p.N1;
+        if constexpr (GATED) {
+          if (f < p.Nout) {
+            b[0] = ld16<F16>(be + f * p.row_step);
+            b[1] = ld16<F16>(be + f * p.row_step + p.half_step);
+          }
+        } else {
+          if (f < p.Nout) b[0] = ld16<F16>(be + f);
+          if (f + 128 < p.Nout) b[1] = ld16<F16>(be + f + 128);
+        }
+      }
+      if (!wait_fast(&sh->tfull[acc], aphase, abort_flag, p.status)) break;
+      tc_fence_after();
+      const uint32_t base = lanes + (uint32_t)(acc * C::ACC_COLS);
+#pragma unroll 1
+      for (int c = 0; c < t.nv; c += 16) {
+        uint32_t r[2][16];
+        tmem_ld16(base + c, r[0]);
+        tmem_ld16(base + NMAX + c, r[1]);
+        tmem_wait_ld();
+        const int nval = min(16, t.nv - c);
+        float v[16];
+        if constexpr (GATED) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            v[i] = gated<ACT>(__uint_as_float(r[0][i]) + b[0], __uint_as_float(r[1][i]) + b[1],
+                              p.limit, p.alpha, p.beta);
+          emit16<MXOUT, F16>(v, p, t.m0 + c, nval, f0, lane);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = act_one<ACT>(__uint_as_float(r[h][i]) + b[h]);
+            // the second half may lie past the padded output
+            if (f0 + h * 128 < mx::padded(p.Nout))
+              emit16<MXOUT, F16>(v, p, t.m0 + c, nval, f0 + h * 128, lane);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sh->tempty[acc]);
+      if (++acc == C::kAccs) { acc = 0; aphase ^= 1u; }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+template <int NMAX, bool GATED, int ACT, bool MXOUT, bool F16>
+cudaError_t go(const CUtensorMap& tm, const MxArgs& p, cudaStream_t s) {
+  using C = Cfg<NMAX>;
+  constexpr size_t smem = (size_t)C::STAGES * (C::STAGE_BYTES + C::SF_BYTES) +
+                          sizeof(MxShared<C::STAGES>) + 1024;
+  static_assert(smem <= kSmemLimit, "shared memory");
+  auto kern = gemm_mx_kernel<NMAX, GATED, ACT, MXOUT, F16>;
+  cudaError_t e = set_smem_limit((const void*)kern, (int)smem);
+  if (e != cudaSuccess) return e;
+  constexpr int FT = GATED ? 128 : 256;
+  const long long chunks = (long long)p.M / NMAX + std::min(p.M, p.E);  // at most this many
+  const long long tiles = chunks * ((p.Nout + FT - 1) / FT);
+  const int grid = (int)std::max<long long>(1, std::min<long long>(tiles, num_sms()));
+  e = launch_pdl(kern, dim3(grid), dim3(NUM_THREADS), smem, s, tm, p);
+  count_launch();
+  return e;
+}
+
+template <int NMAX, bool GATED, int ACT>
+cudaError_t go_out(const CUtensorMap& tm, const MxArgs& p, bool mx_out, bool f16, cudaStream_t s) {
+  if (mx_out)
+    return f16 ? go<NMAX, GATED, ACT, true, true>(tm, p, s)
+               : go<NMAX, GATED, ACT, true, false>(tm, p, s);
+  return f16 ? go<NMAX, GATED, ACT, false, true>(tm, p, s)
+             : go<NMAX, GATED, ACT, false, false>(tm, p, s);
+}
+
+template <int NMAX>
+cudaError_t go_act(const CUtensorMap& tm, const MxArgs& p, int kind, bool mx_out, bool f16,
+                   cudaStream_t s) {
+  switch (kind) {
+    case MOE_ACT_SILU_AND_MUL: return go_out<NMAX, true, MOE_ACT_SILU_AND_MUL>(tm, p, mx_out, f16, s);
+    case MOE_ACT_SWIGLU: return go_out<NMAX, true, MOE_ACT_SWIGLU>(tm, p, mx_out, f16, s);
+    case MOE_ACT_GELU_AND_MUL: return go_out<NMAX, true, MOE_ACT_GELU_AND_MUL>(tm, p, mx_out, f16, s);
+    case MOE_ACT_RELU: return go_out<NMAX, false, MOE_ACT_RELU>(tm, p, mx_out, f16, s);
+    case MOE_ACT_GELU: return go_out<NMAX, false, MOE_ACT_GELU>(tm, p, mx_out, f16, s);
+    case MOE_ACT_SILU: return go_out<NMAX, false, MOE_ACT_SILU>(tm, p, mx_out, f16, s);
+    default: return go_out<NMAX, false, MOE_ACT_IDENTITY>(tm, p, mx_out, f16, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const int32_t* gather_rows,
+                           int gather_div, const void* w, const void* w_scale, const void* bias,
+                           const int32_t* seg_end, int M, int Nout, int K, int E,
+                           const moe_act_params* act, bool f16, void* out, void* out_scale,
+                           int* status, cudaStream_t s) {
+  if (M == 0) return cudaSuccess;
+  const bool gate = act && act_is_gated(act->kind);
+  const bool inter = gate && act->kind == MOE_ACT_SWIGLU && act->swiglu_fusion == 1;
+  MxArgs p{};
+  p.a = static_cast<const uint8_t*>(a);
+  p.a_scale = static_cast<const uint8_t*>(a_scale);
+  p.w_scale = static_cast<const uint8_t*>(w_scale);
+  p.bias = bias;
+  p.seg_end = seg_end;
+  p.grows = gather_rows;
+  p.gdiv = gather_div;
+  p.out = out;
+  p.out_scale = static_cast<uint8_t*>(out_scale);
+  p.status = status;
+  p.M = M;
+  p.Nout = Nout;
+  p.N1 = gate ? 2 * Nout : Nout;
+  p.Kp = mx::padded(K);
+  p.E = E;
+  p.a_rows = a_rows;
+  p.row_step = inter ? 2 : 1;
+  p.half_step = gate ? (inter ? 1 : Nout) : 0;
+  if (act) {
+    p.limit = act->limit;
+    p.alpha = act->alpha;
+    p.beta = act->beta;
+  }
+  // weights [E][N1][Kp / 2 bytes] as [E][halves][Nout][K]
+  CUtensorMap tm;
+  const cuuint64_t row = (cuuint64_t)p.Kp / 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.Kp, (cuuint64_t)Nout, gate ? 2u : 1u, (cuuint64_t)E};
+  const cuuint64_t str[3] = {row * p.row_step, gate ? row * p.half_step : row * Nout, row * p.N1};
+  const cuuint32_t box[4] = {BK, 128, 1, 1};
+  if (!tmap::encode_u4_expanded(&tm, w, 4, dims, str, box)) return cudaErrorInvalidValue;
+  const int kind = act ? act->kind : MOE_ACT_IDENTITY;
+  const long long avg = ((long long)M + std::min(M, E) - 1) / std::min(M, E);
+  if (avg <= 8) return go_act<16>(tm, p, kind, out_scale != nullptr, f16, s);
+  if (avg <= 80) return go_act<112>(tm, p, kind, out_scale != nullptr, f16, s);
+  return go_act<224>(tm, p, kind, out_scale != nullptr, f16, s);
+}
+
+}  // namespace moe

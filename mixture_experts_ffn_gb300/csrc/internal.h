@@ -54,6 +54,26 @@ struct ForwardWs {
   }
 };
 
+// Workspace of the forward over microscaled operands: the permute scratch,
+// routing, index maps, the activation's codes and scales, and the down
+// product's 16-bit rows.
+struct MxForwardWs {
+  size_t topk_w, topk_ids, seg_end, row_to_route, route_to_row, act, act_scale, y, total;
+  MxForwardWs(int T, int H, int F, int E, int K) {
+    const size_t M = (size_t)T * K, Fp = ((size_t)F + 127) / 128 * 128;
+    PermuteWs p((int)M, E);
+    topk_w = p.total;
+    topk_ids = align256(topk_w + M * 4);
+    seg_end = align256(topk_ids + M * 4);
+    row_to_route = align256(seg_end + (size_t)E * 4);
+    route_to_row = align256(row_to_route + M * 4);
+    act = align256(route_to_row + M * 4);
+    act_scale = align256(act + M * Fp);
+    y = align256(act_scale + M * (Fp / 32));
+    total = align256(y + M * (size_t)H * 2);
+  }
+};
+
 void count_launch(int n = 1);
 int num_sms();
 // CTAs of `kernel` that one SM of the current device holds at once with
@@ -184,6 +204,27 @@ cudaError_t launch_gemm_sw(const void* a, const void* w, const void* bias, const
 cudaError_t launch_gemm_fp8(const void* a, const float* a_scale, const void* b,
                             const float* b_scale, const int32_t* counts, int E, int max_m, int N,
                             int K, void* out, int* status, cudaStream_t s);
+
+// Microscaled formats (mx_dev.cuh).  x: `rows` rows of K elements, `stride`
+// elements apart; codes / scales as moe_mx_quantize describes.
+cudaError_t launch_mx_quantize(const void* x, int64_t rows, int K, int64_t stride, moe_dtype dt,
+                               int fmt, void* codes, void* scales, cudaStream_t s);
+cudaError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t rows, int K,
+                                 int fmt, moe_dtype dt, void* out, cudaStream_t s);
+
+// residual addition + RMS norm + 8-bit codes in one launch (rms_norm.cu)
+cudaError_t launch_rms_norm(const void* x, const void* residual, const void* weight, int T, int H,
+                            moe_dtype dt, float eps, int quant, void* residual_out, void* out,
+                            void* codes, void* scales, cudaStream_t s);
+
+// Grouped GEMM of MX e4m3 rows by MX e2m1 weights (gemm_mx.cu).  With
+// gather_rows, row r of the operand is row gather_rows[r] / gather_div of `a`
+// (a_rows rows); out is 16-bit (float16 with f16), or MX e4m3 with out_scale.
+cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows,
+                           const int32_t* gather_rows, int gather_div, const void* w,
+                           const void* w_scale, const void* bias, const int32_t* seg_end, int M,
+                           int Nout, int K, int E, const moe_act_params* act, bool f16, void* out,
+                           void* out_scale, int* status, cudaStream_t s);
 
 // indexed per-route decode path (bf16, silu_and_mul, no bias)
 cudaError_t launch_indexed(const void* hidden, const void* w1, const void* w2, const float* w,

@@ -1,0 +1,170 @@
+// Residual addition, root-mean-square norm and its 8-bit forms in one pass:
+//   h = round(x + r) (or x), y = h * rsqrt(mean(h^2) + eps) * w
+// with h and y written in the operand type and y also as e4m3 codes: MX (an
+// e8m0 scale per 32 columns) or one float32 scale per 128 columns (what the
+// block-scaled FP8 grouped GEMM reads).
+//
+// The mean is taken over the ROUNDED h, so the result is the norm of the
+// residual stream that is stored, and equal to adding first and normalising
+// later.  The codes come from the float32 y, not from its rounded copy: one
+// rounding instead of two.  Squares are summed in float32, eight columns a
+// thread at a time, then across the row's threads in a fixed order.
+//
+// Bound by HBM: x and r in, h, y and the codes out, each once; a row stays in
+// registers between the sum and the scaling.
+#include <algorithm>
+#include <type_traits>
+
+#include "mx_dev.cuh"
+
+namespace moe {
+namespace {
+
+enum : int { kQuantNone = 0, kQuantMx = 1, kQuantB128 = 2 };
+
+struct NormArgs {
+  const void *x, *r, *w;
+  void *h, *y;
+  uint8_t* codes;
+  void* scales;
+  int T, H, Hp;
+  float eps;
+};
+
+// Sum over the `warps` warps of a row group (every thread gets it).
+__device__ __forceinline__ float group_sum(float v, float* red, int warps, int warp, int lane) {
+  v = warp_sum(v);
+  if (warps == 1) return v;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  float s = lane < warps ? red[lane] : 0.0f;
+  return warp_sum(s);
+}
+
+// A row is shared by `blockDim.x` threads (one CTA a row), or by one warp
+// when WARP_ROW (blockDim.x / 32 rows a CTA); each thread owns ITEMS groups
+// of eight columns, consecutive threads owning consecutive groups.
+template <typename T, int QUANT, int ITEMS, bool VEC, bool WARP_ROW>
+__global__ void __launch_bounds__(WARP_ROW ? 256 : 1024)
+    rms_norm_kernel(const __grid_constant__ NormArgs p) {
+  __shared__ float red[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nthr = WARP_ROW ? 32 : (int)blockDim.x;
+  const int t0 = WARP_ROW ? lane : (int)threadIdx.x;
+  const int row = WARP_ROW ? (int)(blockIdx.x * (blockDim.x >> 5)) + warp : (int)blockIdx.x;
+  pdl_wait();
+  if (WARP_ROW && row >= p.T) return;
+  const int H = p.H;
+  const T* x = static_cast<const T*>(p.x) + (size_t)row * H;
+  const T* r = p.r ? static_cast<const T*>(p.r) + (size_t)row * H : nullptr;
+  float v[ITEMS][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) mx::load8<T, VEC>(x, (t0 + i * nthr) * 8, H, v[i]);
+  if (r) {
+    float a[ITEMS][8];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) mx::load8<T, VEC>(r, (t0 + i * nthr) * 8, H, a[i]);
+    T* h = static_cast<T*>(p.h) + (size_t)row * H;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = Elem<T>::to_f(Elem<T>::from_f(v[i][j] + a[i][j]));
+      mx::store8<T, VEC>(h, (t0 + i * nthr) * 8, H, v[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+  ss = group_sum(ss, red, nthr >> 5, warp, lane);
+  const float rstd = rsqrtf(ss / (float)H + p.eps);
+  T* y = p.y ? static_cast<T*>(p.y) + (size_t)row * H : nullptr;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int item = t0 + i * nthr, c0 = item * 8;
+    float w[8];
+    mx::load8<T, VEC>(static_cast<const T*>(p.w), c0, H, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
+    if (y) mx::store8<T, VEC>(y, c0, H, v[i]);
+    if constexpr (QUANT != kQuantNone) {
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, mx::abs_bits(v[i][j]));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      if constexpr (QUANT == kQuantMx) {
+        const uint32_t byte = mx::scale_byte<false>(amax);
+        const float inv = mx::inv_scale(byte);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = mx::scaled(v[i][j], inv);
+        if (c0 < p.Hp && (lane & 3) == 0)
+          static_cast<uint8_t*>(p.scales)[(size_t)row * (p.Hp / 32) + (item >> 2)] = (uint8_t)byte;
+      } else {
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+        // a block with an infinity or a NaN: NaN scale, zero codes
+        const bool bad = amax >= mx::kInfBits;
+        const float s = fmaxf(__uint_as_float(amax) / 448.0f, 1.17549435e-38f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = bad ? 0.0f : v[i][j] / s;
+        if (c0 < p.Hp && (lane & 15) == 0)
+          static_cast<float*>(p.scales)[(size_t)row * (p.Hp / 128) + (item >> 4)] =
+              bad ? __uint_as_float(0x7fc00000u) : s;
+      }
+      if (c0 < p.Hp)
+        reinterpret_cast<uint2*>(p.codes + (size_t)row * p.Hp)[item] = mx::e4m3x8(v[i]);
+    }
+  }
+}
+
+template <typename T, int QUANT, int ITEMS, bool VEC, bool WARP_ROW>
+cudaError_t go(const NormArgs& p, int threads, cudaStream_t s) {
+  const int grid = WARP_ROW ? (p.T + threads / 32 - 1) / (threads / 32) : p.T;
+  cudaError_t e = launch_pdl(rms_norm_kernel<T, QUANT, ITEMS, VEC, WARP_ROW>, dim3(grid),
+                             dim3(threads), 0, s, p);
+  count_launch();
+  return e;
+}
+
+// Threads of a row: short rows (up to 1024 columns) take a warp each, eight
+// to a CTA.  Longer ones take a CTA each: with enough rows to fill the GPU,
+// four groups of eight columns a thread keep more bytes in flight per thread;
+// with fewer rows than SMs, one group a thread shortens the one row's path.
+template <typename T, int QUANT, bool VEC>
+cudaError_t pick(const NormArgs& p, cudaStream_t s) {
+  const int items = p.Hp / 8;
+  if (items <= 128 && p.T >= 2 * num_sms()) return go<T, QUANT, 4, VEC, true>(p, 256, s);
+  const int one = (items + 31) & ~31;
+  if (one <= 1024 && p.T < num_sms()) return go<T, QUANT, 1, VEC, false>(p, one, s);
+  const int four = ((items + 3) / 4 + 31) & ~31;
+  if (four <= 1024) return go<T, QUANT, 4, VEC, false>(p, four, s);
+  return go<T, QUANT, 8, VEC, false>(p, ((items + 7) / 8 + 31) & ~31, s);
+}
+template <typename T>
+cudaError_t pick_q(const NormArgs& p, int quant, bool vec, cudaStream_t s) {
+  if (quant == MOE_QUANT_MX_E4M3)
+    return vec ? pick<T, kQuantMx, true>(p, s) : pick<T, kQuantMx, false>(p, s);
+  if (quant == MOE_QUANT_E4M3_BLOCK128)
+    return vec ? pick<T, kQuantB128, true>(p, s) : pick<T, kQuantB128, false>(p, s);
+  return vec ? pick<T, kQuantNone, true>(p, s) : pick<T, kQuantNone, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rms_norm(const void* x, const void* residual, const void* weight, int T, int H,
+                            moe_dtype dt, float eps, int quant, void* residual_out, void* out,
+                            void* codes, void* scales, cudaStream_t s) {
+  NormArgs p{x, residual, weight, residual_out, out, static_cast<uint8_t*>(codes), scales, T, H,
+             mx::padded(H), eps};
+  const uintptr_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) |
+                        reinterpret_cast<uintptr_t>(weight) |
+                        reinterpret_cast<uintptr_t>(residual_out) | reinterpret_cast<uintptr_t>(out);
+  const bool vec = H % 8 == 0 && (all & 15) == 0;
+  if (dt == MOE_F32) return pick_q<float>(p, quant, vec, s);
+  if (dt == MOE_F16) return pick_q<__half>(p, quant, vec, s);
+  return pick_q<__nv_bfloat16>(p, quant, vec, s);
+}
+
+}  // namespace moe

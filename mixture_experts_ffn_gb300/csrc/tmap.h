@@ -58,5 +58,21 @@ inline bool encode_u8(CUtensorMap* m, const void* ptr, int rank, const cuuint64_
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// rank-D map of packed 4-bit elements (two to a byte in memory) that a copy
+// expands to the shared-memory form tcgen05.mma reads 4-bit operands in: each
+// 16 elements (8 bytes) fill the low half of a 16-byte chunk; 128-byte
+// swizzle, zero fill outside.  dims, box and coordinates count elements; the
+// innermost extent and coordinates are multiples of 128, the address and the
+// strides of 32 bytes.
+inline bool encode_u4_expanded(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims,
+                               const cuuint64_t* strides, const cuuint32_t* box) {
+  EncodeFn fn = get_encode();
+  if (!fn) return false;
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, (cuuint32_t)rank, const_cast<void*>(ptr),
+            dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace tmap
 }  // namespace moe

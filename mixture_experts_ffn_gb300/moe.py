@@ -26,6 +26,9 @@ MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_SILU = 4, 5, 6
 MOE_STATUS_BYTES = 256
 MOE_LAYOUT_PSUM, MOE_LAYOUT_PER_ROW, MOE_LAYOUT_MASKED = 0, 1, 2
 
+MOE_MX_E4M3, MOE_MX_E2M1 = 0, 1
+MOE_QUANT_NONE, MOE_QUANT_MX_E4M3, MOE_QUANT_E4M3_BLOCK128 = 0, 1, 2
+
 # C entry points and their argument types (mirrors include/moe.h)
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, \
     ctypes.c_size_t
@@ -73,6 +76,15 @@ _SIGNATURES = {
     "moe_ffn_forward_local": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                               _vp, _vp, _vp, _sz, _vp],
     "moe_grouped_gemm_fp8_masked": [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp],
+    "moe_mx_quantize": [_vp, _i64, _i, _i64, _i, _i, _vp, _vp, _vp],
+    "moe_mx_dequantize": [_vp, _vp, _i64, _i, _i, _i, _vp, _vp],
+    "moe_add_rms_norm": [_vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _vp, _vp, _vp, _vp],
+    "moe_grouped_gemm_mx": [_vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
+                            _vp, _vp, _vp, _sz, _vp],
+    "moe_grouped_gemm_mx_workspace_size": [_i, _i, _i, _i],
+    "moe_ffn_forward_mx": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
+                           _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "moe_workspace_size_mx": [_i, _i, _i, _i, _i],
     "moe_shared_expert_workspace_size": [_i, _i, _i, _i],
     "moe_ffn_forward_shared": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp,
                                _vp, _vp, _vp, _vp, _sz, _vp],
@@ -91,7 +103,8 @@ _SIGNATURES = {
 _RESTYPES = {"moe_workspace_size": _sz, "moe_permute_workspace_size": _sz,
              "moe_workspace_size_host": _sz, "moe_shared_expert_workspace_size": _sz,
              "moe_workspace_size_shared": _sz, "moe_permute_align_workspace_size": _sz,
-             "moe_grouped_gemm_workspace_size": _sz,
+             "moe_grouped_gemm_workspace_size": _sz, "moe_workspace_size_mx": _sz,
+             "moe_grouped_gemm_mx_workspace_size": _sz,
              "moe_status_string": ctypes.c_char_p, "moe_launch_count": ctypes.c_uint64}
 
 _lib = None
@@ -505,6 +518,185 @@ def moe_grouped_gemm_fp8_masked(a, a_scale, b, b_scale, layout_metadata, out=Non
            lib.moe_grouped_gemm_fp8_masked(_p(a), _p(a_scale), _p(b), _p(b_scale),
                                            _p(layout_metadata), E, max_m, N, K, _p(out), _p(ws),
                                            ws.numel(), _stream()))
+    return out
+
+
+def moe_mx_columns(K: int) -> int:
+    """Columns of an MX row of K values: K rounded up to a multiple of 128."""
+    return (K + 127) // 128 * 128
+
+
+def moe_mx_quantize(x, format: int = MOE_MX_E4M3, codes=None, scales=None):
+    """Rows of x [..., K] as microscaled floats: (codes, scales), codes [..., Kp]
+    float8_e4m3fn or [..., Kp / 2] uint8 (MOE_MX_E2M1, two to a byte), scales
+    [..., Kp / 32] float8_e8m0fnu, Kp = moe_mx_columns(K).  A 2-D x may have any
+    row stride >= K; other shapes are contiguous."""
+    lib = load_library()
+    if not x.is_cuda:
+        raise ValueError("libmoe takes CUDA tensors only")
+    K = x.shape[-1]
+    if x.dim() == 2 and x.shape[0] > 1 and x.stride(1) == 1 and x.stride(0) >= K:
+        stride = x.stride(0)
+    elif x.is_contiguous():
+        stride = K
+    else:
+        raise ValueError("moe_mx_quantize takes contiguous rows")
+    Kp = moe_mx_columns(K)
+    rows = x.numel() // K if K else 0
+    if codes is None:
+        codes = (torch.empty((*x.shape[:-1], Kp // 2), dtype=torch.uint8, device=x.device)
+                 if format == MOE_MX_E2M1 else
+                 torch.empty((*x.shape[:-1], Kp), dtype=torch.float8_e4m3fn, device=x.device))
+    if scales is None:
+        scales = torch.empty((*x.shape[:-1], Kp // 32), dtype=torch.float8_e8m0fnu,
+                             device=x.device)
+    _cuda(codes, scales)
+    _check("moe_mx_quantize",
+           lib.moe_mx_quantize(x.data_ptr(), rows, K, stride, _dt(x), format, codes.data_ptr(),
+                               scales.data_ptr(), _stream()))
+    return codes, scales
+
+
+def moe_mx_dequantize(codes, scales, K: int, format=None, dtype=torch.bfloat16, out=None):
+    """The values of an MX tensor, [..., K] in dtype.  format defaults to the
+    codes' own (MOE_MX_E2M1 when they are half as wide as an e4m3 row)."""
+    lib = load_library()
+    _cuda(codes, scales)
+    if format is None:
+        format = MOE_MX_E2M1 if codes.shape[-1] * 2 == scales.shape[-1] * 32 else MOE_MX_E4M3
+    Kp = moe_mx_columns(K)
+    if codes.shape[-1] != (Kp // 2 if format == MOE_MX_E2M1 else Kp) or \
+            scales.shape[-1] * 32 != Kp or codes.shape[:-1] != scales.shape[:-1]:
+        raise ValueError("codes and scales are not an MX tensor of K columns")
+    if out is None:
+        out = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
+    _check("moe_mx_dequantize",
+           lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), scales.numel() // (Kp // 32),
+                                 K, format, _dt(out), out.data_ptr(), _stream()))
+    return out
+
+
+def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_NONE, out=True,
+                     residual_out=None, codes=None, scales=None):
+    """h = x + residual (rounded; x without a residual), y = h * rsqrt(mean(h^2)
+    + eps) * weight; returns dict(residual=h or None, out=y or None, codes,
+    scales): y in 8 bits, MX (MOE_QUANT_MX_E4M3) or with a float32 scale per 128
+    columns (MOE_QUANT_E4M3_BLOCK128).  out: True, False, or the tensor to
+    write; residual_out may be residual itself."""
+    lib = load_library()
+    _cuda(x, weight, residual, residual_out, codes, scales)
+    if weight.dtype != x.dtype or (residual is not None and residual.dtype != x.dtype):
+        raise TypeError("x, weight and residual take one dtype")
+    T, H = x.shape
+    if weight.numel() != H or (residual is not None and residual.shape != x.shape):
+        raise ValueError("weight is [H] and residual has the shape of x")
+    if out is True:
+        out = torch.empty_like(x)
+    elif out is False:
+        out = None
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    if quant != MOE_QUANT_NONE:
+        Hp = moe_mx_columns(H)
+        if codes is None:
+            codes = torch.empty((T, Hp), dtype=torch.float8_e4m3fn, device=x.device)
+        if scales is None:
+            scales = (torch.empty((T, Hp // 32), dtype=torch.float8_e8m0fnu, device=x.device)
+                      if quant == MOE_QUANT_MX_E4M3 else
+                      torch.empty((T, Hp // 128), dtype=torch.float32, device=x.device))
+    _check("moe_add_rms_norm",
+           lib.moe_add_rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(),
+                                weight.data_ptr(), T, H, _dt(x), eps, quant,
+                                None if residual_out is None else residual_out.data_ptr(),
+                                None if out is None else out.data_ptr(),
+                                None if codes is None else codes.data_ptr(),
+                                None if scales is None else scales.data_ptr(), _stream()))
+    return {"residual": residual_out, "out": out, "codes": codes, "scales": scales}
+
+
+def moe_grouped_gemm_mx_workspace_size(M, N, K, E) -> int:
+    return load_library().moe_grouped_gemm_mx_workspace_size(M, N, K, E)
+
+
+def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[ActParams] = None,
+                        bias=None, row_to_route=None, top_k: int = 1, dtype=torch.bfloat16,
+                        mx_out: bool = False, out=None, out_scale=None, ws=None):
+    """Grouped GEMM of MX e4m3 rows a [R, Kp] by MX e2m1 weights w [E, N1, Kp / 2]
+    over the tight layout; row m is a[row_to_route[m] // top_k] when row_to_route
+    is given.  Returns out [M, N] in dtype, or with mx_out the MX e4m3 rows
+    (codes [M, Np], scales [M, Np / 32])."""
+    lib = load_library()
+    _cuda(a, a_scale, w, w_scale, seg_end, bias, row_to_route, out, out_scale)
+    R, Kp = a.shape
+    E, N1 = w.shape[0], w.shape[1]
+    M = R if row_to_route is None else row_to_route.numel()
+    gated = act is not None and act.kind in (MOE_ACT_SILU_AND_MUL, MOE_ACT_SWIGLU,
+                                             MOE_ACT_GELU_AND_MUL)
+    if Kp % 128 or w.shape[2] * 2 != Kp or a_scale.shape != (R, Kp // 32) or \
+            w_scale.shape != (E, N1, Kp // 32) or N1 != (2 * N if gated else N) or \
+            seg_end.numel() != E or (bias is not None and bias.shape != (E, N1)):
+        raise ValueError("operands are not MX tensors of matching extents")
+    if bias is not None and bias.dtype != dtype:
+        raise TypeError("bias takes the output's dtype")
+    if mx_out:
+        Np = moe_mx_columns(N)
+        if out is None:
+            out = torch.empty((M, Np), dtype=torch.float8_e4m3fn, device=a.device)
+        if out_scale is None:
+            out_scale = torch.empty((M, Np // 32), dtype=torch.float8_e8m0fnu, device=a.device)
+    elif out is None:
+        out = torch.empty((M, N), dtype=dtype, device=a.device)
+    if ws is None:
+        ws = _ws(lib.moe_grouped_gemm_mx_workspace_size(M, N, Kp, E), a.device)
+    dt = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}.get(dtype, MOE_F32)
+    _check("moe_grouped_gemm_mx",
+           lib.moe_grouped_gemm_mx(a.data_ptr(), a_scale.data_ptr(), R,
+                                   None if row_to_route is None else row_to_route.data_ptr(),
+                                   top_k, w.data_ptr(), w_scale.data_ptr(), _p(bias),
+                                   seg_end.data_ptr(), M, N, Kp, E, dt,
+                                   None if act is None else ctypes.byref(act), out.data_ptr(),
+                                   _p(out_scale), ws.data_ptr(), ws.numel(), _stream()))
+    return (out, out_scale) if mx_out else out
+
+
+def moe_workspace_size_mx(T, H, F, E, K) -> int:
+    return load_library().moe_workspace_size_mx(T, H, F, E, K)
+
+
+def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale, w_down,
+                       w_down_scale, H: int, F: int, p: RouteParams, act: ActParams,
+                       correction_bias=None, expert_ids=None, b_gate_up=None, b_down=None,
+                       dtype=torch.bfloat16, out=None, topk_weights_out=None, topk_ids_out=None,
+                       ws=None):
+    """The routed forward over MX operands: hidden MX e4m3 [T, Hp], weights MX
+    e2m1 [E, N1, Hp / 2] and [E, H, Fp / 2]; returns out [T, H] in dtype."""
+    lib = load_library()
+    _cuda(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale, w_down, w_down_scale,
+          correction_bias, expert_ids, b_gate_up, b_down, out)
+    T, Hp = hidden.shape
+    E, N1 = w_gate_up.shape[:2]
+    Fp = moe_mx_columns(F)
+    gated = act.kind in (MOE_ACT_SILU_AND_MUL, MOE_ACT_SWIGLU, MOE_ACT_GELU_AND_MUL)
+    if Hp != moe_mx_columns(H) or hidden_scale.shape != (T, Hp // 32) or \
+            N1 != (2 * F if gated else F) or w_gate_up.shape[2] * 2 != Hp or \
+            w_gate_up_scale.shape != (E, N1, Hp // 32) or w_down.shape != (E, H, Fp // 2) or \
+            w_down_scale.shape != (E, H, Fp // 32) or logits.shape != (T, E):
+        raise ValueError("operands are not MX tensors of matching extents")
+    for b, shape in ((b_gate_up, (E, N1)), (b_down, (E, H))):
+        if b is not None and (b.dtype != dtype or b.shape != shape):
+            raise ValueError("a bias is [E, rows] in the output's dtype")
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=hidden.device)
+    if ws is None:
+        ws = _ws(lib.moe_workspace_size_mx(T, H, F, E, p.top_k), hidden.device)
+    _check("moe_ffn_forward_mx",
+           lib.moe_ffn_forward_mx(hidden.data_ptr(), hidden_scale.data_ptr(), logits.data_ptr(),
+                                  w_gate_up.data_ptr(), w_gate_up_scale.data_ptr(),
+                                  w_down.data_ptr(), w_down_scale.data_ptr(), _p(correction_bias),
+                                  _p(expert_ids), _p(b_gate_up), _p(b_down), T, H, F, E, _dt(out),
+                                  ctypes.byref(_rp(p, logits)), ctypes.byref(act), out.data_ptr(),
+                                  _p(topk_weights_out), _p(topk_ids_out), ws.data_ptr(),
+                                  ws.numel(), _stream()))
     return out
 
 
