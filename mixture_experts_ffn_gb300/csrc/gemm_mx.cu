@@ -17,17 +17,24 @@
 // 32 lanes are one MX block of a token's output, so its scale is one
 // redux.sync.
 //
-// Roles (320 threads, one CTA per SM, persistent)
+// Roles (512 threads, one CTA per SM, persistent)
 //   warp 0 lane 0 : TMA producer of the weight codes.  The map's type expands
 //                   each 16 packed values (8 bytes) into a 16-byte chunk of
 //                   shared memory, the form the MMA reads 4-bit values in.
-//   warp 1        : TMEM; lane 0 copies each stage's scales from shared
-//                   memory into TMEM (tcgen05.cp) and issues the MMAs
-//   warps 2..5    : epilogue
-//   warps 6..9    : cp.async loaders of the token rows (gathered through
-//                   row_to_route when given) and of both operands' scales
+//   warp 1        : TMEM; lane 0 issues the MMAs
+//   warps 2..3    : cp.async loaders of the token rows (gathered through
+//                   row_to_route when given)
+//   warps 4..7    : both operands' scales, four stages at a time through shared
+//                   memory into registers, then tcgen05.st into TMEM, each warp
+//                   its own lane quarter (the MMA wants them in all four).
+//                   tcgen05.cp would need no warps but runs in the MMAs' own
+//                   pipe: 170 cycles a stage on top of 600 (N <= 144), where a
+//                   stage's weights take 705 at HBM speed.
+//   warps 8..15   : epilogue, two warps a lane quarter
 // Stage: 128 columns of K, i.e. four K32 MMA steps; the 4 scale bytes of a
 // row and stage are one 32-bit TMEM cell, step j using byte j of it.
+// Measured back to back, an M128 K32 step with 4-bit weights takes
+// max(75, N / 2) cycles.
 // Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
 
@@ -49,9 +56,11 @@ constexpr int BK = 128;                    // columns of K per stage
 constexpr int W_BYTES = 128 * BK;          // one half's weights, expanded: 16 KB
 constexpr int W_TX = W_BYTES / 2;          // bytes its copy counts: the packed ones (the gaps of
                                            // the expanded form are not written)
-constexpr int SF_ATOM = 512;               // scales of 128 rows and one stage
-constexpr int NUM_THREADS = 320;
-constexpr int kEpiWarp0 = 2, kLoadWarp0 = 6;
+constexpr int SG = 4;                      // stages whose scales travel together
+constexpr int kLoadWarp0 = 2, kScaleWarp0 = 4, kEpiWarp0 = 8, kEpiWarps = 8;
+constexpr int kLoaders = 32 * (kScaleWarp0 - kLoadWarp0);
+constexpr int NUM_THREADS = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kScaleBar = 1;               // named barrier of the scale warps
 constexpr size_t kSmemLimit = 227 * 1024;
 
 // Token columns of a tile and what follows from them: ring depth and TMEM.
@@ -60,12 +69,14 @@ struct Cfg {
   static constexpr int NMAX = NMAX_;
   static constexpr int kAccs = NMAX <= 112 ? 2 : 1;  // accumulators (512 TMEM columns in all)
   static constexpr int B_BYTES = NMAX * BK;
-  static constexpr int SFB_ATOMS = (NMAX + 127) / 128;
-  static constexpr int SF_BYTES = (2 + SFB_ATOMS) * SF_ATOM;
   static constexpr int STAGE_BYTES = 2 * W_BYTES + B_BYTES;
-  static constexpr int kFixed = 8 * 1024;  // barriers, tile prefix, alignment
-  static constexpr int STAGES = (int)((kSmemLimit - kFixed) / (STAGE_BYTES + SF_BYTES));
-  static constexpr int SF_COLS = 4 * (2 + SFB_ATOMS);  // TMEM columns of a stage's scales
+  static constexpr int SF_ROWS = 256 + (NMAX + 31) / 32 * 32;  // rows with scales, 16 bytes each
+  static constexpr int SF_BYTES = SF_ROWS * 4 * SG;
+  static constexpr int kFixed = 6 * 1024 + SF_BYTES;  // barriers, tile prefix, alignment, scales
+  static constexpr int STAGES = (int)((kSmemLimit - kFixed) / STAGE_BYTES);
+  static constexpr int SFB = (NMAX + 31) / 32;  // TMEM columns of the tokens' scales
+  static constexpr int SFB_ST = SFB > 4 ? 8 : SFB > 2 ? 4 : SFB;  // ... as one store writes them
+  static constexpr int SF_COLS = 8 + (SFB_ST + 3) / 4 * 4;  // TMEM columns of a stage's scales
   static constexpr int ACC_COLS = 2 * NMAX;
   static constexpr int kSf0 = kAccs * ACC_COLS;
   static_assert(kSf0 + STAGES * SF_COLS <= 512, "TMEM columns");
@@ -100,20 +111,26 @@ struct MxArgs {
   float limit, alpha, beta;
 };
 
-// Shared-memory descriptor of a 32-row x 16-byte scale matrix: no swizzle,
-// 8-row core matrices 128 bytes apart.
-__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(128 >> 4) << 32;  // stride byte offset
-  d |= (uint64_t)1 << 46;           // descriptor version
-  return d;
-}
-// 128 rows' scales (32 rows x 16 bytes) to four TMEM columns, repeated in all
-// four lane quarters
-__device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-               : "memory");
+// N consecutive TMEM columns of this warp's lanes from registers
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
+  if constexpr (N == 1)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r[0])
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1])
+                 : "memory");
+  else if constexpr (N == 4)
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+  else
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
 }
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
@@ -146,12 +163,36 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok
                "r"(ok ? 4 : 0)
                : "memory");
 }
-// byte offset of row r's four scales in its 128-row scale matrix
-__device__ __forceinline__ uint32_t sf_off(int r) { return (uint32_t)((r & 31) * 16 + (r >> 5) * 4); }
 
 struct MxTile {
   int e, ft, m0, nv, N;  // expert, output tile, first row, rows, MMA columns
 };
+// row of `a` for tile row r, or -1 (padding, or a map entry out of range)
+__device__ __forceinline__ int source_row(const MxArgs& p, const MxTile& t, int r) {
+  if (r >= t.nv) return -1;
+  int m = t.m0 + r;
+  if (p.grows) {
+    m = p.grows[m];
+    m = m < 0 ? -1 : m / p.gdiv;
+  }
+  return m < p.a_rows ? m : -1;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// named_sync that returns whether v is true in every thread
+__device__ __forceinline__ bool named_and(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
 template <int NMAX>
 __device__ __forceinline__ MxTile mx_decode(int t, const int* prefix, const int32_t* seg_end, int E,
                                             int M) {
@@ -230,18 +271,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sf = smem + (size_t)STAGES * C::STAGE_BYTES;
-  auto* sh = reinterpret_cast<MxShared<STAGES>*>(sf + (size_t)STAGES * C::SF_BYTES);
+  auto* sh = reinterpret_cast<MxShared<STAGES>*>(sf + C::SF_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh->abort;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&sh->full[s], 1 + 128);  // the producer's expect-tx and every loader thread
+      // the producer's expect-tx, every token loader thread, every scale warp
+      mbar_init(&sh->full[s], 1 + kLoaders + 4);
       mbar_init(&sh->empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sh->tfull[a], 1);
-      mbar_init(&sh->tempty[a], 128);
+      mbar_init(&sh->tempty[a], 32 * kEpiWarps);
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
@@ -311,22 +353,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
         const uint32_t idesc = idesc_mx(t.N);
-        const bool two = t.N > 128;
         for (int kb = 0; kb < nkb; ++kb) {
           if (!wait_fast(&sh->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
           // the loaders wrote through the generic proxy; tcgen05 reads through
           // the async proxy
           fence_proxy_async_smem();
           tc_fence_after();
-          // the stage's scales go to TMEM columns of their own, free since the
-          // stage's last MMAs completed; copies and MMAs of one thread run in
-          // issue order
           const uint32_t sfa = tmem + (uint32_t)(C::kSf0 + stage * C::SF_COLS), sfb = sfa + 8;
-          const uint64_t sd = sf_desc(su32(sf + (size_t)stage * C::SF_BYTES));
-          sf_copy(sfa, sd);
-          sf_copy(sfa + 4, sd + (SF_ATOM >> 4));
-          sf_copy(sfb, sd + 2 * (SF_ATOM >> 4));
-          if (C::SFB_ATOMS == 2 && two) sf_copy(sfb + 4, sd + 3 * (SF_ATOM >> 4));
           const uint64_t ad = sw128_desc(su32(smem + (size_t)stage * C::STAGE_BYTES));
           const uint64_t bd = ad + (2 * W_BYTES >> 4);
 #pragma unroll
@@ -349,67 +382,37 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         drain_wait(&sh->drain, 0);
       }
     }
-  } else if (warp >= kLoadWarp0) {
-    // ------------------------------------------------ loaders (tokens, scales)
-    // Token rows: thread lt owns 16-byte chunk lt % 8 of rows lt / 8 + 16 i, so
-    // eight lanes read one 128-byte row piece; chunk ch of row r lands at chunk
-    // ch ^ (r % 8), the 128-byte swizzle.  Scales: one 4-byte piece per row.
+  } else if (warp < kScaleWarp0) {
+    // ------------------------------------------------ token loaders
+    // Thread lt owns 16-byte chunk lt % 8 of rows lt / 8 + 8 i, so eight lanes
+    // read one 128-byte row piece; chunk ch of row r lands at chunk
+    // ch ^ (r % 8), the 128-byte swizzle.
     const int lt = threadIdx.x - kLoadWarp0 * 32;
     const int ch = lt & 7, r0 = lt >> 3;
     const uint32_t dst0 = (uint32_t)(2 * W_BYTES + r0 * 128 + ((ch ^ (r0 & 7)) << 4));
-    constexpr int RI = NMAX / 16, SI = C::SFB_ATOMS;
+    constexpr int STEP = kLoaders / 8, RI = NMAX / STEP;
+    static_assert(STEP % 8 == 0, "the swizzle of a thread's rows");
     // the token rows are read again by every output tile of their expert:
     // kept in L2 ahead of the weight stream
     uint64_t keep;
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
-    const int sp = p.Kp / 32;  // scale bytes of a row
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    // row of `a` for tile row r, or -1 (padding, or a map entry out of range)
-    auto source = [&](const MxTile& t, int r) {
-      if (r >= t.nv) return -1;
-      int m = t.m0 + r;
-      if (p.grows) {
-        m = p.grows[m];
-        m = m < 0 ? -1 : m / p.gdiv;
-      }
-      return m < p.a_rows ? m : -1;
-    };
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
       const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
       if (t.nv == 0) continue;
-      int src[RI], ssrc[SI];
+      int src[RI];
 #pragma unroll
-      for (int i = 0; i < RI; ++i) src[i] = 16 * i < t.N ? source(t, r0 + 16 * i) : -1;
-#pragma unroll
-      for (int i = 0; i < SI; ++i) ssrc[i] = source(t, lt + 128 * i);
-      // weight rows of the two halves
-      const uint8_t* ws[2];
-      bool wok[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int f = GATED ? t.ft * 128 + lt : t.ft * 256 + h * 128 + lt;
-        wok[h] = f < p.Nout;
-        const int row = GATED ? f * p.row_step + h * p.half_step : f;
-        ws[h] = p.w_scale + ((size_t)t.e * p.N1 + (wok[h] ? row : 0)) * sp;
-      }
+      for (int i = 0; i < RI; ++i) src[i] = STEP * i < t.N ? source_row(p, t, r0 + STEP * i) : -1;
       for (int kb = 0; kb < nkb; ++kb) {
         if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
-        const uint32_t sfs = su32(sf + (size_t)stage * C::SF_BYTES);
-        cp_async4(sfs + sf_off(lt), ws[0] + kb * 4, wok[0]);
-        cp_async4(sfs + SF_ATOM + sf_off(lt), ws[1] + kb * 4, wok[1]);
-#pragma unroll
-        for (int i = 0; i < SI; ++i)
-          if (lt + 128 * i < t.N)
-            cp_async4(sfs + (2 + i) * SF_ATOM + sf_off(lt),
-                      p.a_scale + (size_t)max(ssrc[i], 0) * sp + kb * 4, ssrc[i] >= 0);
         const uint32_t dst = su32(smem + (size_t)stage * C::STAGE_BYTES) + dst0;
         const uint8_t* a = p.a + kb * BK + ch * 16;
 #pragma unroll
         for (int i = 0; i < RI; ++i)
-          if (16 * i < t.N)
-            cp_async16(dst + i * 16 * 128, a + (size_t)max(src[i], 0) * p.Kp, src[i] >= 0, keep);
+          if (STEP * i < t.N)
+            cp_async16(dst + i * STEP * 128, a + (size_t)max(src[i], 0) * p.Kp, src[i] >= 0, keep);
         // arrives on the stage's full barrier once this thread's copies land
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                          su32(&sh->full[stage]))
@@ -418,9 +421,111 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight at exit
+  } else if (warp < kEpiWarp0) {
+    // ------------------------------------------------ scales
+    // Rows 0..255 of the buffer are the two halves' weight rows, the others the
+    // tokens; a row holds SG stages' words.  Copying, four lanes share a row
+    // and eight rows go at once (a row's scales need not be 16-byte aligned);
+    // reading back, lane l takes rows l, 32 + l, ...: the TMEM cells of its lane.
+    const int st = threadIdx.x - kScaleWarp0 * 32, quad = warp & 3;
+    constexpr int ROWS = 256 + C::SFB * 32, PER = ROWS / 32;  // rows; rows a copying thread
+    const int sp = p.Kp / 32;  // scale bytes of a row
+    const int word = st & 3, rw0 = st >> 2;
+    const uint32_t sf_dst = su32(sf) + (uint32_t)(rw0 * 16 + word * 4);
+    const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + C::kSf0;
+    const int ngr = (nkb + SG - 1) / SG;
+    // The copies run one group ahead of the stores: (ltile, lg) is the next
+    // group to copy, src its rows' scales (null: zeros).
+    const uint8_t* src[PER];
+    int ltile = blockIdx.x, lg = 0;
+    auto seek = [&]() {  // rows of the first tile at or after ltile that has any
+      for (; ltile < total; ltile += gridDim.x) {
+        const MxTile t = mx_decode<NMAX>(ltile, sh->prefix, p.seg_end, p.E, p.M);
+        if (t.nv == 0) continue;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int r = rw0 + 32 * i;
+          if (i < 8) {  // weight row of half i / 4
+            const int h = i >> 2;
+            const int f = GATED ? t.ft * 128 + (r & 127) : t.ft * 256 + r;
+            const int row = GATED ? f * p.row_step + h * p.half_step : f;
+            src[i] = f < p.Nout ? p.w_scale + ((size_t)t.e * p.N1 + row) * sp : nullptr;
+          } else {
+            const int m = source_row(p, t, r - 256);
+            src[i] = m >= 0 ? p.a_scale + (size_t)m * sp : nullptr;
+          }
+        }
+        return;
+      }
+    };
+    auto copy_group = [&]() {
+      if (ltile < total) {
+        const int kb = lg * SG + word;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const bool v = src[i] != nullptr && kb < nkb;
+          cp_async4(sf_dst + i * 32 * 16, v ? src[i] + kb * 4 : p.w_scale, v);
+        }
+        if (++lg == ngr) {
+          lg = 0;
+          ltile += gridDim.x;
+          seek();
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    seek();
+    copy_group();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+      if (t.nv == 0) continue;
+      for (int gr = 0; gr < ngr && ok; ++gr) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        named_sync(kScaleBar, 128);
+        uint32_t w[SG][8], b[SG][C::SFB_ST];
+#pragma unroll
+        for (int c = 0; c < 8 + C::SFB_ST; ++c) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (c < 8 + C::SFB) v = *reinterpret_cast<const uint4*>(sf + (c * 32 + lane) * 16);
+          if (c < 8) {
+            w[0][c] = v.x; w[1][c] = v.y; w[2][c] = v.z; w[3][c] = v.w;
+          } else {
+            b[0][c - 8] = v.x; b[1][c - 8] = v.y; b[2][c - 8] = v.z; b[3][c - 8] = v.w;
+          }
+        }
+        named_sync(kScaleBar, 128);  // read by all four warps: the buffer is free
+        copy_group();
+#pragma unroll
+        for (int j = 0; j < SG; ++j) {
+          if (gr * SG + j < nkb && ok) {
+            // the stage's TMEM columns are free once its last MMAs completed
+            ok = wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+              tc_fence_after();
+              const uint32_t d = taddr + (uint32_t)(stage * C::SF_COLS);
+              tmem_st<8>(d, w[j]);
+              tmem_st<C::SFB_ST>(d + 8, b[j]);
+              asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh->full[stage]);
+              if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+          }
+        }
+        // the four warps stop together: they share the barrier
+        ok = named_and(kScaleBar, 128, ok);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
-    // ------------------------------------------------ epilogue (warps 2..5)
+    // ------------------------------------------------ epilogue
     const int quad = warp & 3;  // TMEM lanes 32 * quad ..
+    const int c0 = (warp - kEpiWarp0) >> 2;  // 16-token groups c0, c0 + 2, ..
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     int acc = 0;
     uint32_t aphase = 0;
@@ -446,7 +551,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       const uint32_t base = lanes + (uint32_t)(acc * C::ACC_COLS);
 #pragma unroll 1
-      for (int c = 0; c < t.nv; c += 16) {
+      for (int c = 16 * c0; c < t.nv; c += 16 * (kEpiWarps / 4)) {
         uint32_t r[2][16];
         tmem_ld16(base + c, r[0]);
         tmem_ld16(base + NMAX + c, r[1]);
@@ -488,7 +593,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 template <int NMAX, bool GATED, int ACT, bool MXOUT, bool F16>
 cudaError_t go(const CUtensorMap& tm, const MxArgs& p, cudaStream_t s) {
   using C = Cfg<NMAX>;
-  constexpr size_t smem = (size_t)C::STAGES * (C::STAGE_BYTES + C::SF_BYTES) +
+  constexpr size_t smem = (size_t)C::STAGES * C::STAGE_BYTES + C::SF_BYTES +
                           sizeof(MxShared<C::STAGES>) + 1024;
   static_assert(smem <= kSmemLimit, "shared memory");
   auto kern = gemm_mx_kernel<NMAX, GATED, ACT, MXOUT, F16>;
