@@ -27,14 +27,12 @@
 //   warps 4..7    : both operands' scales, four stages at a time through shared
 //                   memory into registers, then tcgen05.st into TMEM, each warp
 //                   its own lane quarter (the MMA wants them in all four).
-//                   tcgen05.cp would need no warps but runs in the MMAs' own
-//                   pipe: 170 cycles a stage on top of 600 (N <= 144), where a
-//                   stage's weights take 705 at HBM speed.
+//                   tcgen05.cp would need no warps, but runs in the MMAs' own
+//                   pipe and costs it 170 cycles a stage.
 //   warps 8..15   : epilogue, two warps a lane quarter
 // Stage: 128 columns of K, i.e. four K32 MMA steps; the 4 scale bytes of a
 // row and stage are one 32-bit TMEM cell, step j using byte j of it.
-// Measured back to back, an M128 K32 step with 4-bit weights takes
-// max(75, N / 2) cycles.
+// Measured back to back, a stage's eight MMAs take max(313, 4 N) cycles.
 // Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
 
@@ -57,6 +55,7 @@ constexpr int W_BYTES = 128 * BK;          // one half's weights, expanded: 16 K
 constexpr int W_TX = W_BYTES / 2;          // bytes its copy counts: the packed ones (the gaps of
                                            // the expanded form are not written)
 constexpr int SG = 4;                      // stages whose scales travel together
+constexpr int SBUFS = 3;                   // such groups in flight or in use
 constexpr int kLoadWarp0 = 2, kScaleWarp0 = 4, kEpiWarp0 = 8, kEpiWarps = 8;
 constexpr int kLoaders = 32 * (kScaleWarp0 - kLoadWarp0);
 constexpr int NUM_THREADS = 32 * (kEpiWarp0 + kEpiWarps);
@@ -72,7 +71,7 @@ struct Cfg {
   static constexpr int STAGE_BYTES = 2 * W_BYTES + B_BYTES;
   static constexpr int SF_ROWS = 256 + (NMAX + 31) / 32 * 32;  // rows with scales, 16 bytes each
   static constexpr int SF_BYTES = SF_ROWS * 4 * SG;
-  static constexpr int kFixed = 6 * 1024 + SF_BYTES;  // barriers, tile prefix, alignment, scales
+  static constexpr int kFixed = 6 * 1024 + SBUFS * SF_BYTES;  // barriers, tile prefix, alignment, scales
   static constexpr int STAGES = (int)((kSmemLimit - kFixed) / STAGE_BYTES);
   static constexpr int SFB = (NMAX + 31) / 32;  // TMEM columns of the tokens' scales
   static constexpr int SFB_ST = SFB > 4 ? 8 : SFB > 2 ? 4 : SFB;  // ... as one store writes them
@@ -132,19 +131,53 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
-__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
-                                       uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+// The eight MMAs of a stage (four K32 steps of both halves; half 1's weights
+// 16 KB on, its accumulator in d1) and the commit that frees the stage, issued
+// by one elected lane of a CONVERGED warp.  All operands are warp-uniform, so
+// they stay in uniform registers: the stage then takes max(313, 4 N) cycles,
+// against 600 when a diverged lane issues the MMAs one by one and moves every
+// operand over first.  Descriptors advance by 32 bytes (2) a step; a step's
+// scale byte is selected in the instruction descriptor (bits 4 and 29).
+#define MOE_MX_MMA(d, a, b, i, sa, p) \
+  "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [" d "], " a ", " b ", " i \
+  ", [" sa "], [sb], " p ";\n\t"
+__device__ __forceinline__ void mma_stage(uint32_t d0, uint32_t d1, uint64_t ad, uint64_t bd,
+                                          uint32_t idesc, uint32_t sfa, uint32_t accumulate,
+                                          uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], "
-      "[%6], p;\n\t}" ::"r"(d),
-      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a0, a1, b0;\n\t.reg .b32 i0, s1, sb;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "setp.eq.b32 t, %6, %6;\n\t"
+      "add.u32 s1, %5, 4;\n\t"
+      "add.u32 sb, %5, 8;\n\t"
+      "add.u64 a1, %2, 1024;\n\t"
+      MOE_MX_MMA("%0", "%2", "%3", "%4", "%5", "p")
+      MOE_MX_MMA("%1", "a1", "%3", "%4", "s1", "p")
+      "add.u64 a0, %2, 2;\n\tadd.u64 a1, %2, 1026;\n\tadd.u64 b0, %3, 2;\n\t"
+      "add.u32 i0, %4, 0x20000010;\n\t"
+      MOE_MX_MMA("%0", "a0", "b0", "i0", "%5", "t")
+      MOE_MX_MMA("%1", "a1", "b0", "i0", "s1", "t")
+      "add.u64 a0, %2, 4;\n\tadd.u64 a1, %2, 1028;\n\tadd.u64 b0, %3, 4;\n\t"
+      "add.u32 i0, %4, 0x40000020;\n\t"
+      MOE_MX_MMA("%0", "a0", "b0", "i0", "%5", "t")
+      MOE_MX_MMA("%1", "a1", "b0", "i0", "s1", "t")
+      "add.u64 a0, %2, 6;\n\tadd.u64 a1, %2, 1030;\n\tadd.u64 b0, %3, 6;\n\t"
+      "add.u32 i0, %4, 0x60000030;\n\t"
+      MOE_MX_MMA("%0", "a0", "b0", "i0", "%5", "t")
+      MOE_MX_MMA("%1", "a1", "b0", "i0", "s1", "t")
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t}" ::"r"(d0),
+      "r"(d1), "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(accumulate), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void mx_commit(uint32_t bar) {
+#undef MOE_MX_MMA
+static_assert((W_BYTES >> 4) == 1024, "half 1's descriptor offset");
+// commit by one elected lane of a converged warp
+__device__ __forceinline__ void mx_commit_elect(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 // Instruction descriptor, kind::mxf8f6f4: A e2m1 (format 5 at bit 7), B e4m3
@@ -271,7 +304,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sf = smem + (size_t)STAGES * C::STAGE_BYTES;
-  auto* sh = reinterpret_cast<MxShared<STAGES>*>(sf + C::SF_BYTES);
+  auto* sh = reinterpret_cast<MxShared<STAGES>*>(sf + SBUFS * C::SF_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh->abort;
 
@@ -341,46 +374,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------ MMA issuer
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, aphase = 0;
-      bool ok = true, any = false;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
-        if (t.nv == 0) continue;
-        if (!wait_fast(&sh->tempty[acc], aphase ^ 1u, abort_flag, p.status)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
-        const uint32_t idesc = idesc_mx(t.N);
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!wait_fast(&sh->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
-          // the loaders wrote through the generic proxy; tcgen05 reads through
-          // the async proxy
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint32_t sfa = tmem + (uint32_t)(C::kSf0 + stage * C::SF_COLS), sfb = sfa + 8;
-          const uint64_t ad = sw128_desc(su32(smem + (size_t)stage * C::STAGE_BYTES));
-          const uint64_t bd = ad + (2 * W_BYTES >> 4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t id = idesc | ((uint32_t)j << 4) | ((uint32_t)j << 29);
-            const uint32_t go = (kb | j) != 0;
-            mma_mx(d, ad + 2 * j, bd + 2 * j, id, sfa, sfb, go);
-            mma_mx(d + NMAX, ad + (W_BYTES >> 4) + 2 * j, bd + 2 * j, id, sfa + 4, sfb, go);
-          }
-          mx_commit(su32(&sh->empty[stage]));
-          any = true;
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-        }
+    // ------------------------------------------------ MMA issuer (whole warp)
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, aphase = 0;
+    bool ok = true, any = false;
+    const uint64_t ad0 = sw128_desc(su32(smem));
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+      if (t.nv == 0) continue;
+      ok = __all_sync(0xffffffffu, wait_fast(&sh->tempty[acc], aphase ^ 1u, abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
+      const uint32_t idesc = idesc_mx(__shfl_sync(0xffffffffu, t.N, 0));
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_fast(&sh->full[stage], phase, abort_flag, p.status));
         if (!ok) break;
-        mx_commit(su32(&sh->tfull[acc]));
-        if (++acc == C::kAccs) { acc = 0; aphase ^= 1u; }
+        // the loaders wrote through the generic proxy; tcgen05 reads through
+        // the async proxy
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t ad = ad0 + (uint64_t)((stage * C::STAGE_BYTES) >> 4);
+        mma_stage(d, d + NMAX, ad, ad + (2 * W_BYTES >> 4), idesc,
+                  tmem + (uint32_t)(C::kSf0 + stage * C::SF_COLS), kb != 0 ? 1u : 0u,
+                  su32(&sh->empty[stage]));
+        any = true;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      if (!ok && any) {  // every MMA issued so far done before TMEM is freed
-        mx_commit(su32(&sh->drain));
-        drain_wait(&sh->drain, 0);
-      }
+      if (!ok) break;
+      mx_commit_elect(su32(&sh->tfull[acc]));
+      if (++acc == C::kAccs) { acc = 0; aphase ^= 1u; }
+    }
+    if (!ok && any) {  // every MMA issued so far done before TMEM is freed
+      mx_commit_elect(su32(&sh->drain));
+      drain_wait(&sh->drain, 0);
     }
   } else if (warp < kScaleWarp0) {
     // ------------------------------------------------ token loaders
@@ -434,10 +461,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t sf_dst = su32(sf) + (uint32_t)(rw0 * 16 + word * 4);
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + C::kSf0;
     const int ngr = (nkb + SG - 1) / SG;
-    // The copies run one group ahead of the stores: (ltile, lg) is the next
-    // group to copy, src its rows' scales (null: zeros).
+    // The copies run SBUFS groups ahead of the stores (one group is four
+    // stages, about 2800 cycles at HBM speed; a load under that load can take
+    // longer): (ltile, lg) is the next group to copy, into buffer lbuf, src its
+    // rows' scales (null: zeros).
     const uint8_t* src[PER];
-    int ltile = blockIdx.x, lg = 0;
+    int ltile = blockIdx.x, lg = 0, lbuf = 0, buf = 0;
     auto seek = [&]() {  // rows of the first tile at or after ltile that has any
       for (; ltile < total; ltile += gridDim.x) {
         const MxTile t = mx_decode<NMAX>(ltile, sh->prefix, p.seg_end, p.E, p.M);
@@ -464,8 +493,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
           const bool v = src[i] != nullptr && kb < nkb;
-          cp_async4(sf_dst + i * 32 * 16, v ? src[i] + kb * 4 : p.w_scale, v);
+          cp_async4(sf_dst + lbuf * C::SF_BYTES + i * 32 * 16, v ? src[i] + kb * 4 : p.w_scale, v);
         }
+        if (++lbuf == SBUFS) lbuf = 0;
         if (++lg == ngr) {
           lg = 0;
           ltile += gridDim.x;
@@ -475,7 +505,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     seek();
-    copy_group();
+    for (int i = 0; i < SBUFS; ++i) copy_group();
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -483,13 +513,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
       if (t.nv == 0) continue;
       for (int gr = 0; gr < ngr && ok; ++gr) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(SBUFS - 1) : "memory");
         named_sync(kScaleBar, 128);
         uint32_t w[SG][8], b[SG][C::SFB_ST];
 #pragma unroll
         for (int c = 0; c < 8 + C::SFB_ST; ++c) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (c < 8 + C::SFB) v = *reinterpret_cast<const uint4*>(sf + (c * 32 + lane) * 16);
+          if (c < 8 + C::SFB) v = *reinterpret_cast<const uint4*>(sf + buf * C::SF_BYTES + (c * 32 + lane) * 16);
           if (c < 8) {
             w[0][c] = v.x; w[1][c] = v.y; w[2][c] = v.z; w[3][c] = v.w;
           } else {
@@ -498,6 +528,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         named_sync(kScaleBar, 128);  // read by all four warps: the buffer is free
         copy_group();
+        if (++buf == SBUFS) buf = 0;
 #pragma unroll
         for (int j = 0; j < SG; ++j) {
           if (gr * SG + j < nkb && ok) {
@@ -593,7 +624,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 template <int NMAX, bool GATED, int ACT, bool MXOUT, bool F16>
 cudaError_t go(const CUtensorMap& tm, const MxArgs& p, cudaStream_t s) {
   using C = Cfg<NMAX>;
-  constexpr size_t smem = (size_t)C::STAGES * C::STAGE_BYTES + C::SF_BYTES +
+  constexpr size_t smem = (size_t)C::STAGES * C::STAGE_BYTES + SBUFS * C::SF_BYTES +
                           sizeof(MxShared<C::STAGES>) + 1024;
   static_assert(smem <= kSmemLimit, "shared memory");
   auto kern = gemm_mx_kernel<NMAX, GATED, ACT, MXOUT, F16>;
