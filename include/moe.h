@@ -621,8 +621,8 @@ moe_status moe_add_rms_norm(const void* x, const void* residual, const void* wei
  *                and out_scale are MX e4m3 rows [M, Np], [M, Np / 32] of the
  *                unrounded act(p): the next product's operand
  *   ws           >= moe_grouped_gemm_mx_workspace_size(M, N, K, E) bytes
- * a 16-byte, w 32-byte, the scales 4-byte aligned, and out and out_scale
- * 16-byte aligned when MX (MOE_ERR_UNSUPPORTED otherwise, and for MOE_F32).
+ * a and the scales 16-byte, w 32-byte aligned, and out and out_scale 16-byte
+ * aligned when MX (MOE_ERR_UNSUPPORTED otherwise, and for MOE_F32).
  * Rows past seg_end[E-1] are not written.  E <= 1024. */
 moe_status moe_grouped_gemm_mx(const void* a, const void* a_scale, int a_rows,
                                const int32_t* row_to_route, int top_k, const void* w,

@@ -1021,7 +1021,7 @@ moe_status moe_grouped_gemm_mx(const void* a, const void* a_scale, int a_rows,
   if (dtype == MOE_F32) return MOE_ERR_UNSUPPORTED;
   if (!w || !w_scale || !seg_end || (M > 0 && (!out || (a_rows > 0 && (!a || !a_scale)))))
     return MOE_ERR_INVALID_ARG;
-  if (!aligned16(a) || !aligned(a_scale, 4) || !aligned(w, 32) || !aligned(w_scale, 4) ||
+  if (!aligned16(a) || !aligned16(a_scale) || !aligned(w, 32) || !aligned16(w_scale) ||
       !aligned(out, out_scale ? 16 : 2) || !aligned16(out_scale))
     return MOE_ERR_UNSUPPORTED;
   const size_t need = moe_grouped_gemm_mx_workspace_size(M, N, K, E);
@@ -1069,8 +1069,8 @@ moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, cons
   if (!w_gate_up || !w_gate_up_scale || !w_down || !w_down_scale ||
       (T > 0 && (!hidden || !hidden_scale || !out)))
     return MOE_ERR_INVALID_ARG;
-  if (!aligned16(hidden) || !aligned(hidden_scale, 4) || !aligned(w_gate_up, 32) ||
-      !aligned(w_gate_up_scale, 4) || !aligned(w_down, 32) || !aligned(w_down_scale, 4) ||
+  if (!aligned16(hidden) || !aligned16(hidden_scale) || !aligned(w_gate_up, 32) ||
+      !aligned16(w_gate_up_scale) || !aligned(w_down, 32) || !aligned16(w_down_scale) ||
       !aligned(out, 2))
     return MOE_ERR_UNSUPPORTED;
   const MxForwardWs L(T, H, F, E, K);

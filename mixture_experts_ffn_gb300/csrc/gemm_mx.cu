@@ -55,7 +55,7 @@ constexpr int W_BYTES = 128 * BK;          // one half's weights, expanded: 16 K
 constexpr int W_TX = W_BYTES / 2;          // bytes its copy counts: the packed ones (the gaps of
                                            // the expanded form are not written)
 constexpr int SG = 4;                      // stages whose scales travel together
-constexpr int SBUFS = 3;                   // such groups in flight or in use
+constexpr int SBUFS = 4;                   // chunks of scales in flight or in use
 constexpr int kLoadWarp0 = 2, kScaleWarp0 = 4, kEpiWarp0 = 8, kEpiWarps = 8;
 constexpr int kLoaders = 32 * (kScaleWarp0 - kLoadWarp0);
 constexpr int NUM_THREADS = 32 * (kEpiWarp0 + kEpiWarps);
@@ -69,9 +69,8 @@ struct Cfg {
   static constexpr int kAccs = NMAX <= 112 ? 2 : 1;  // accumulators (512 TMEM columns in all)
   static constexpr int B_BYTES = NMAX * BK;
   static constexpr int STAGE_BYTES = 2 * W_BYTES + B_BYTES;
-  static constexpr int SF_ROWS = 256 + (NMAX + 31) / 32 * 32;  // rows with scales, 16 bytes each
-  static constexpr int SF_BYTES = SF_ROWS * 4 * SG;
-  static constexpr int kFixed = 6 * 1024 + SBUFS * SF_BYTES;  // barriers, tile prefix, alignment, scales
+  static constexpr int SF_BYTES = (256 + NMAX) * 4 * SG;  // a chunk of every row's scales
+  static constexpr int kFixed = 6 * 1024 - 512 + SBUFS * SF_BYTES;  // scales, barriers, prefix
   static constexpr int STAGES = (int)((kSmemLimit - kFixed) / STAGE_BYTES);
   static constexpr int SFB = (NMAX + 31) / 32;  // TMEM columns of the tokens' scales
   static constexpr int SFB_ST = SFB > 4 ? 8 : SFB > 2 ? 4 : SFB;  // ... as one store writes them
@@ -189,11 +188,6 @@ __device__ __forceinline__ uint32_t idesc_mx(int N) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok, uint64_t pol) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
                "l"(src), "r"(ok ? 16 : 0), "l"(pol)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 4 : 0)
                : "memory");
 }
 
@@ -357,13 +351,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint8_t* dst = smem + (size_t)stage * C::STAGE_BYTES;
           mbar_expect_tx(&sh->full[stage], 2 * W_TX);
           // rows past the operand read as zeros and count in full
-          if constexpr (GATED) {
-            tma_4d(dst, &tm_w, &sh->full[stage], kb * BK, t.ft * 128, 0, t.e);
-            tma_4d(dst + W_BYTES, &tm_w, &sh->full[stage], kb * BK, t.ft * 128, 1, t.e);
-          } else {
-            tma_4d(dst, &tm_w, &sh->full[stage], kb * BK, t.ft * 256, 0, t.e);
-            tma_4d(dst + W_BYTES, &tm_w, &sh->full[stage], kb * BK, t.ft * 256 + 128, 0, t.e);
-          }
+          tma_4d(dst, &tm_w, &sh->full[stage], kb * BK, t.ft * FT, 0, t.e);
           ++issued[stage];
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -418,28 +406,37 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int ch = lt & 7, r0 = lt >> 3;
     const uint32_t dst0 = (uint32_t)(2 * W_BYTES + r0 * 128 + ((ch ^ (r0 & 7)) << 4));
     constexpr int STEP = kLoaders / 8, RI = NMAX / STEP;
-    static_assert(STEP % 8 == 0, "the swizzle of a thread's rows");
+    static_assert(STEP % 8 == 0 && RI <= 32, "the swizzle and the masks of a thread's rows");
     // the token rows are read again by every output tile of their expert:
     // kept in L2 ahead of the weight stream
     uint64_t keep;
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    const uint8_t* a = p.a + ch * 16;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
       const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
       if (t.nv == 0) continue;
-      int src[RI];
+      // The rows' offsets in 128-byte blocks.  Rows of the MMA's padding are not
+      // copied (their columns are never read); a row with a bad map entry is
+      // zeroed.
+      uint32_t at[RI], mine = 0, good = 0;
 #pragma unroll
-      for (int i = 0; i < RI; ++i) src[i] = STEP * i < t.N ? source_row(p, t, r0 + STEP * i) : -1;
+      for (int i = 0; i < RI; ++i) {
+        const int r = r0 + STEP * i, m = source_row(p, t, r);
+        if (r < t.nv) mine |= 1u << i;
+        if (m >= 0) good |= 1u << i;
+        at[i] = (uint32_t)max(m, 0) * (uint32_t)nkb;
+      }
       for (int kb = 0; kb < nkb; ++kb) {
         if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
         const uint32_t dst = su32(smem + (size_t)stage * C::STAGE_BYTES) + dst0;
-        const uint8_t* a = p.a + kb * BK + ch * 16;
 #pragma unroll
         for (int i = 0; i < RI; ++i)
-          if (STEP * i < t.N)
-            cp_async16(dst + i * STEP * 128, a + (size_t)max(src[i], 0) * p.Kp, src[i] >= 0, keep);
+          if (mine & (1u << i))
+            cp_async16(dst + i * STEP * 128, a + ((uint64_t)(at[i] + (uint32_t)kb) << 7),
+                       (good & (1u << i)) != 0, keep);
         // arrives on the stage's full barrier once this thread's copies land
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                          su32(&sh->full[stage]))
@@ -450,54 +447,61 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight at exit
   } else if (warp < kEpiWarp0) {
     // ------------------------------------------------ scales
-    // Rows 0..255 of the buffer are the two halves' weight rows, the others the
-    // tokens; a row holds SG stages' words.  Copying, four lanes share a row
-    // and eight rows go at once (a row's scales need not be 16-byte aligned);
-    // reading back, lane l takes rows l, 32 + l, ...: the TMEM cells of its lane.
+    // Rows 0..255 of a buffer are the two halves' weight rows, the others the
+    // tokens; one aligned 16-byte chunk each.  A row's scales start `skew` words
+    // into its first chunk (its pitch need not be a multiple of 16 bytes), so a
+    // group of SG stages' words lies in chunk g, or in chunks g and g + 1.
+    // Reading back, lane l takes rows l, 32 + l, ...: the TMEM cells of its lane.
     const int st = threadIdx.x - kScaleWarp0 * 32, quad = warp & 3;
-    constexpr int ROWS = 256 + C::SFB * 32, PER = ROWS / 32;  // rows; rows a copying thread
-    const int sp = p.Kp / 32;  // scale bytes of a row
-    const int word = st & 3, rw0 = st >> 2;
-    const uint32_t sf_dst = su32(sf) + (uint32_t)(rw0 * 16 + word * 4);
+    constexpr int PER = 2 + (NMAX + 127) / 128;  // rows a copying thread
+    const int sp = p.Kp / 32;                    // scale bytes of a row
+    const bool skewed = (sp & 15) != 0;
+    const uint32_t sf_dst = su32(sf) + (uint32_t)(st * 16);
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + C::kSf0;
-    const int ngr = (nkb + SG - 1) / SG;
-    // The copies run SBUFS groups ahead of the stores (one group is four
-    // stages, about 2800 cycles at HBM speed; a load under that load can take
-    // longer): (ltile, lg) is the next group to copy, into buffer lbuf, src its
-    // rows' scales (null: zeros).
+    const int ngr = (nkb + SG - 1) / SG, nch = ngr + (skewed ? 1 : 0);
+    // weight row of tile row r (0..255) inside its expert, or -1 past the end
+    auto weight_row = [&](int ft, int r) {
+      const int f = GATED ? ft * 128 + (r & 127) : ft * 256 + r;
+      if (f >= p.Nout) return -1;
+      return GATED ? f * p.row_step + (r >> 7) * p.half_step : f;
+    };
+    // Copies run SBUFS chunks ahead of the reads: chunk lc of tile ltile is
+    // next, into buffer lbuf; src and left are its rows' next chunk and bytes.
     const uint8_t* src[PER];
-    int ltile = blockIdx.x, lg = 0, lbuf = 0, buf = 0;
+    int left[PER];
+    int ltile = blockIdx.x, lc = 0, lbuf = 0, buf = 0;
     auto seek = [&]() {  // rows of the first tile at or after ltile that has any
       for (; ltile < total; ltile += gridDim.x) {
         const MxTile t = mx_decode<NMAX>(ltile, sh->prefix, p.seg_end, p.E, p.M);
         if (t.nv == 0) continue;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const int r = rw0 + 32 * i;
-          if (i < 8) {  // weight row of half i / 4
-            const int h = i >> 2;
-            const int f = GATED ? t.ft * 128 + (r & 127) : t.ft * 256 + r;
-            const int row = GATED ? f * p.row_step + h * p.half_step : f;
-            src[i] = f < p.Nout ? p.w_scale + ((size_t)t.e * p.N1 + row) * sp : nullptr;
-          } else {
-            const int m = source_row(p, t, r - 256);
-            src[i] = m >= 0 ? p.a_scale + (size_t)m * sp : nullptr;
-          }
+          const int row = i < 2 ? weight_row(t.ft, st + 128 * i) : source_row(p, t, st + 128 * (i - 2));
+          const size_t at = ((i < 2 ? (size_t)t.e * p.N1 : 0) + max(row, 0)) * sp;
+          src[i] = (i < 2 ? p.w_scale : p.a_scale) + (at & ~size_t(15));
+          left[i] = row >= 0 ? sp + (int)(at & 15) : 0;
         }
         return;
       }
     };
-    auto copy_group = [&]() {
+    auto copy_chunk = [&]() {
       if (ltile < total) {
-        const int kb = lg * SG + word;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const bool v = src[i] != nullptr && kb < nkb;
-          cp_async4(sf_dst + lbuf * C::SF_BYTES + i * 32 * 16, v ? src[i] + kb * 4 : p.w_scale, v);
+          if (i < 2 || st + 128 * (i - 2) < NMAX) {
+            // no byte past the row's own scales is read
+            const int n = min(16, max(left[i], 0));
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             sf_dst + lbuf * C::SF_BYTES + i * 2048),
+                         "l"(n ? src[i] : p.w_scale), "r"(n)
+                         : "memory");
+            src[i] += 16;
+            left[i] -= 16;
+          }
         }
         if (++lbuf == SBUFS) lbuf = 0;
-        if (++lg == ngr) {
-          lg = 0;
+        if (++lc == nch) {
+          lc = 0;
           ltile += gridDim.x;
           seek();
         }
@@ -505,30 +509,52 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     seek();
-    for (int i = 0; i < SBUFS; ++i) copy_group();
+    for (int i = 0; i < SBUFS; ++i) copy_chunk();
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
       const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
       if (t.nv == 0) continue;
+      // where the rows of this lane's cells start in their chunks
+      uint32_t skew[8 + C::SFB];
+#pragma unroll
+      for (int c = 0; c < 8 + C::SFB; ++c) {
+        const int r = c * 32 + lane;
+        const int row = c < 8 ? weight_row(t.ft, r) : source_row(p, t, r - 256);
+        skew[c] = skewed ? (uint32_t)((((c < 8 ? (size_t)t.e * p.N1 : 0) + max(row, 0)) * sp) & 15) >> 2 : 0u;
+      }
       for (int gr = 0; gr < ngr && ok; ++gr) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(SBUFS - 1) : "memory");
+        // chunk g, and g + 1 when rows are skewed, landed
+        asm volatile("cp.async.wait_group %0;" ::"n"(SBUFS - 2) : "memory");
         named_sync(kScaleBar, 128);
+        const int buf1 = buf + 1 == SBUFS ? 0 : buf + 1;
         uint32_t w[SG][8], b[SG][C::SFB_ST];
 #pragma unroll
         for (int c = 0; c < 8 + C::SFB_ST; ++c) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (c < 8 + C::SFB) v = *reinterpret_cast<const uint4*>(sf + buf * C::SF_BYTES + (c * 32 + lane) * 16);
+          if (c < 8 + C::SFB && c * 32 + lane < 256 + NMAX) {
+            v = *reinterpret_cast<const uint4*>(sf + buf * C::SF_BYTES + (c * 32 + lane) * 16);
+            if (skewed) {  // words skew .. skew + 3 of the two chunks
+              const uint4 n = *reinterpret_cast<const uint4*>(sf + buf1 * C::SF_BYTES + (c * 32 + lane) * 16);
+              const uint32_t k = skew[c < 8 + C::SFB ? c : 0];
+              if (k & 1) v = make_uint4(v.y, v.z, v.w, n.x);
+              if (k & 2) v = (k & 1) ? make_uint4(v.z, v.w, n.y, n.z) : make_uint4(v.z, v.w, n.x, n.y);
+            }
+          }
           if (c < 8) {
             w[0][c] = v.x; w[1][c] = v.y; w[2][c] = v.z; w[3][c] = v.w;
           } else {
             b[0][c - 8] = v.x; b[1][c - 8] = v.y; b[2][c - 8] = v.z; b[3][c - 8] = v.w;
           }
         }
-        named_sync(kScaleBar, 128);  // read by all four warps: the buffer is free
-        copy_group();
-        if (++buf == SBUFS) buf = 0;
+        named_sync(kScaleBar, 128);  // read by all four warps: chunk g is free
+        copy_chunk();
+        buf = buf1;
+        if (skewed && gr == ngr - 1) {  // and so is the tile's last chunk
+          copy_chunk();
+          if (++buf == SBUFS) buf = 0;
+        }
 #pragma unroll
         for (int j = 0; j < SG; ++j) {
           if (gr * SG + j < nkb && ok) {
@@ -701,7 +727,7 @@ cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const
   const cuuint64_t row = (cuuint64_t)p.Kp / 2;
   const cuuint64_t dims[4] = {(cuuint64_t)p.Kp, (cuuint64_t)Nout, gate ? 2u : 1u, (cuuint64_t)E};
   const cuuint64_t str[3] = {row * p.row_step, gate ? row * p.half_step : row * Nout, row * p.N1};
-  const cuuint32_t box[4] = {BK, 128, 1, 1};
+  const cuuint32_t box[4] = {BK, gate ? 128u : 256u, gate ? 2u : 1u, 1};  // both halves
   if (!tmap::encode_u4_expanded(&tm, w, 4, dims, str, box)) return cudaErrorInvalidValue;
   const int kind = act ? act->kind : MOE_ACT_IDENTITY;
   const long long avg = ((long long)M + std::min(M, E) - 1) / std::min(M, E);

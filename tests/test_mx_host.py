@@ -116,8 +116,8 @@ def test_gemm_mx_refuses(moe):
                dict(out=None), dict(a=None), dict(asc=None), dict(M=1 << 30, rows=1 << 30),
                dict(act=moe.act_params(9)), dict(act=moe.act_params(1, swiglu_fusion=0))):
         assert g(**kw) == inv, kw
-    for kw in (dict(dt=moe.MOE_F32), dict(a=A(0, 8)), dict(asc=A(1, 2)), dict(w=A(2, 16)),
-               dict(wsc=A(3, 2)), dict(out=A(5, 1)), dict(out=A(5, 8), osc=A(7)),
+    for kw in (dict(dt=moe.MOE_F32), dict(a=A(0, 8)), dict(asc=A(1, 4)), dict(w=A(2, 16)),
+               dict(wsc=A(3, 8)), dict(out=A(5, 1)), dict(out=A(5, 8), osc=A(7)),
                dict(osc=A(7, 8))):
         assert g(**kw) == uns, kw
     assert g(ws=None) == moe.MOE_ERR_WORKSPACE and g(wsb=255) == moe.MOE_ERR_WORKSPACE
@@ -146,8 +146,8 @@ def test_layer_mx_refuses(moe):
                dict(act=moe.act_params(1, swiglu_fusion=0)),
                dict(p=moe.route_params(2, local_expert_count=4))):
         assert f(**kw) == inv, kw
-    for kw in (dict(dt=moe.MOE_F32), dict(h=A(0, 4)), dict(hs=A(1, 2)), dict(w1=A(3, 16)),
-               dict(w2=A(5, 16)), dict(s1=A(4, 1)), dict(s2=A(6, 2)), dict(out=A(7, 1))):
+    for kw in (dict(dt=moe.MOE_F32), dict(h=A(0, 4)), dict(hs=A(1, 8)), dict(w1=A(3, 16)),
+               dict(w2=A(5, 16)), dict(s1=A(4, 4)), dict(s2=A(6, 8)), dict(out=A(7, 1))):
         assert f(**kw) == uns, kw
     assert f(wsb=need - 1) == moe.MOE_ERR_WORKSPACE and f(ws=None) == moe.MOE_ERR_WORKSPACE
     for kw in (dict(out=A(0)), dict(out=A(8)), dict(ws=A(3)), dict(ti=A(2)), dict(tw=A(7))):
