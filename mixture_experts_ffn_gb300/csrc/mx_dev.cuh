@@ -49,9 +49,17 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7fc00000u : byte << 23);
 }
 
-// a zero inverse scale marks a block with a non-finite value: 0 * inf is NaN,
-// so its values are replaced before the conversion
+// A zero inverse scale marks a block with a non-finite value: 0 * inf is NaN,
+// so its values are replaced before the conversion.
 __device__ __forceinline__ float scaled(float v, float inv) { return inv == 0.0f ? 0.0f : v * inv; }
+__device__ __forceinline__ void scale8(float (&v)[8], float inv) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= inv;
+  if (inv == 0.0f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  }
+}
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);

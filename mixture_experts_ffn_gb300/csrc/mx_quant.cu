@@ -13,37 +13,74 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// item i of the grid: columns 8 (i % ipr) .. of row i / ipr, ipr = Kp / 8 (a
-// multiple of 16, so a block's four lanes never straddle two rows)
+// Item i: columns 8 (i % ipr) .. of row i / ipr, ipr = Kp / 8 (a multiple of
+// 16, so a block's four lanes never straddle two rows).  A thread's next item
+// is a grid's width on: row and column advance by fixed amounts, so the loop
+// divides nothing (the division was a fifth of its instructions, and the
+// kernel issues nearly as long as it waits for HBM).
+struct Walk {
+  uint32_t i, row, col, ipr, step, drow, dcol;
+  __device__ __forceinline__ explicit Walk(uint32_t ipr_) {
+    ipr = ipr_;
+    i = blockIdx.x * kThreads + threadIdx.x;
+    step = gridDim.x * kThreads;
+    row = i / ipr;
+    col = i - row * ipr;
+    drow = step / ipr;
+    dcol = step - drow * ipr;
+  }
+  __device__ __forceinline__ void next() {
+    i += step;
+    row += drow;
+    col += dcol;
+    if (col >= ipr) {
+      col -= ipr;
+      ++row;
+    }
+  }
+};
+
+// Largest magnitude of a 16-byte vector of bfloat16, as float bits: the bits
+// of a magnitude order as the magnitudes do, two at a time.
+__device__ __forceinline__ uint32_t amax_bf16x8(const uint4& u) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
+  return max(a & 0xffff0000u, a << 16);
+}
+
 template <typename T, bool E2M1, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     mx_quantize_kernel(const T* __restrict__ x, int64_t stride, uint32_t items, int K, int Kp,
                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   pdl_wait();
-  const uint32_t ipr = (uint32_t)Kp / 8;
-  const uint32_t step = gridDim.x * kThreads;
   // the lanes of a warp leave the loop together: items is a multiple of 16
   // and a block is four lanes, so a shuffle's partners are in or out as one
-  for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < items; i += step) {
-    const uint32_t row = i / ipr;
-    const int c0 = (int)(i - row * ipr) * 8;
+  const uint32_t mask = 0xfu << (threadIdx.x & 28);
+  for (Walk w((uint32_t)Kp / 8); w.i < items; w.next()) {
+    const T* xr = x + (int64_t)w.row * stride;
+    const int c0 = (int)w.col * 8;
     float v[8];
-    mx::load8<T, VEC>(x + (int64_t)row * stride, c0, K, v);
     uint32_t amax = 0;
+    if constexpr (VEC && std::is_same<T, __nv_bfloat16>::value) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (c0 < K) u = __ldcs(reinterpret_cast<const uint4*>(xr + c0));
+      amax = amax_bf16x8(u);
+      v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+      v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
+    } else {
+      mx::load8<T, VEC>(xr, c0, K, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, mx::abs_bits(v[j]));
-    const uint32_t mask = 0xfu << (threadIdx.x & 28);
+      for (int j = 0; j < 8; ++j) amax = max(amax, mx::abs_bits(v[j]));
+    }
     amax = max(amax, __shfl_xor_sync(mask, amax, 1));
     amax = max(amax, __shfl_xor_sync(mask, amax, 2));
     const uint32_t byte = mx::scale_byte<E2M1>(amax);
-    const float inv = mx::inv_scale(byte);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = mx::scaled(v[j], inv);
+    mx::scale8(v, mx::inv_scale(byte));
     if constexpr (E2M1)
-      reinterpret_cast<uint32_t*>(codes)[i] = mx::e2m1x8(v);
+      reinterpret_cast<uint32_t*>(codes)[w.i] = mx::e2m1x8(v);
     else
-      reinterpret_cast<uint2*>(codes)[i] = mx::e4m3x8(v);
-    if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+      reinterpret_cast<uint2*>(codes)[w.i] = mx::e4m3x8(v);
+    if ((threadIdx.x & 3) == 0) scales[w.i >> 2] = (uint8_t)byte;
   }
 }
 
@@ -52,36 +89,29 @@ __global__ void __launch_bounds__(kThreads)
     mx_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                          uint32_t items, int K, int Kp, T* __restrict__ out) {
   pdl_wait();
-  const uint32_t ipr = (uint32_t)Kp / 8;
-  const uint32_t step = gridDim.x * kThreads;
-  for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < items; i += step) {
-    const uint32_t row = i / ipr;
-    const int c0 = (int)(i - row * ipr) * 8;
+  for (Walk w((uint32_t)Kp / 8); w.i < items; w.next()) {
+    const int c0 = (int)w.col * 8;
     if (c0 >= K) continue;
-    const float s = mx::scale_value(scales[i >> 2]);
+    const float s = mx::scale_value(scales[w.i >> 2]);
+    uint2 q;
+    if constexpr (E2M1)
+      q.x = reinterpret_cast<const uint32_t*>(codes)[w.i];
+    else
+      q = reinterpret_cast<const uint2*>(codes)[w.i];
     float v[8];
-    if constexpr (E2M1) {
-      const uint32_t q = reinterpret_cast<const uint32_t*>(codes)[i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2 h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(q >> (8 * j)), __NV_E2M1);
-        const float2 f = __half22float2(h);
-        v[2 * j] = f.x * s;
-        v[2 * j + 1] = f.y * s;
-      }
-    } else {
-      const uint2 q = reinterpret_cast<const uint2*>(codes)[i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w = j < 2 ? q.x : q.y;
-        const __half2 h = __nv_cvt_fp8x2_to_halfraw2(
-            (__nv_fp8x2_storage_t)(w >> (16 * (j & 1))), __NV_E4M3);
-        const float2 f = __half22float2(h);
-        v[2 * j] = f.x * s;
-        v[2 * j + 1] = f.y * s;
-      }
+    for (int j = 0; j < 4; ++j) {
+      __half2 h;
+      if constexpr (E2M1)
+        h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(q.x >> (8 * j)), __NV_E2M1);
+      else
+        h = __nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)((j < 2 ? q.x : q.y) >> (16 * (j & 1))), __NV_E4M3);
+      const float2 f = __half22float2(h);
+      v[2 * j] = f.x * s;
+      v[2 * j + 1] = f.y * s;
     }
-    mx::store8<T, VEC>(out + (int64_t)row * K, c0, K, v);
+    mx::store8<T, VEC>(out + (int64_t)w.row * K, c0, K, v);
   }
 }
 

@@ -96,9 +96,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024)
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       if constexpr (QUANT == kQuantMx) {
         const uint32_t byte = mx::scale_byte<false>(amax);
-        const float inv = mx::inv_scale(byte);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = mx::scaled(v[i][j], inv);
+        mx::scale8(v[i], mx::inv_scale(byte));
         if (c0 < p.Hp && (lane & 3) == 0)
           static_cast<uint8_t*>(p.scales)[(size_t)row * (p.Hp / 32) + (item >> 2)] = (uint8_t)byte;
       } else {
@@ -107,8 +105,9 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024)
         // a block with an infinity or a NaN: NaN scale, zero codes
         const bool bad = amax >= mx::kInfBits;
         const float s = fmaxf(__uint_as_float(amax) / 448.0f, 1.17549435e-38f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = bad ? 0.0f : v[i][j] / s;
+        // one quotient a block instead of one a value: a code's argument is
+        // then within 2 ulp of y / s
+        mx::scale8(v[i], bad ? 0.0f : 1.0f / s);
         if (c0 < p.Hp && (lane & 15) == 0)
           static_cast<float*>(p.scales)[(size_t)row * (p.Hp / 128) + (item >> 4)] =
               bad ? __uint_as_float(0x7fc00000u) : s;

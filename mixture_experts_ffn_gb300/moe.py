@@ -146,6 +146,16 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    """Handle of the current stream of t's device (an integer; a tenth of the
+    time that building a Stream object takes, which counts for calls of a few
+    microseconds)."""
+    return _raw_stream(t.device.index)
+
+
 def _dt(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return MOE_BF16
@@ -543,17 +553,17 @@ def moe_mx_quantize(x, format: int = MOE_MX_E4M3, codes=None, scales=None):
         raise ValueError("moe_mx_quantize takes contiguous rows")
     Kp = moe_mx_columns(K)
     rows = x.numel() // K if K else 0
+    lead = x.shape[:-1]
     if codes is None:
-        codes = (torch.empty((*x.shape[:-1], Kp // 2), dtype=torch.uint8, device=x.device)
+        codes = (torch.empty((*lead, Kp // 2), dtype=torch.uint8, device=x.device)
                  if format == MOE_MX_E2M1 else
-                 torch.empty((*x.shape[:-1], Kp), dtype=torch.float8_e4m3fn, device=x.device))
+                 torch.empty((*lead, Kp), dtype=torch.float8_e4m3fn, device=x.device))
     if scales is None:
-        scales = torch.empty((*x.shape[:-1], Kp // 32), dtype=torch.float8_e8m0fnu,
-                             device=x.device)
+        scales = torch.empty((*lead, Kp // 32), dtype=torch.float8_e8m0fnu, device=x.device)
     _cuda(codes, scales)
     _check("moe_mx_quantize",
            lib.moe_mx_quantize(x.data_ptr(), rows, K, stride, _dt(x), format, codes.data_ptr(),
-                               scales.data_ptr(), _stream()))
+                               scales.data_ptr(), _stream_of(x)))
     return codes, scales
 
 
@@ -572,7 +582,7 @@ def moe_mx_dequantize(codes, scales, K: int, format=None, dtype=torch.bfloat16, 
         out = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
     _check("moe_mx_dequantize",
            lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), scales.numel() // (Kp // 32),
-                                 K, format, _dt(out), out.data_ptr(), _stream()))
+                                 K, format, _dt(out), out.data_ptr(), _stream_of(codes)))
     return out
 
 
@@ -610,7 +620,7 @@ def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_
                                 None if residual_out is None else residual_out.data_ptr(),
                                 None if out is None else out.data_ptr(),
                                 None if codes is None else codes.data_ptr(),
-                                None if scales is None else scales.data_ptr(), _stream()))
+                                None if scales is None else scales.data_ptr(), _stream_of(x)))
     return {"residual": residual_out, "out": out, "codes": codes, "scales": scales}
 
 
@@ -655,7 +665,7 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
                                    top_k, w.data_ptr(), w_scale.data_ptr(), _p(bias),
                                    seg_end.data_ptr(), M, N, Kp, E, dt,
                                    None if act is None else ctypes.byref(act), out.data_ptr(),
-                                   _p(out_scale), ws.data_ptr(), ws.numel(), _stream()))
+                                   _p(out_scale), ws.data_ptr(), ws.numel(), _stream_of(a)))
     return (out, out_scale) if mx_out else out
 
 
@@ -696,7 +706,7 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
                                   _p(expert_ids), _p(b_gate_up), _p(b_down), T, H, F, E, _dt(out),
                                   ctypes.byref(_rp(p, logits)), ctypes.byref(act), out.data_ptr(),
                                   _p(topk_weights_out), _p(topk_ids_out), ws.data_ptr(),
-                                  ws.numel(), _stream()))
+                                  ws.numel(), _stream_of(hidden)))
     return out
 
 
