@@ -26,7 +26,10 @@
 //                   row_to_route when given)
 //   warps 4..7    : both operands' scales, four stages at a time through shared
 //                   memory into registers, then tcgen05.st into TMEM, each warp
-//                   its own lane quarter (the MMA wants them in all four).
+//                   its own lane quarter (the MMA wants them in all four).  They
+//                   have a ring of their own, of two or four stages a slot: tied
+//                   to the operands' ring, a stage at a time, these warps set
+//                   the pace (585 cycles a stage).
 //                   tcgen05.cp would need no warps, but runs in the MMAs' own
 //                   pipe and costs it 170 cycles a stage.
 //   warps 8..15   : epilogue, two warps a lane quarter
@@ -55,7 +58,7 @@ constexpr int W_BYTES = 128 * BK;          // one half's weights, expanded: 16 K
 constexpr int W_TX = W_BYTES / 2;          // bytes its copy counts: the packed ones (the gaps of
                                            // the expanded form are not written)
 constexpr int SG = 4;                      // stages whose scales travel together
-constexpr int SBUFS = 4;                   // chunks of scales in flight or in use
+constexpr int SBUFS = 3;                   // chunks of scales in flight or in use
 constexpr int kLoadWarp0 = 2, kScaleWarp0 = 4, kEpiWarp0 = 8, kEpiWarps = 8;
 constexpr int kLoaders = 32 * (kScaleWarp0 - kLoadWarp0);
 constexpr int NUM_THREADS = 32 * (kEpiWarp0 + kEpiWarps);
@@ -70,27 +73,36 @@ struct Cfg {
   static constexpr int B_BYTES = NMAX * BK;
   static constexpr int STAGE_BYTES = 2 * W_BYTES + B_BYTES;
   static constexpr int SF_BYTES = (256 + NMAX) * 4 * SG;  // a chunk of every row's scales
-  static constexpr int kFixed = 6 * 1024 - 512 + SBUFS * SF_BYTES;  // scales, barriers, prefix
+  // scales, barriers, tile prefix and segment starts, alignment
+  static constexpr int kFixed = SBUFS * SF_BYTES + 10 * 1024;
   static constexpr int STAGES = (int)((kSmemLimit - kFixed) / STAGE_BYTES);
   static constexpr int SFB = (NMAX + 31) / 32;  // TMEM columns of the tokens' scales
   static constexpr int SFB_ST = SFB > 4 ? 8 : SFB > 2 ? 4 : SFB;  // ... as one store writes them
   static constexpr int SF_COLS = 8 + (SFB_ST + 3) / 4 * 4;  // TMEM columns of a stage's scales
   static constexpr int ACC_COLS = 2 * NMAX;
   static constexpr int kSf0 = kAccs * ACC_COLS;
-  static_assert(kSf0 + STAGES * SF_COLS <= 512, "TMEM columns");
+  // Scales wait in TMEM in slots of TG stages, a ring of their own: as many
+  // slots as the accumulators leave room for.
+  static constexpr int TG = 512 - kSf0 >= 2 * 4 * SF_COLS ? 4 : 2;
+  static constexpr int kFit = (512 - kSf0) / (TG * SF_COLS);
+  static constexpr int SLOTS = kFit > 4 ? 4 : kFit;
+  static_assert(SLOTS >= 2, "TMEM columns");
   static_assert(NMAX % 16 == 0 && NMAX <= 256, "N");
 };
 
-template <int STAGES>
+template <int STAGES, int SLOTS>
 struct MxShared {
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
+  uint64_t sfull[SLOTS];   // a slot's scales are in TMEM
+  uint64_t sempty[SLOTS];  // ... and its last MMAs have read them
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
   int prefix[kMaxExperts + 1];
+  int start[kMaxExperts + 1];  // first row of every expert
   int scan_tmp[33];
 };
 
@@ -221,25 +233,22 @@ __device__ __forceinline__ bool named_and(int id, int threads, bool v) {
   return r != 0;
 }
 template <int NMAX>
-__device__ __forceinline__ MxTile mx_decode(int t, const int* prefix, const int32_t* seg_end, int E,
-                                            int M) {
+__device__ __forceinline__ MxTile mx_decode(int t, const int* prefix, const int* start, int E) {
   int lo = 0, hi = E - 1;
   while (lo < hi) {  // last e with prefix[e] <= t (skips empty experts)
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
   }
-  int s, u;
-  seg_bounds(seg_end, lo, M, 0, s, u);
-  const int n = u - s;
+  const int s = start[lo], n = start[lo + 1] - s;
   const int ce = (n + NMAX - 1) / NMAX;  // chunks of equal size, rounded up to 16
   const int local = t - prefix[lo];
   MxTile r;
   r.e = lo;
   r.ft = local / ce;
   const int per = (((n + ce - 1) / ce) + 15) & ~15;
-  const int start = min((local % ce) * per, n);
-  r.m0 = s + start;
-  r.nv = min(per, n - start);  // 0 for a chunk that rounding left empty
+  const int first = min((local % ce) * per, n);
+  r.m0 = s + first;
+  r.nv = min(per, n - first);  // 0 for a chunk that rounding left empty
   r.N = max(16, (r.nv + 15) & ~15);
   return r;
 }
@@ -298,15 +307,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sf = smem + (size_t)STAGES * C::STAGE_BYTES;
-  auto* sh = reinterpret_cast<MxShared<STAGES>*>(sf + SBUFS * C::SF_BYTES);
+  auto* sh = reinterpret_cast<MxShared<STAGES, C::SLOTS>*>(sf + SBUFS * C::SF_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh->abort;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      // the producer's expect-tx, every token loader thread, every scale warp
-      mbar_init(&sh->full[s], 1 + kLoaders + 4);
+      mbar_init(&sh->full[s], 1 + kLoaders);  // the producer's expect-tx, every loader thread
       mbar_init(&sh->empty[s], 1);
+    }
+    for (int s = 0; s < C::SLOTS; ++s) {
+      mbar_init(&sh->sfull[s], 4);  // every scale warp
+      mbar_init(&sh->sempty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sh->tfull[a], 1);
@@ -329,6 +341,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int n_ftiles = (p.Nout + FT - 1) / FT;
   const int nkb = p.Kp / BK;
   pdl_wait();
+  // every expert's rows start where the one before ends (never before it)
+  for (int e = threadIdx.x; e <= p.E; e += NUM_THREADS) {
+    int s0 = 0, u = 0;
+    if (e > 0) seg_bounds(p.seg_end, e - 1, p.M, 0, s0, u);
+    sh->start[e] = u;
+  }
   const int total = build_tile_prefix(p.seg_end, p.E, p.M, NMAX, n_ftiles, sh->prefix, sh->scan_tmp);
   tc_fence_before();
   __syncthreads();
@@ -338,55 +356,104 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------ TMA producer (weights)
-      int stage = 0;
+      // It also passes on the release of the scale slots: a stage's completion
+      // tells it, as it takes the stage again, that the slot whose last stage
+      // that was is free.  (A commit of the MMA warp's own for the slots, next
+      // to the one for the stage, stalls that warp until the MMAs are done.)
+      int stage = 0, slot = 0;
       uint32_t phase = 0;
       uint32_t issued[STAGES];
-      for (int s = 0; s < STAGES; ++s) issued[s] = 0;
+      int owner[STAGES];  // slot that the stage's last MMAs free, or -1
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s) {
+        issued[s] = 0;
+        owner[s] = -1;
+      }
       bool ok = true;
+      auto take = [&](int freed) {  // waits for the stage; freed: the slot it was to free
+        if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) return false;
+        if (freed >= 0) {
+          tc_fence_after();
+          tc_fence_before();
+          mbar_arrive(&sh->sempty[freed]);
+        }
+        return true;
+      };
+      auto get = [&](int s) {
+        int v = -1;
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i)
+          if (i == s) v = owner[i];
+        return v;
+      };
       for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+        const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
         if (t.nv == 0) continue;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+          if (!(ok = take(get(stage)))) break;
           uint8_t* dst = smem + (size_t)stage * C::STAGE_BYTES;
           mbar_expect_tx(&sh->full[stage], 2 * W_TX);
           // rows past the operand read as zeros and count in full
           tma_4d(dst, &tm_w, &sh->full[stage], kb * BK, t.ft * FT, 0, t.e);
-          ++issued[stage];
+          const bool last = kb % C::TG == C::TG - 1 || kb == nkb - 1;
+#pragma unroll
+          for (int i = 0; i < STAGES; ++i)
+            if (i == stage) {
+              ++issued[i];
+              owner[i] = last ? slot : -1;
+            }
+          if (last && ++slot == C::SLOTS) slot = 0;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
+      for (int i = 0; i < STAGES && ok; ++i) {  // the last stages' releases
+        ok = take(get(stage));
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
       if (!ok) {  // let every copy already in flight land before the block exits
+#pragma unroll
         for (int s = 0; s < STAGES; ++s)
           if (issued[s]) drain_wait(&sh->full[s], (issued[s] - 1u) & 1u);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer (whole warp)
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, aphase = 0;
+    int stage = 0, acc = 0, slot = 0;
+    uint32_t phase = 0, aphase = 0, sphase = 0;
     bool ok = true, any = false;
     const uint64_t ad0 = sw128_desc(su32(smem));
+    // warp reductions leave their result in a uniform register
+    const uint32_t tm0 = __reduce_max_sync(0xffffffffu, tmem);
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
       if (t.nv == 0) continue;
       ok = __all_sync(0xffffffffu, wait_fast(&sh->tempty[acc], aphase ^ 1u, abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)(acc * C::ACC_COLS);
-      const uint32_t idesc = idesc_mx(__shfl_sync(0xffffffffu, t.N, 0));
+      const uint32_t d = tm0 + (uint32_t)(acc * C::ACC_COLS);
+      const uint32_t idesc = idesc_mx((int)__reduce_max_sync(0xffffffffu, (uint32_t)t.N));
       for (int kb = 0; kb < nkb; ++kb) {
-        ok = __all_sync(0xffffffffu, wait_fast(&sh->full[stage], phase, abort_flag, p.status));
-        if (!ok) break;
+        // both barriers tried at once, the slow paths only when one is not there yet
+        const bool first = kb % C::TG == 0;
+        const bool f0 = mbar_try_wait(su32(&sh->full[stage]), phase);
+        const bool f1 = !first || mbar_try_wait(su32(&sh->sfull[slot]), sphase);
+        if (!__all_sync(0xffffffffu, f0 && f1)) {
+          ok = wait_bar(&sh->full[stage], phase, abort_flag, p.status);
+          if (first) ok = wait_bar(&sh->sfull[slot], sphase, abort_flag, p.status) && ok;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
         // the loaders wrote through the generic proxy; tcgen05 reads through
         // the async proxy
         fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t ad = ad0 + (uint64_t)((stage * C::STAGE_BYTES) >> 4);
         mma_stage(d, d + NMAX, ad, ad + (2 * W_BYTES >> 4), idesc,
-                  tmem + (uint32_t)(C::kSf0 + stage * C::SF_COLS), kb != 0 ? 1u : 0u,
-                  su32(&sh->empty[stage]));
+                  tm0 + (uint32_t)(C::kSf0 + (slot * C::TG + kb % C::TG) * C::SF_COLS),
+                  kb != 0 ? 1u : 0u, su32(&sh->empty[stage]));
         any = true;
+        if (kb % C::TG == C::TG - 1 || kb == nkb - 1)
+          if (++slot == C::SLOTS) { slot = 0; sphase ^= 1u; }
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
       if (!ok) break;
@@ -416,7 +483,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
       if (t.nv == 0) continue;
       // The rows' offsets in 128-byte blocks.  Rows of the MMA's padding are not
       // copied (their columns are never read); a row with a bad map entry is
@@ -472,7 +539,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int ltile = blockIdx.x, lc = 0, lbuf = 0, buf = 0;
     auto seek = [&]() {  // rows of the first tile at or after ltile that has any
       for (; ltile < total; ltile += gridDim.x) {
-        const MxTile t = mx_decode<NMAX>(ltile, sh->prefix, p.seg_end, p.E, p.M);
+        const MxTile t = mx_decode<NMAX>(ltile, sh->prefix, sh->start, p.E);
         if (t.nv == 0) continue;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -510,11 +577,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     };
     seek();
     for (int i = 0; i < SBUFS; ++i) copy_chunk();
-    int stage = 0;
-    uint32_t phase = 0;
+    int slot = 0;
+    uint32_t sphase = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
       if (t.nv == 0) continue;
       // where the rows of this lane's cells start in their chunks
       uint32_t skew[8 + C::SFB];
@@ -538,8 +605,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (skewed) {  // words skew .. skew + 3 of the two chunks
               const uint4 n = *reinterpret_cast<const uint4*>(sf + buf1 * C::SF_BYTES + (c * 32 + lane) * 16);
               const uint32_t k = skew[c < 8 + C::SFB ? c : 0];
-              if (k & 1) v = make_uint4(v.y, v.z, v.w, n.x);
-              if (k & 2) v = (k & 1) ? make_uint4(v.z, v.w, n.y, n.z) : make_uint4(v.z, v.w, n.x, n.y);
+              const bool one = (k & 1) != 0, two = (k & 2) != 0;
+              const uint32_t x0 = one ? v.y : v.x, x1 = one ? v.z : v.y, x2 = one ? v.w : v.z,
+                             x3 = one ? n.x : v.w, x4 = one ? n.y : n.x, x5 = one ? n.z : n.y;
+              v = make_uint4(two ? x2 : x0, two ? x3 : x1, two ? x4 : x2, two ? x5 : x3);
             }
           }
           if (c < 8) {
@@ -556,21 +625,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (++buf == SBUFS) buf = 0;
         }
 #pragma unroll
-        for (int j = 0; j < SG; ++j) {
-          if (gr * SG + j < nkb && ok) {
-            // the stage's TMEM columns are free once its last MMAs completed
-            ok = wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status);
+        for (int j0 = 0; j0 < SG; j0 += C::TG) {
+          if (gr * SG + j0 < nkb && ok) {
+            // the slot's TMEM columns are free once its last MMAs completed
+            ok = wait_fast(&sh->sempty[slot], sphase ^ 1u, abort_flag, p.status);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
               tc_fence_after();
-              const uint32_t d = taddr + (uint32_t)(stage * C::SF_COLS);
-              tmem_st<8>(d, w[j]);
-              tmem_st<C::SFB_ST>(d + 8, b[j]);
+              const uint32_t d = taddr + (uint32_t)(slot * C::TG * C::SF_COLS);
+#pragma unroll
+              for (int j = 0; j < C::TG; ++j) {  // stages past the last: unread
+                tmem_st<8>(d + j * C::SF_COLS, w[j0 + j]);
+                tmem_st<C::SFB_ST>(d + j * C::SF_COLS + 8, b[j0 + j]);
+              }
               asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&sh->full[stage]);
-              if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+              if (lane == 0) mbar_arrive(&sh->sfull[slot]);
+              if (++slot == C::SLOTS) { slot = 0; sphase ^= 1u; }
             }
           }
         }
@@ -587,7 +659,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int acc = 0;
     uint32_t aphase = 0;
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, p.seg_end, p.E, p.M);
+      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
       if (t.nv == 0) continue;
       // the lane's biases, loaded before the accumulator is ready
       float b[2] = {0.0f, 0.0f};
@@ -651,7 +723,7 @@ template <int NMAX, bool GATED, int ACT, bool MXOUT, bool F16>
 cudaError_t go(const CUtensorMap& tm, const MxArgs& p, cudaStream_t s) {
   using C = Cfg<NMAX>;
   constexpr size_t smem = (size_t)C::STAGES * C::STAGE_BYTES + SBUFS * C::SF_BYTES +
-                          sizeof(MxShared<C::STAGES>) + 1024;
+                          sizeof(MxShared<C::STAGES, C::SLOTS>) + 1024;
   static_assert(smem <= kSmemLimit, "shared memory");
   auto kern = gemm_mx_kernel<NMAX, GATED, ACT, MXOUT, F16>;
   cudaError_t e = set_smem_limit((const void*)kern, (int)smem);
@@ -732,8 +804,8 @@ cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const
   const int kind = act ? act->kind : MOE_ACT_IDENTITY;
   const long long avg = ((long long)M + std::min(M, E) - 1) / std::min(M, E);
   if (avg <= 8) return go_act<16>(tm, p, kind, out_scale != nullptr, f16, s);
-  if (avg <= 80) return go_act<112>(tm, p, kind, out_scale != nullptr, f16, s);
-  return go_act<224>(tm, p, kind, out_scale != nullptr, f16, s);
+  if (avg <= 80) return go_act<96>(tm, p, kind, out_scale != nullptr, f16, s);
+  return go_act<208>(tm, p, kind, out_scale != nullptr, f16, s);
 }
 
 }  // namespace moe
