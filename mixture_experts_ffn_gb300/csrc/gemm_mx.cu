@@ -66,20 +66,22 @@ constexpr int kScaleBar = 1;               // named barrier of the scale warps
 constexpr size_t kSmemLimit = 227 * 1024;
 
 // Token columns of a tile and what follows from them: ring depth and TMEM.
-template <int NMAX_>
+// HALVES: 128-row halves of weights a tile holds.
+template <int NMAX_, int HALVES>
 struct Cfg {
   static constexpr int NMAX = NMAX_;
   static constexpr int kAccs = NMAX <= 112 ? 2 : 1;  // accumulators (512 TMEM columns in all)
   static constexpr int B_BYTES = NMAX * BK;
-  static constexpr int STAGE_BYTES = 2 * W_BYTES + B_BYTES;
-  static constexpr int SF_BYTES = (256 + NMAX) * 4 * SG;  // a chunk of every row's scales
+  static constexpr int STAGE_BYTES = HALVES * W_BYTES + B_BYTES;
+  static constexpr int SF_BYTES = (128 * HALVES + NMAX) * 4 * SG;  // a chunk of every row's scales
   // scales, barriers, tile prefix and segment starts, alignment
   static constexpr int kFixed = SBUFS * SF_BYTES + 10 * 1024;
   static constexpr int STAGES = (int)((kSmemLimit - kFixed) / STAGE_BYTES);
   static constexpr int SFB = (NMAX + 31) / 32;  // TMEM columns of the tokens' scales
   static constexpr int SFB_ST = SFB > 4 ? 8 : SFB > 2 ? 4 : SFB;  // ... as one store writes them
-  static constexpr int SF_COLS = 8 + (SFB_ST + 3) / 4 * 4;  // TMEM columns of a stage's scales
-  static constexpr int ACC_COLS = 2 * NMAX;
+  static constexpr int SFA = 4 * HALVES;        // ... of the weights' scales, in front of them
+  static constexpr int SF_COLS = SFA + (SFB_ST + 3) / 4 * 4;  // TMEM columns of a stage's scales
+  static constexpr int ACC_COLS = HALVES * NMAX;
   static constexpr int kSf0 = kAccs * ACC_COLS;
   // Scales wait in TMEM in slots of TG stages, a ring of their own: as many
   // slots as the accumulators leave room for.
@@ -118,6 +120,7 @@ struct MxArgs {
   int* status;
   int M, Nout, N1, Kp, E, a_rows, gdiv;
   int row_step, half_step;  // weight row of output f, half h: f * row_step + h * half_step
+  int f16;                  // bias and 16-bit output: float16, else bfloat16
   float limit, alpha, beta;
 };
 
@@ -142,7 +145,7 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
-// The eight MMAs of a stage (four K32 steps of both halves; half 1's weights
+// The MMAs of a stage (four K32 steps of each half; half 1's weights
 // 16 KB on, its accumulator in d1) and the commit that frees the stage, issued
 // by one elected lane of a CONVERGED warp.  All operands are warp-uniform, so
 // they stay in uniform registers: the stage then takes max(313, 4 N) cycles,
@@ -152,34 +155,43 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
 #define MOE_MX_MMA(d, a, b, i, sa, p) \
   "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [" d "], " a ", " b ", " i \
   ", [" sa "], [sb], " p ";\n\t"
+template <int HALVES>
 __device__ __forceinline__ void mma_stage(uint32_t d0, uint32_t d1, uint64_t ad, uint64_t bd,
                                           uint32_t idesc, uint32_t sfa, uint32_t accumulate,
                                           uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a0, a1, b0;\n\t.reg .b32 i0, s1, sb;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "setp.eq.b32 t, %6, %6;\n\t"
-      "add.u32 s1, %5, 4;\n\t"
-      "add.u32 sb, %5, 8;\n\t"
-      "add.u64 a1, %2, 1024;\n\t"
-      MOE_MX_MMA("%0", "%2", "%3", "%4", "%5", "p")
-      MOE_MX_MMA("%1", "a1", "%3", "%4", "s1", "p")
-      "add.u64 a0, %2, 2;\n\tadd.u64 a1, %2, 1026;\n\tadd.u64 b0, %3, 2;\n\t"
-      "add.u32 i0, %4, 0x20000010;\n\t"
-      MOE_MX_MMA("%0", "a0", "b0", "i0", "%5", "t")
-      MOE_MX_MMA("%1", "a1", "b0", "i0", "s1", "t")
-      "add.u64 a0, %2, 4;\n\tadd.u64 a1, %2, 1028;\n\tadd.u64 b0, %3, 4;\n\t"
-      "add.u32 i0, %4, 0x40000020;\n\t"
-      MOE_MX_MMA("%0", "a0", "b0", "i0", "%5", "t")
-      MOE_MX_MMA("%1", "a1", "b0", "i0", "s1", "t")
-      "add.u64 a0, %2, 6;\n\tadd.u64 a1, %2, 1030;\n\tadd.u64 b0, %3, 6;\n\t"
-      "add.u32 i0, %4, 0x60000030;\n\t"
-      MOE_MX_MMA("%0", "a0", "b0", "i0", "%5", "t")
-      MOE_MX_MMA("%1", "a1", "b0", "i0", "s1", "t")
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t}" ::"r"(d0),
-      "r"(d1), "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(accumulate), "r"(bar)
-      : "memory");
+#define MOE_MX_STEP(a0, a1, b, i, p) \
+  MOE_MX_MMA("%0", a0, b, i, "%5", p) MOE_MX_MMA("%1", a1, b, i, "s1", p)
+#define MOE_MX_BODY(SB, STEP)                                                              \
+  "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a0, a1, b0;\n\t.reg .b32 i0, s1, sb;\n\t"       \
+  "elect.sync _|e, 0xffffffff;\n\t"                                                        \
+  "setp.ne.b32 p, %6, 0;\n\t"                                                              \
+  "setp.eq.b32 t, %6, %6;\n\t"                                                             \
+  "add.u32 s1, %5, 4;\n\t"                                                                 \
+  "add.u32 sb, %5, " SB ";\n\t"                                                            \
+  "add.u64 a1, %2, 1024;\n\t"                                                              \
+  STEP("%2", "a1", "%3", "%4", "p")                                                        \
+  "add.u64 a0, %2, 2;\n\tadd.u64 a1, %2, 1026;\n\tadd.u64 b0, %3, 2;\n\t"                  \
+  "add.u32 i0, %4, 0x20000010;\n\t"                                                        \
+  STEP("a0", "a1", "b0", "i0", "t")                                                        \
+  "add.u64 a0, %2, 4;\n\tadd.u64 a1, %2, 1028;\n\tadd.u64 b0, %3, 4;\n\t"                  \
+  "add.u32 i0, %4, 0x40000020;\n\t"                                                        \
+  STEP("a0", "a1", "b0", "i0", "t")                                                        \
+  "add.u64 a0, %2, 6;\n\tadd.u64 a1, %2, 1030;\n\tadd.u64 b0, %3, 6;\n\t"                  \
+  "add.u32 i0, %4, 0x60000030;\n\t"                                                        \
+  STEP("a0", "a1", "b0", "i0", "t")                                                        \
+  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t}"
+#define MOE_MX_STEP1(a0, a1, b, i, p) MOE_MX_MMA("%0", a0, b, i, "%5", p)
+  if constexpr (HALVES == 2)
+    asm volatile(MOE_MX_BODY("8", MOE_MX_STEP)::"r"(d0), "r"(d1), "l"(ad), "l"(bd), "r"(idesc),
+                 "r"(sfa), "r"(accumulate), "r"(bar)
+                 : "memory");
+  else
+    asm volatile(MOE_MX_BODY("4", MOE_MX_STEP1)::"r"(d0), "r"(d1), "l"(ad), "l"(bd), "r"(idesc),
+                 "r"(sfa), "r"(accumulate), "r"(bar)
+                 : "memory");
+#undef MOE_MX_STEP
+#undef MOE_MX_STEP1
+#undef MOE_MX_BODY
 }
 #undef MOE_MX_MMA
 static_assert((W_BYTES >> 4) == 1024, "half 1's descriptor offset");
@@ -274,7 +286,7 @@ __device__ __forceinline__ float act_one(float x) {
 
 // The calling warp's 32 output columns f0 + lane for 16 tokens m0 .. (nval of
 // them): 16-bit rows, or MX e4m3 codes with one scale per token.
-template <bool MXOUT, bool F16>
+template <bool MXOUT>
 __device__ __forceinline__ void emit16(const float (&v)[16], const MxArgs& p, int m0, int nval,
                                        int f0, int lane) {
   const int f = f0 + lane;
@@ -294,14 +306,16 @@ __device__ __forceinline__ void emit16(const float (&v)[16], const MxArgs& p, in
     uint16_t* o = static_cast<uint16_t*>(p.out) + (size_t)m0 * p.Nout + f;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (i < nval) o[(size_t)i * p.Nout] = (uint16_t)pack2<F16>(v[i], 0.0f);
+      if (i < nval)
+        o[(size_t)i * p.Nout] = (uint16_t)(p.f16 ? pack_f16x2(v[i], 0.0f) : pack_bf16x2(v[i], 0.0f));
   }
 }
 
-template <int NMAX, bool GATED, int ACT, bool MXOUT, bool F16>
+template <int NMAX, int HALVES, bool GATED, int ACT, bool MXOUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ MxArgs p) {
-  using C = Cfg<NMAX>;
+  static_assert(HALVES == 2 || !GATED, "gate and up rows");
+  using C = Cfg<NMAX, HALVES>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -337,7 +351,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  constexpr int FT = GATED ? 128 : 256;  // output columns of a tile
+  pdl_launch();
+  constexpr int FT = GATED ? 128 : 128 * HALVES;  // output columns of a tile
   const int n_ftiles = (p.Nout + FT - 1) / FT;
   const int nkb = p.Kp / BK;
   pdl_wait();
@@ -392,7 +407,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int kb = 0; kb < nkb; ++kb) {
           if (!(ok = take(get(stage)))) break;
           uint8_t* dst = smem + (size_t)stage * C::STAGE_BYTES;
-          mbar_expect_tx(&sh->full[stage], 2 * W_TX);
+          mbar_expect_tx(&sh->full[stage], HALVES * W_TX);
           // rows past the operand read as zeros and count in full
           tma_4d(dst, &tm_w, &sh->full[stage], kb * BK, t.ft * FT, 0, t.e);
           const bool last = kb % C::TG == C::TG - 1 || kb == nkb - 1;
@@ -448,7 +463,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t ad = ad0 + (uint64_t)((stage * C::STAGE_BYTES) >> 4);
-        mma_stage(d, d + NMAX, ad, ad + (2 * W_BYTES >> 4), idesc,
+        mma_stage<HALVES>(d, d + NMAX, ad, ad + (HALVES * W_BYTES >> 4), idesc,
                   tm0 + (uint32_t)(C::kSf0 + (slot * C::TG + kb % C::TG) * C::SF_COLS),
                   kb != 0 ? 1u : 0u, su32(&sh->empty[stage]));
         any = true;
@@ -471,7 +486,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ch ^ (r % 8), the 128-byte swizzle.
     const int lt = threadIdx.x - kLoadWarp0 * 32;
     const int ch = lt & 7, r0 = lt >> 3;
-    const uint32_t dst0 = (uint32_t)(2 * W_BYTES + r0 * 128 + ((ch ^ (r0 & 7)) << 4));
+    const uint32_t dst0 = (uint32_t)(HALVES * W_BYTES + r0 * 128 + ((ch ^ (r0 & 7)) << 4));
     constexpr int STEP = kLoaders / 8, RI = NMAX / STEP;
     static_assert(STEP % 8 == 0 && RI <= 32, "the swizzle and the masks of a thread's rows");
     // the token rows are read again by every output tile of their expert:
@@ -514,21 +529,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight at exit
   } else if (warp < kEpiWarp0) {
     // ------------------------------------------------ scales
-    // Rows 0..255 of a buffer are the two halves' weight rows, the others the
+    // The first rows of a buffer are the halves' weight rows, the others the
     // tokens; one aligned 16-byte chunk each.  A row's scales start `skew` words
     // into its first chunk (its pitch need not be a multiple of 16 bytes), so a
     // group of SG stages' words lies in chunk g, or in chunks g and g + 1.
     // Reading back, lane l takes rows l, 32 + l, ...: the TMEM cells of its lane.
     const int st = threadIdx.x - kScaleWarp0 * 32, quad = warp & 3;
-    constexpr int PER = 2 + (NMAX + 127) / 128;  // rows a copying thread
+    constexpr int WR = 128 * HALVES, NA = C::SFA;  // weight rows and their TMEM columns
+    constexpr int PER = HALVES + (NMAX + 127) / 128;  // rows a copying thread
     const int sp = p.Kp / 32;                    // scale bytes of a row
     const bool skewed = (sp & 15) != 0;
     const uint32_t sf_dst = su32(sf) + (uint32_t)(st * 16);
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + C::kSf0;
     const int ngr = (nkb + SG - 1) / SG, nch = ngr + (skewed ? 1 : 0);
-    // weight row of tile row r (0..255) inside its expert, or -1 past the end
+    // weight row of tile row r (0 .. WR - 1) inside its expert, or -1 past the end
     auto weight_row = [&](int ft, int r) {
-      const int f = GATED ? ft * 128 + (r & 127) : ft * 256 + r;
+      const int f = GATED ? ft * 128 + (r & 127) : ft * FT + r;
       if (f >= p.Nout) return -1;
       return GATED ? f * p.row_step + (r >> 7) * p.half_step : f;
     };
@@ -543,9 +559,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (t.nv == 0) continue;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const int row = i < 2 ? weight_row(t.ft, st + 128 * i) : source_row(p, t, st + 128 * (i - 2));
-          const size_t at = ((i < 2 ? (size_t)t.e * p.N1 : 0) + max(row, 0)) * sp;
-          src[i] = (i < 2 ? p.w_scale : p.a_scale) + (at & ~size_t(15));
+          const int row = i < HALVES ? weight_row(t.ft, st + 128 * i)
+                                     : source_row(p, t, st + 128 * (i - HALVES));
+          const size_t at = ((i < HALVES ? (size_t)t.e * p.N1 : 0) + max(row, 0)) * sp;
+          src[i] = (i < HALVES ? p.w_scale : p.a_scale) + (at & ~size_t(15));
           left[i] = row >= 0 ? sp + (int)(at & 15) : 0;
         }
         return;
@@ -555,7 +572,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (ltile < total) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          if (i < 2 || st + 128 * (i - 2) < NMAX) {
+          if (i < HALVES || st + 128 * (i - HALVES) < NMAX) {
             // no byte past the row's own scales is read
             const int n = min(16, max(left[i], 0));
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
@@ -584,37 +601,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
       if (t.nv == 0) continue;
       // where the rows of this lane's cells start in their chunks
-      uint32_t skew[8 + C::SFB];
+      uint32_t skew[NA + C::SFB];
 #pragma unroll
-      for (int c = 0; c < 8 + C::SFB; ++c) {
+      for (int c = 0; c < NA + C::SFB; ++c) {
         const int r = c * 32 + lane;
-        const int row = c < 8 ? weight_row(t.ft, r) : source_row(p, t, r - 256);
-        skew[c] = skewed ? (uint32_t)((((c < 8 ? (size_t)t.e * p.N1 : 0) + max(row, 0)) * sp) & 15) >> 2 : 0u;
+        const int row = c < NA ? weight_row(t.ft, r) : source_row(p, t, r - WR);
+        const size_t at = ((c < NA ? (size_t)t.e * p.N1 : 0) + max(row, 0)) * sp;
+        skew[c] = skewed ? (uint32_t)(at & 15) >> 2 : 0u;
       }
       for (int gr = 0; gr < ngr && ok; ++gr) {
         // chunk g, and g + 1 when rows are skewed, landed
         asm volatile("cp.async.wait_group %0;" ::"n"(SBUFS - 2) : "memory");
         named_sync(kScaleBar, 128);
         const int buf1 = buf + 1 == SBUFS ? 0 : buf + 1;
-        uint32_t w[SG][8], b[SG][C::SFB_ST];
+        uint32_t w[SG][NA], b[SG][C::SFB_ST];
 #pragma unroll
-        for (int c = 0; c < 8 + C::SFB_ST; ++c) {
+        for (int c = 0; c < NA + C::SFB_ST; ++c) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (c < 8 + C::SFB && c * 32 + lane < 256 + NMAX) {
+          if (c < NA + C::SFB && c * 32 + lane < WR + NMAX) {
             v = *reinterpret_cast<const uint4*>(sf + buf * C::SF_BYTES + (c * 32 + lane) * 16);
             if (skewed) {  // words skew .. skew + 3 of the two chunks
               const uint4 n = *reinterpret_cast<const uint4*>(sf + buf1 * C::SF_BYTES + (c * 32 + lane) * 16);
-              const uint32_t k = skew[c < 8 + C::SFB ? c : 0];
+              const uint32_t k = skew[c < NA + C::SFB ? c : 0];
               const bool one = (k & 1) != 0, two = (k & 2) != 0;
               const uint32_t x0 = one ? v.y : v.x, x1 = one ? v.z : v.y, x2 = one ? v.w : v.z,
                              x3 = one ? n.x : v.w, x4 = one ? n.y : n.x, x5 = one ? n.z : n.y;
               v = make_uint4(two ? x2 : x0, two ? x3 : x1, two ? x4 : x2, two ? x5 : x3);
             }
           }
-          if (c < 8) {
+          if (c < NA) {
             w[0][c] = v.x; w[1][c] = v.y; w[2][c] = v.z; w[3][c] = v.w;
           } else {
-            b[0][c - 8] = v.x; b[1][c - 8] = v.y; b[2][c - 8] = v.z; b[3][c - 8] = v.w;
+            b[0][c - NA] = v.x; b[1][c - NA] = v.y; b[2][c - NA] = v.z; b[3][c - NA] = v.w;
           }
         }
         named_sync(kScaleBar, 128);  // read by all four warps: chunk g is free
@@ -635,8 +653,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const uint32_t d = taddr + (uint32_t)(slot * C::TG * C::SF_COLS);
 #pragma unroll
               for (int j = 0; j < C::TG; ++j) {  // stages past the last: unread
-                tmem_st<8>(d + j * C::SF_COLS, w[j0 + j]);
-                tmem_st<C::SFB_ST>(d + j * C::SF_COLS + 8, b[j0 + j]);
+                tmem_st<NA>(d + j * C::SF_COLS, w[j0 + j]);
+                tmem_st<C::SFB_ST>(d + j * C::SF_COLS + NA, b[j0 + j]);
               }
               asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
               tc_fence_before();
@@ -665,15 +683,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float b[2] = {0.0f, 0.0f};
       const int f0 = t.ft * FT + quad * 32, f = f0 + lane;
       if (p.bias) {
-        const __nv_bfloat16* be = static_cast<const __nv_bfloat16*>(p.bias) + (size_t)t.e * p.N1;
+        const uint16_t* be = static_cast<const uint16_t*>(p.bias) + (size_t)t.e * p.N1;
+        auto bias_at = [&](int i) {
+          return p.f16 ? __half2float(__ushort_as_half(be[i])) : bf16_lo(be[i]);
+        };
         if constexpr (GATED) {
           if (f < p.Nout) {
-            b[0] = ld16<F16>(be + f * p.row_step);
-            b[1] = ld16<F16>(be + f * p.row_step + p.half_step);
+            b[0] = bias_at(f * p.row_step);
+            b[1] = bias_at(f * p.row_step + p.half_step);
           }
         } else {
-          if (f < p.Nout) b[0] = ld16<F16>(be + f);
-          if (f + 128 < p.Nout) b[1] = ld16<F16>(be + f + 128);
+          if (f < p.Nout) b[0] = bias_at(f);
+          if (HALVES == 2 && f + 128 < p.Nout) b[1] = bias_at(f + 128);
         }
       }
       if (!wait_fast(&sh->tfull[acc], aphase, abort_flag, p.status)) break;
@@ -681,26 +702,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t base = lanes + (uint32_t)(acc * C::ACC_COLS);
 #pragma unroll 1
       for (int c = 16 * c0; c < t.nv; c += 16 * (kEpiWarps / 4)) {
-        uint32_t r[2][16];
+        uint32_t r[HALVES][16];
         tmem_ld16(base + c, r[0]);
-        tmem_ld16(base + NMAX + c, r[1]);
+        if constexpr (HALVES == 2) tmem_ld16(base + NMAX + c, r[HALVES - 1]);
         tmem_wait_ld();
         const int nval = min(16, t.nv - c);
         float v[16];
         if constexpr (GATED) {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            v[i] = gated<ACT>(__uint_as_float(r[0][i]) + b[0], __uint_as_float(r[1][i]) + b[1],
+            v[i] = gated<ACT>(__uint_as_float(r[0][i]) + b[0],
+                              __uint_as_float(r[HALVES - 1][i]) + b[1],
                               p.limit, p.alpha, p.beta);
-          emit16<MXOUT, F16>(v, p, t.m0 + c, nval, f0, lane);
+          emit16<MXOUT>(v, p, t.m0 + c, nval, f0, lane);
         } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < HALVES; ++h) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = act_one<ACT>(__uint_as_float(r[h][i]) + b[h]);
             // the second half may lie past the padded output
             if (f0 + h * 128 < mx::padded(p.Nout))
-              emit16<MXOUT, F16>(v, p, t.m0 + c, nval, f0 + h * 128, lane);
+              emit16<MXOUT>(v, p, t.m0 + c, nval, f0 + h * 128, lane);
           }
         }
       }
@@ -719,45 +741,53 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-template <int NMAX, bool GATED, int ACT, bool MXOUT, bool F16>
-cudaError_t go(const CUtensorMap& tm, const MxArgs& p, cudaStream_t s) {
-  using C = Cfg<NMAX>;
+// at most this many chunks of n tokens
+long long chunks_bound(const MxArgs& p, int n) { return (long long)p.M / n + std::min(p.M, p.E); }
+
+template <int NMAX, int HALVES, bool GATED, int ACT, bool MXOUT>
+cudaError_t go(const void* w, const MxArgs& p, cudaStream_t s) {
+  using C = Cfg<NMAX, HALVES>;
   constexpr size_t smem = (size_t)C::STAGES * C::STAGE_BYTES + SBUFS * C::SF_BYTES +
                           sizeof(MxShared<C::STAGES, C::SLOTS>) + 1024;
   static_assert(smem <= kSmemLimit, "shared memory");
-  auto kern = gemm_mx_kernel<NMAX, GATED, ACT, MXOUT, F16>;
+  // weights [E][N1][Kp / 2 bytes] as [E][halves][Nout][K]; a box is a stage's rows
+  CUtensorMap tm;
+  const cuuint64_t row = (cuuint64_t)p.Kp / 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.Kp, (cuuint64_t)p.Nout, GATED ? 2u : 1u,
+                              (cuuint64_t)p.E};
+  const cuuint64_t str[3] = {row * p.row_step, GATED ? row * p.half_step : row * p.Nout,
+                             row * p.N1};
+  const cuuint32_t box[4] = {BK, GATED ? 128u : 128u * HALVES, GATED ? 2u : 1u, 1};
+  if (!tmap::encode_u4_expanded(&tm, w, 4, dims, str, box)) return cudaErrorInvalidValue;
+  auto kern = gemm_mx_kernel<NMAX, HALVES, GATED, ACT, MXOUT>;
   cudaError_t e = set_smem_limit((const void*)kern, (int)smem);
   if (e != cudaSuccess) return e;
-  constexpr int FT = GATED ? 128 : 256;
-  const long long chunks = (long long)p.M / NMAX + std::min(p.M, p.E);  // at most this many
-  const long long tiles = chunks * ((p.Nout + FT - 1) / FT);
+  constexpr int FT = GATED ? 128 : 128 * HALVES;
+  const long long tiles = chunks_bound(p, NMAX) * ((p.Nout + FT - 1) / FT);
   const int grid = (int)std::max<long long>(1, std::min<long long>(tiles, num_sms()));
   e = launch_pdl(kern, dim3(grid), dim3(NUM_THREADS), smem, s, tm, p);
   count_launch();
   return e;
 }
 
-template <int NMAX, bool GATED, int ACT>
-cudaError_t go_out(const CUtensorMap& tm, const MxArgs& p, bool mx_out, bool f16, cudaStream_t s) {
-  if (mx_out)
-    return f16 ? go<NMAX, GATED, ACT, true, true>(tm, p, s)
-               : go<NMAX, GATED, ACT, true, false>(tm, p, s);
-  return f16 ? go<NMAX, GATED, ACT, false, true>(tm, p, s)
-             : go<NMAX, GATED, ACT, false, false>(tm, p, s);
-}
-
-template <int NMAX>
-cudaError_t go_act(const CUtensorMap& tm, const MxArgs& p, int kind, bool mx_out, bool f16,
-                   cudaStream_t s) {
-  switch (kind) {
-    case MOE_ACT_SILU_AND_MUL: return go_out<NMAX, true, MOE_ACT_SILU_AND_MUL>(tm, p, mx_out, f16, s);
-    case MOE_ACT_SWIGLU: return go_out<NMAX, true, MOE_ACT_SWIGLU>(tm, p, mx_out, f16, s);
-    case MOE_ACT_GELU_AND_MUL: return go_out<NMAX, true, MOE_ACT_GELU_AND_MUL>(tm, p, mx_out, f16, s);
-    case MOE_ACT_RELU: return go_out<NMAX, false, MOE_ACT_RELU>(tm, p, mx_out, f16, s);
-    case MOE_ACT_GELU: return go_out<NMAX, false, MOE_ACT_GELU>(tm, p, mx_out, f16, s);
-    case MOE_ACT_SILU: return go_out<NMAX, false, MOE_ACT_SILU>(tm, p, mx_out, f16, s);
-    default: return go_out<NMAX, false, MOE_ACT_IDENTITY>(tm, p, mx_out, f16, s);
+// Tiles: see launch_gemm_mx.
+template <bool GATED, int ACT, bool MXOUT>
+cudaError_t go_size(const void* w, const MxArgs& p, cudaStream_t s) {
+  const int hit = std::min(p.M, p.E);
+  const long long avg = ((long long)p.M + hit - 1) / hit;
+  if (avg <= 8) {
+    if constexpr (!GATED)
+      if (chunks_bound(p, 16) * ((p.Nout + 255) / 256) < num_sms())
+        return go<16, 1, GATED, ACT, MXOUT>(w, p, s);
+    return go<16, 2, GATED, ACT, MXOUT>(w, p, s);
   }
+  if (avg <= 24) return go<64, 2, GATED, ACT, MXOUT>(w, p, s);
+  if (avg <= 224) return go<96, 2, GATED, ACT, MXOUT>(w, p, s);
+  return go<208, 2, GATED, ACT, MXOUT>(w, p, s);
+}
+template <bool GATED, int ACT>
+cudaError_t go_out(const void* w, const MxArgs& p, cudaStream_t s) {
+  return p.out_scale ? go_size<GATED, ACT, true>(w, p, s) : go_size<GATED, ACT, false>(w, p, s);
 }
 
 }  // namespace
@@ -794,18 +824,28 @@ cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const
     p.alpha = act->alpha;
     p.beta = act->beta;
   }
-  // weights [E][N1][Kp / 2 bytes] as [E][halves][Nout][K]
-  CUtensorMap tm;
-  const cuuint64_t row = (cuuint64_t)p.Kp / 2;
-  const cuuint64_t dims[4] = {(cuuint64_t)p.Kp, (cuuint64_t)Nout, gate ? 2u : 1u, (cuuint64_t)E};
-  const cuuint64_t str[3] = {row * p.row_step, gate ? row * p.half_step : row * Nout, row * p.N1};
-  const cuuint32_t box[4] = {BK, gate ? 128u : 256u, gate ? 2u : 1u, 1};  // both halves
-  if (!tmap::encode_u4_expanded(&tm, w, 4, dims, str, box)) return cudaErrorInvalidValue;
-  const int kind = act ? act->kind : MOE_ACT_IDENTITY;
-  const long long avg = ((long long)M + std::min(M, E) - 1) / std::min(M, E);
-  if (avg <= 8) return go_act<16>(tm, p, kind, out_scale != nullptr, f16, s);
-  if (avg <= 80) return go_act<96>(tm, p, kind, out_scale != nullptr, f16, s);
-  return go_act<208>(tm, p, kind, out_scale != nullptr, f16, s);
+  p.f16 = f16 ? 1 : 0;
+  // Token columns of a tile, by the rows an expert that has any gets on
+  // average (the host does not know the counts):
+  //   up to 8     16 columns, six stages in flight: decode, bound by the weights.
+  //               A plain product whose tiles would not reach every SM takes
+  //               128 weight rows a tile instead of 256.
+  //   up to 24    64 columns, five stages (2000 rows on 128 experts, gate_up
+  //               2880 x 2880: 201 us, against 220 with 96)
+  //   up to 224   96 columns, four stages, two accumulators (8192 ragged rows,
+  //               gate_up 2880 x 2880: 275 us, 287 with 64, 314 with 208;
+  //               256 rows an expert, 768 x 2048: 126 us, 152 with 64, 134 with 208)
+  //   above       208 columns, one accumulator: the fewest bytes per product
+  //               (1024 rows an expert, 2048 x 7168: 1287 us)
+  switch (act ? act->kind : MOE_ACT_IDENTITY) {
+    case MOE_ACT_SILU_AND_MUL: return go_out<true, MOE_ACT_SILU_AND_MUL>(w, p, s);
+    case MOE_ACT_SWIGLU: return go_out<true, MOE_ACT_SWIGLU>(w, p, s);
+    case MOE_ACT_GELU_AND_MUL: return go_out<true, MOE_ACT_GELU_AND_MUL>(w, p, s);
+    case MOE_ACT_RELU: return go_out<false, MOE_ACT_RELU>(w, p, s);
+    case MOE_ACT_GELU: return go_out<false, MOE_ACT_GELU>(w, p, s);
+    case MOE_ACT_SILU: return go_out<false, MOE_ACT_SILU>(w, p, s);
+    default: return go_out<false, MOE_ACT_IDENTITY>(w, p, s);
+  }
 }
 
 }  // namespace moe

@@ -52,6 +52,7 @@ template <typename T, bool E2M1, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     mx_quantize_kernel(const T* __restrict__ x, int64_t stride, uint32_t items, int K, int Kp,
                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  pdl_launch();
   pdl_wait();
   // the lanes of a warp leave the loop together: items is a multiple of 16
   // and a block is four lanes, so a shuffle's partners are in or out as one
@@ -88,6 +89,7 @@ template <typename T, bool E2M1, bool VEC>
 __global__ void __launch_bounds__(kThreads)
     mx_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                          uint32_t items, int K, int Kp, T* __restrict__ out) {
+  pdl_launch();
   pdl_wait();
   for (Walk w((uint32_t)Kp / 8); w.i < items; w.next()) {
     const int c0 = (int)w.col * 8;

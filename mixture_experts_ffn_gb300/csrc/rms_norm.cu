@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024)
   const int nthr = WARP_ROW ? 32 : (int)blockDim.x;
   const int t0 = WARP_ROW ? lane : (int)threadIdx.x;
   const int row = WARP_ROW ? (int)(blockIdx.x * (blockDim.x >> 5)) + warp : (int)blockIdx.x;
+  pdl_launch();
   pdl_wait();
   if (WARP_ROW && row >= p.T) return;
   const int H = p.H;
