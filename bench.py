@@ -733,12 +733,50 @@ def run_stage(args, moe, cfg, inp, p, a, ws, flush, timed):
                  "bytes": E8 * N8 * K8 + rows * K8 + rows * N8 * 2
                  + (E8 * mm + E8 * (N8 // 128)) * (K8 // 128) * 4,
                  "tensor_peak_dtype": "fp8 (measured bf16 x 2, the nominal fp8 / bf16 ratio)"}
+    if args.stage in ("mx_layer", "mx_gate_up"):
+        # the layer over microscaled operands: weights quantised to e2m1 once;
+        # per step the norm (residual added, MX e4m3 out) and the layer, or
+        # the gate_up product alone on the rows the workload's routing gives
+        w1, s1 = moe.moe_mx_quantize(inp["w_gate_up"], moe.MOE_MX_E2M1)
+        w2, s2 = moe.moe_mx_quantize(inp["w_down"], moe.MOE_MX_E2M1)
+        tdt = inp["hidden"].dtype
+        res, gamma = torch.randn_like(inp["hidden"]), torch.ones(H, dtype=tdt, device=dev)
+        x_ws = moe._ws(moe.moe_workspace_size_mx(T, H, F, E, K), dev)
+        x_out = torch.empty_like(inp["hidden"])
+        nq = moe.moe_add_rms_norm(inp["hidden"], gamma, residual=res, out=False,
+                                  quant=moe.MOE_QUANT_MX_E4M3)
+
+        def mx_layer():
+            moe.moe_add_rms_norm(inp["hidden"], gamma, residual=res, out=False,
+                                 quant=moe.MOE_QUANT_MX_E4M3, residual_out=nq["residual"],
+                                 codes=nq["codes"], scales=nq["scales"])
+            moe.moe_ffn_forward_mx(nq["codes"], nq["scales"], inp["logits"], w1, s1, w2, s2, H, F, p,
+                                   a, inp["correction_bias"], inp["expert_ids"],
+                                   inp["b_gate_up"], inp["b_down"], dtype=tdt, out=x_out, ws=x_ws)
+
+        q_out = torch.empty((T * K, moe.moe_mx_columns(F)), dtype=torch.uint8, device=dev)
+        q_scale = torch.empty((T * K, moe.moe_mx_columns(F) // 32), dtype=torch.uint8, device=dev)
+        g_ws = moe._ws(moe.moe_grouped_gemm_mx_workspace_size(T * K, F, H, E), dev)
+        fns["mx_layer"] = mx_layer
+        fns["mx_gate_up"] = lambda: moe.moe_grouped_gemm_mx(
+            nq["codes"], nq["scales"], w1, s1, perm["seg_end"], F, act=a, bias=inp["b_gate_up"],
+            row_to_route=perm["row_to_route"], top_k=K, dtype=tdt, mx_out=True, out=q_out,
+            out_scale=q_scale, ws=g_ws)
+        D, M, n1 = int(torch.unique(ti).numel()), T * K, cfg.n_gate_up
+        wb = 0.5 + 1 / 32
+        if args.stage == "mx_layer":
+            extra = {"flops": 2.0 * M * (n1 + F) * H,
+                     "bytes": D * (n1 + F) * H * wb + T * (8 * H + 4 * E)}
+        else:
+            extra = {"flops": 2.0 * M * n1 * H,
+                     "bytes": D * n1 * H * wb + (T * H + M * F) * (1 + 1 / 32)}
+        extra["tensor_peak_dtype"] = "fp8 (measured bf16 x 2, the nominal fp8 / bf16 ratio)"
     st, nl = timed(fns[args.stage], args.steps, args.warmup)
     line = {"stage": args.stage, "workload": args.workload,
             "us": [round(1e3 * x, 2) for x in st], "launches": nl}
     if extra:
         pk, pk_src = load_peaks()
-        tpk = pk["bf16_tflops"] * (2.0 if args.stage == "fp8_gemm" else 1.0)
+        tpk = pk["bf16_tflops"] * (2.0 if "tensor_peak_dtype" in extra else 1.0)
         us = 1e3 * sorted(st)[len(st) // 2]
         tf = extra["flops"] / (us * 1e-6) / 1e12
         gbs = extra["bytes"] / (us * 1e-6) / 1e9
@@ -804,7 +842,7 @@ def main():
     ap.add_argument("--stage", default=None,
                     choices=["route", "route_permute", "permute", "gemm_act", "gemm_down",
                              "combine", "indexed_mlp", "shared_mlp", "fp8_gemm",
-                             "gemm_act_split", "swiglu"],
+                             "gemm_act_split", "swiglu", "mx_layer", "mx_gate_up"],
                     help="time one stage alone (for profiler captures)")
     ap.add_argument("--shared-s", type=int, default=2048,
                     help="intermediate size of the shared expert timed by --stage shared_mlp "

@@ -15,12 +15,6 @@ namespace moe {
 // their memory to be visible; a no-op when launched without it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Lets the next kernel of the stream start its set-up as soon as every CTA of
-// this grid has started (it still waits for this grid's end in pdl_wait).
-__device__ __forceinline__ void pdl_launch() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ---------------------------------------------------------------- element I/O
 template <typename T> struct Elem;
 template <> struct Elem<float> {

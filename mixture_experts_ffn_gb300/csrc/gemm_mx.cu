@@ -66,12 +66,14 @@ constexpr int kScaleBar = 1;               // named barrier of the scale warps
 constexpr size_t kSmemLimit = 227 * 1024;
 
 // Token columns of a tile and what follows from them: ring depth and TMEM.
-// HALVES: 128-row halves of weights a tile holds.
-template <int NMAX_, int HALVES>
+// HALVES: 128-row halves of weights a CTA's tile holds.  PAIR: two CTAs of a
+// cluster share a tile of twice the weight rows, each holding half its tokens.
+template <int NMAX_, int HALVES, bool PAIR>
 struct Cfg {
   static constexpr int NMAX = NMAX_;
   static constexpr int kAccs = NMAX <= 112 ? 2 : 1;  // accumulators (512 TMEM columns in all)
-  static constexpr int B_BYTES = NMAX * BK;
+  static constexpr int BROWS = PAIR ? NMAX / 2 : NMAX;  // token rows in this CTA's memory
+  static constexpr int B_BYTES = BROWS * BK;
   static constexpr int STAGE_BYTES = HALVES * W_BYTES + B_BYTES;
   static constexpr int SF_BYTES = (128 * HALVES + NMAX) * 4 * SG;  // a chunk of every row's scales
   // scales, barriers, tile prefix and segment starts, alignment
@@ -152,16 +154,17 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
 // against 600 when a diverged lane issues the MMAs one by one and moves every
 // operand over first.  Descriptors advance by 32 bytes (2) a step; a step's
 // scale byte is selected in the instruction descriptor (bits 4 and 29).
-#define MOE_MX_MMA(d, a, b, i, sa, p) \
-  "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [" d "], " a ", " b ", " i \
-  ", [" sa "], [sb], " p ";\n\t"
-template <int HALVES>
+template <int HALVES, bool PAIR>
 __device__ __forceinline__ void mma_stage(uint32_t d0, uint32_t d1, uint64_t ad, uint64_t bd,
                                           uint32_t idesc, uint32_t sfa, uint32_t accumulate,
                                           uint32_t bar) {
-#define MOE_MX_STEP(a0, a1, b, i, p) \
-  MOE_MX_MMA("%0", a0, b, i, "%5", p) MOE_MX_MMA("%1", a1, b, i, "s1", p)
-#define MOE_MX_BODY(SB, STEP)                                                              \
+#define MOE_MX_MMA(G, d, a, b, i, sa, p)                                                      \
+  "@e tcgen05.mma.cta_group::" G ".kind::mxf8f6f4.block_scale.scale_vec::1X [" d "], " a ", " \
+  b ", " i ", [" sa "], [sb], " p ";\n\t"
+#define MOE_MX_STEP2(G, a0, a1, b, i, p) \
+  MOE_MX_MMA(G, "%0", a0, b, i, "%5", p) MOE_MX_MMA(G, "%1", a1, b, i, "s1", p)
+#define MOE_MX_STEP1(G, a0, a1, b, i, p) MOE_MX_MMA(G, "%0", a0, b, i, "%5", p)
+#define MOE_MX_BODY(G, SB, STEP, COMMIT)                                                   \
   "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a0, a1, b0;\n\t.reg .b32 i0, s1, sb;\n\t"       \
   "elect.sync _|e, 0xffffffff;\n\t"                                                        \
   "setp.ne.b32 p, %6, 0;\n\t"                                                              \
@@ -169,45 +172,113 @@ __device__ __forceinline__ void mma_stage(uint32_t d0, uint32_t d1, uint64_t ad,
   "add.u32 s1, %5, 4;\n\t"                                                                 \
   "add.u32 sb, %5, " SB ";\n\t"                                                            \
   "add.u64 a1, %2, 1024;\n\t"                                                              \
-  STEP("%2", "a1", "%3", "%4", "p")                                                        \
+  STEP(G, "%2", "a1", "%3", "%4", "p")                                                     \
   "add.u64 a0, %2, 2;\n\tadd.u64 a1, %2, 1026;\n\tadd.u64 b0, %3, 2;\n\t"                  \
   "add.u32 i0, %4, 0x20000010;\n\t"                                                        \
-  STEP("a0", "a1", "b0", "i0", "t")                                                        \
+  STEP(G, "a0", "a1", "b0", "i0", "t")                                                     \
   "add.u64 a0, %2, 4;\n\tadd.u64 a1, %2, 1028;\n\tadd.u64 b0, %3, 4;\n\t"                  \
   "add.u32 i0, %4, 0x40000020;\n\t"                                                        \
-  STEP("a0", "a1", "b0", "i0", "t")                                                        \
+  STEP(G, "a0", "a1", "b0", "i0", "t")                                                     \
   "add.u64 a0, %2, 6;\n\tadd.u64 a1, %2, 1030;\n\tadd.u64 b0, %3, 6;\n\t"                  \
   "add.u32 i0, %4, 0x60000030;\n\t"                                                        \
-  STEP("a0", "a1", "b0", "i0", "t")                                                        \
-  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%7];\n\t}"
-#define MOE_MX_STEP1(a0, a1, b, i, p) MOE_MX_MMA("%0", a0, b, i, "%5", p)
-  if constexpr (HALVES == 2)
-    asm volatile(MOE_MX_BODY("8", MOE_MX_STEP)::"r"(d0), "r"(d1), "l"(ad), "l"(bd), "r"(idesc),
-                 "r"(sfa), "r"(accumulate), "r"(bar)
+  STEP(G, "a0", "a1", "b0", "i0", "t") "@e " COMMIT
+#define MOE_MX_OPS "r"(d0), "r"(d1), "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(accumulate), "r"(bar)
+  if constexpr (PAIR) {
+    static_assert(HALVES == 2, "pair tiles hold both halves");
+    asm volatile(MOE_MX_BODY("2", "8", MOE_MX_STEP2,
+                             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."
+                             "multicast::cluster.b64 [%7], %8;\n\t}")::MOE_MX_OPS,
+                 "h"((uint16_t)3)
                  : "memory");
-  else
-    asm volatile(MOE_MX_BODY("4", MOE_MX_STEP1)::"r"(d0), "r"(d1), "l"(ad), "l"(bd), "r"(idesc),
-                 "r"(sfa), "r"(accumulate), "r"(bar)
+  } else if constexpr (HALVES == 2) {
+    asm volatile(MOE_MX_BODY("1", "8", MOE_MX_STEP2,
+                             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster."
+                             "b64 [%7];\n\t}")::MOE_MX_OPS
                  : "memory");
-#undef MOE_MX_STEP
-#undef MOE_MX_STEP1
+  } else {
+    asm volatile(MOE_MX_BODY("1", "4", MOE_MX_STEP1,
+                             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster."
+                             "b64 [%7];\n\t}")::MOE_MX_OPS
+                 : "memory");
+  }
+#undef MOE_MX_OPS
 #undef MOE_MX_BODY
-}
+#undef MOE_MX_STEP1
+#undef MOE_MX_STEP2
 #undef MOE_MX_MMA
+}
 static_assert((W_BYTES >> 4) == 1024, "half 1's descriptor offset");
-// commit by one elected lane of a converged warp
+// commit by one elected lane of a converged warp, to both CTAs' barriers of a pair
+template <bool PAIR>
 __device__ __forceinline__ void mx_commit_elect(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            bar)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t d;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(saddr), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ void cluster_sync() {
   asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      "barrier.cluster.arrive.release.aligned;\n\t"
+      "barrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+// arrival on a barrier of either CTA of the pair (shared::cluster address),
+// released at CTA scope: a cluster-scope release would wait for every copy this
+// SM has in flight, and what it orders is this SM's own shared memory (after
+// the proxy fence) and TMEM (after the tcgen05 fence)
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// a load into this CTA's shared memory that completes on a barrier of the
+// pair's leader (shared::cluster address)
+__device__ __forceinline__ void tma2_4d(void* dst, const CUtensorMap* m, uint32_t bar, int c0,
+                                        int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+      "bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(su32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
 // Instruction descriptor, kind::mxf8f6f4: A e2m1 (format 5 at bit 7), B e4m3
 // (format 0 at bit 10), both K-major, N / 8 at bit 17, e8m0 scales (bit 23),
-// M = 128 (bit 27); the scale byte of K step j at bits 4 (B) and 29 (A).
+// M / 128 at bit 27 (256 across a pair); the scale byte of K step j at bits 4
+// (B) and 29 (A).
+template <bool PAIR>
 __device__ __forceinline__ uint32_t idesc_mx(int N) {
-  return (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27);
+  return (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((PAIR ? 2u : 1u) << 27);
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok, uint64_t pol) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
@@ -311,12 +382,14 @@ __device__ __forceinline__ void emit16(const float (&v)[16], const MxArgs& p, in
   }
 }
 
-template <int NMAX, int HALVES, bool GATED, int ACT, bool MXOUT>
+template <int NMAX, int HALVES, bool PAIR, bool GATED, int ACT, bool MXOUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ MxArgs p) {
   static_assert(HALVES == 2 || !GATED, "gate and up rows");
-  using C = Cfg<NMAX, HALVES>;
+  using C = Cfg<NMAX, HALVES, PAIR>;
   constexpr int STAGES = C::STAGES;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;  // 0: the leader, which issues the MMAs
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -327,16 +400,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&sh->full[s], 1 + kLoaders);  // the producer's expect-tx, every loader thread
+      // the producer's expect-tx, every loader thread, and the peer's rows; the
+      // peer's own barrier counts its loaders
+      mbar_init(&sh->full[s], kLoaders + (rank == 0 ? 1 + (PAIR ? 1 : 0) : 0));
       mbar_init(&sh->empty[s], 1);
     }
     for (int s = 0; s < C::SLOTS; ++s) {
-      mbar_init(&sh->sfull[s], 4);  // every scale warp
+      mbar_init(&sh->sfull[s], PAIR ? 8 : 4);  // every scale warp
       mbar_init(&sh->sempty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sh->tfull[a], 1);
-      mbar_init(&sh->tempty[a], 32 * kEpiWarps);
+      mbar_init(&sh->tempty[a], (PAIR ? 2 : 1) * kEpiWarps);
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
@@ -345,15 +420,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0 && lane == 0)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_w)) : "memory");
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     su32(&sh->tmem_base)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       su32(&sh->tmem_base)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       su32(&sh->tmem_base)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   pdl_launch();
   constexpr int FT = GATED ? 128 : 128 * HALVES;  // output columns of a tile
-  const int n_ftiles = (p.Nout + FT - 1) / FT;
+  constexpr int FTU = PAIR ? 2 * FT : FT;  // ... and of a pair's
+  const int n_ftiles = (p.Nout + FTU - 1) / FTU;
   const int nkb = p.Kp / BK;
   pdl_wait();
   // every expert's rows start where the one before ends (never before it)
@@ -364,9 +448,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   const int total = build_tile_prefix(p.seg_end, p.E, p.M, NMAX, n_ftiles, sh->prefix, sh->scan_tmp);
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync(); else __syncthreads();  // barriers, TMEM, tile list
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
+  // tile t as this CTA sees it: its own output tile of the pair's two
+  auto decode = [&](int t) {
+    MxTile r = mx_decode<NMAX>(t, sh->prefix, sh->start, p.E);
+    if constexpr (PAIR) r.ft = 2 * r.ft + (int)rank;
+    return r;
+  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -401,15 +491,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (i == s) v = owner[i];
         return v;
       };
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
+      for (int tile = unit; tile < total && ok; tile += units) {
+        const MxTile t = decode(tile);
         if (t.nv == 0) continue;
         for (int kb = 0; kb < nkb; ++kb) {
           if (!(ok = take(get(stage)))) break;
           uint8_t* dst = smem + (size_t)stage * C::STAGE_BYTES;
-          mbar_expect_tx(&sh->full[stage], HALVES * W_TX);
           // rows past the operand read as zeros and count in full
-          tma_4d(dst, &tm_w, &sh->full[stage], kb * BK, t.ft * FT, 0, t.e);
+          if constexpr (PAIR) {
+            if (rank == 0) mbar_expect_tx(&sh->full[stage], 2 * HALVES * W_TX);
+            tma2_4d(dst, &tm_w, map_to_rank(su32(&sh->full[stage]), 0), kb * BK, t.ft * FT, 0, t.e);
+          } else {
+            mbar_expect_tx(&sh->full[stage], HALVES * W_TX);
+            tma_4d(dst, &tm_w, &sh->full[stage], kb * BK, t.ft * FT, 0, t.e);
+          }
           const bool last = kb % C::TG == C::TG - 1 || kb == nkb - 1;
 #pragma unroll
           for (int i = 0; i < STAGES; ++i)
@@ -425,10 +520,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ok = take(get(stage));
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      if (!ok) {  // let every copy already in flight land before the block exits
+      if (!ok && rank == 0) {  // let every copy already in flight land before the block exits
 #pragma unroll
         for (int s = 0; s < STAGES; ++s)
           if (issued[s]) drain_wait(&sh->full[s], (issued[s] - 1u) & 1u);
+      }
+    }
+  } else if (PAIR && warp == 1 && rank != 0) {
+    // ------------------------------------------------ the peer's rows of a stage landed
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = unit; tile < total && ok; tile += units) {
+        if (decode(tile).nv == 0) continue;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!wait_fast(&sh->full[stage], phase, abort_flag, p.status)) { ok = false; break; }
+          fence_proxy_async_smem();
+          mbar_arrive_cluster(map_to_rank(su32(&sh->full[stage]), 0));
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
       }
     }
   } else if (warp == 1) {
@@ -437,24 +548,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t phase = 0, aphase = 0, sphase = 0;
     bool ok = true, any = false;
     const uint64_t ad0 = sw128_desc(su32(smem));
+    // a pair's barriers take arrivals of both CTAs: acquire at cluster scope
+    auto try_full = [&](uint64_t* b, uint32_t parity) {
+      return PAIR ? mbar_try_wait_cluster(su32(b), parity) : mbar_try_wait(su32(b), parity);
+    };
     // warp reductions leave their result in a uniform register
     const uint32_t tm0 = __reduce_max_sync(0xffffffffu, tmem);
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
+    for (int tile = unit; tile < total && ok; tile += units) {
+      const MxTile t = decode(tile);
       if (t.nv == 0) continue;
       ok = __all_sync(0xffffffffu, wait_fast(&sh->tempty[acc], aphase ^ 1u, abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tm0 + (uint32_t)(acc * C::ACC_COLS);
-      const uint32_t idesc = idesc_mx((int)__reduce_max_sync(0xffffffffu, (uint32_t)t.N));
+      const uint32_t idesc = idesc_mx<PAIR>((int)__reduce_max_sync(0xffffffffu, (uint32_t)t.N));
       for (int kb = 0; kb < nkb; ++kb) {
         // both barriers tried at once, the slow paths only when one is not there yet
         const bool first = kb % C::TG == 0;
-        const bool f0 = mbar_try_wait(su32(&sh->full[stage]), phase);
-        const bool f1 = !first || mbar_try_wait(su32(&sh->sfull[slot]), sphase);
+        const bool f0 = try_full(&sh->full[stage], phase);
+        const bool f1 = !first || try_full(&sh->sfull[slot], sphase);
         if (!__all_sync(0xffffffffu, f0 && f1)) {
           ok = wait_bar(&sh->full[stage], phase, abort_flag, p.status);
           if (first) ok = wait_bar(&sh->sfull[slot], sphase, abort_flag, p.status) && ok;
+          // done, so these return at once; they order the peer's writes
+          if (PAIR && ok) {
+            ok = try_full(&sh->full[stage], phase);
+            if (first) ok = try_full(&sh->sfull[slot], sphase) && ok;
+          }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
@@ -463,7 +583,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         fence_proxy_async_smem();
         tc_fence_after();
         const uint64_t ad = ad0 + (uint64_t)((stage * C::STAGE_BYTES) >> 4);
-        mma_stage<HALVES>(d, d + NMAX, ad, ad + (HALVES * W_BYTES >> 4), idesc,
+        mma_stage<HALVES, PAIR>(d, d + NMAX, ad, ad + (HALVES * W_BYTES >> 4), idesc,
                   tm0 + (uint32_t)(C::kSf0 + (slot * C::TG + kb % C::TG) * C::SF_COLS),
                   kb != 0 ? 1u : 0u, su32(&sh->empty[stage]));
         any = true;
@@ -472,11 +592,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
       if (!ok) break;
-      mx_commit_elect(su32(&sh->tfull[acc]));
+      mx_commit_elect<PAIR>(su32(&sh->tfull[acc]));
       if (++acc == C::kAccs) { acc = 0; aphase ^= 1u; }
     }
     if (!ok && any) {  // every MMA issued so far done before TMEM is freed
-      mx_commit_elect(su32(&sh->drain));
+      mx_commit_elect<PAIR>(su32(&sh->drain));
       drain_wait(&sh->drain, 0);
     }
   } else if (warp < kScaleWarp0) {
@@ -487,7 +607,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int lt = threadIdx.x - kLoadWarp0 * 32;
     const int ch = lt & 7, r0 = lt >> 3;
     const uint32_t dst0 = (uint32_t)(HALVES * W_BYTES + r0 * 128 + ((ch ^ (r0 & 7)) << 4));
-    constexpr int STEP = kLoaders / 8, RI = NMAX / STEP;
+    constexpr int STEP = kLoaders / 8, RI = C::BROWS / STEP;
     static_assert(STEP % 8 == 0 && RI <= 32, "the swizzle and the masks of a thread's rows");
     // the token rows are read again by every output tile of their expert:
     // kept in L2 ahead of the weight stream
@@ -497,8 +617,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
+    for (int tile = unit; tile < total && ok; tile += units) {
+      const MxTile t = decode(tile);
       if (t.nv == 0) continue;
       // The rows' offsets in 128-byte blocks.  Rows of the MMA's padding are not
       // copied (their columns are never read); a row with a bad map entry is
@@ -506,8 +626,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t at[RI], mine = 0, good = 0;
 #pragma unroll
       for (int i = 0; i < RI; ++i) {
-        const int r = r0 + STEP * i, m = source_row(p, t, r);
-        if (r < t.nv) mine |= 1u << i;
+        const int b = r0 + STEP * i;  // row of this CTA's buffer
+        const int r = PAIR ? b + (int)rank * (t.N / 2) : b, m = source_row(p, t, r);
+        if (r < t.nv && (!PAIR || b < t.N / 2)) mine |= 1u << i;
         if (m >= 0) good |= 1u << i;
         at[i] = (uint32_t)max(m, 0) * (uint32_t)nkb;
       }
@@ -552,10 +673,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // next, into buffer lbuf; src and left are its rows' next chunk and bytes.
     const uint8_t* src[PER];
     int left[PER];
-    int ltile = blockIdx.x, lc = 0, lbuf = 0, buf = 0;
+    int ltile = unit, lc = 0, lbuf = 0, buf = 0;
     auto seek = [&]() {  // rows of the first tile at or after ltile that has any
-      for (; ltile < total; ltile += gridDim.x) {
-        const MxTile t = mx_decode<NMAX>(ltile, sh->prefix, sh->start, p.E);
+      for (; ltile < total; ltile += units) {
+        const MxTile t = decode(ltile);
         if (t.nv == 0) continue;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -586,7 +707,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (++lbuf == SBUFS) lbuf = 0;
         if (++lc == nch) {
           lc = 0;
-          ltile += gridDim.x;
+          ltile += units;
           seek();
         }
       }
@@ -597,8 +718,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int slot = 0;
     uint32_t sphase = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
+    for (int tile = unit; tile < total && ok; tile += units) {
+      const MxTile t = decode(tile);
       if (t.nv == 0) continue;
       // where the rows of this lane's cells start in their chunks
       uint32_t skew[NA + C::SFB];
@@ -659,7 +780,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&sh->sfull[slot]);
+              if (lane == 0) {
+                if constexpr (PAIR)
+                  mbar_arrive_cluster(map_to_rank(su32(&sh->sfull[slot]), 0));
+                else
+                  mbar_arrive(&sh->sfull[slot]);
+              }
               if (++slot == C::SLOTS) { slot = 0; sphase ^= 1u; }
             }
           }
@@ -676,8 +802,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     int acc = 0;
     uint32_t aphase = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      const MxTile t = mx_decode<NMAX>(tile, sh->prefix, sh->start, p.E);
+    for (int tile = unit; tile < total; tile += units) {
+      const MxTile t = decode(tile);
       if (t.nv == 0) continue;
       // the lane's biases, loaded before the accumulator is ready
       float b[2] = {0.0f, 0.0f};
@@ -714,7 +840,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             v[i] = gated<ACT>(__uint_as_float(r[0][i]) + b[0],
                               __uint_as_float(r[HALVES - 1][i]) + b[1],
                               p.limit, p.alpha, p.beta);
-          emit16<MXOUT>(v, p, t.m0 + c, nval, f0, lane);
+          // a pair's second output tile may lie past the padded output
+          if (!PAIR || f0 < mx::padded(p.Nout)) emit16<MXOUT>(v, p, t.m0 + c, nval, f0, lane);
         } else {
 #pragma unroll
           for (int h = 0; h < HALVES; ++h) {
@@ -727,26 +854,37 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&sh->tempty[acc]);
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_cluster(map_to_rank(su32(&sh->tempty[acc]), 0));
+        else
+          mbar_arrive(&sh->tempty[acc]);
+      }
       if (++acc == C::kAccs) { acc = 0; aphase ^= 1u; }
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // neither CTA frees TMEM or exits while its peer works
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
-                 : "memory");
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                   : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                   : "memory");
   }
 }
 
 // at most this many chunks of n tokens
 long long chunks_bound(const MxArgs& p, int n) { return (long long)p.M / n + std::min(p.M, p.E); }
 
-template <int NMAX, int HALVES, bool GATED, int ACT, bool MXOUT>
+template <int NMAX, int HALVES, bool PAIR, bool GATED, int ACT, bool MXOUT>
 cudaError_t go(const void* w, const MxArgs& p, cudaStream_t s) {
-  using C = Cfg<NMAX, HALVES>;
+  using C = Cfg<NMAX, HALVES, PAIR>;
   constexpr size_t smem = (size_t)C::STAGES * C::STAGE_BYTES + SBUFS * C::SF_BYTES +
                           sizeof(MxShared<C::STAGES, C::SLOTS>) + 1024;
   static_assert(smem <= kSmemLimit, "shared memory");
@@ -759,13 +897,31 @@ cudaError_t go(const void* w, const MxArgs& p, cudaStream_t s) {
                              row * p.N1};
   const cuuint32_t box[4] = {BK, GATED ? 128u : 128u * HALVES, GATED ? 2u : 1u, 1};
   if (!tmap::encode_u4_expanded(&tm, w, 4, dims, str, box)) return cudaErrorInvalidValue;
-  auto kern = gemm_mx_kernel<NMAX, HALVES, GATED, ACT, MXOUT>;
+  auto kern = gemm_mx_kernel<NMAX, HALVES, PAIR, GATED, ACT, MXOUT>;
   cudaError_t e = set_smem_limit((const void*)kern, (int)smem);
   if (e != cudaSuccess) return e;
-  constexpr int FT = GATED ? 128 : 128 * HALVES;
+  constexpr int CTAS = PAIR ? 2 : 1, FT = CTAS * (GATED ? 128 : 128 * HALVES);
   const long long tiles = chunks_bound(p, NMAX) * ((p.Nout + FT - 1) / FT);
-  const int grid = (int)std::max<long long>(1, std::min<long long>(tiles, num_sms()));
-  e = launch_pdl(kern, dim3(grid), dim3(NUM_THREADS), smem, s, tm, p);
+  const int units = (int)std::max<long long>(1, std::min<long long>(tiles, num_sms() / CTAS));
+  if constexpr (PAIR) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * units);
+    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_pdl
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, tm, p);
+  } else {
+    e = launch_pdl(kern, dim3(units), dim3(NUM_THREADS), smem, s, tm, p);
+  }
   count_launch();
   return e;
 }
@@ -778,12 +934,12 @@ cudaError_t go_size(const void* w, const MxArgs& p, cudaStream_t s) {
   if (avg <= 8) {
     if constexpr (!GATED)
       if (chunks_bound(p, 16) * ((p.Nout + 255) / 256) < num_sms())
-        return go<16, 1, GATED, ACT, MXOUT>(w, p, s);
-    return go<16, 2, GATED, ACT, MXOUT>(w, p, s);
+        return go<16, 1, false, GATED, ACT, MXOUT>(w, p, s);
+    return go<16, 2, false, GATED, ACT, MXOUT>(w, p, s);
   }
-  if (avg <= 24) return go<64, 2, GATED, ACT, MXOUT>(w, p, s);
-  if (avg <= 224) return go<96, 2, GATED, ACT, MXOUT>(w, p, s);
-  return go<208, 2, GATED, ACT, MXOUT>(w, p, s);
+  if (avg <= 24) return go<64, 2, false, GATED, ACT, MXOUT>(w, p, s);
+  if (avg <= 224) return go<96, 2, false, GATED, ACT, MXOUT>(w, p, s);
+  return go<208, 2, true, GATED, ACT, MXOUT>(w, p, s);
 }
 template <bool GATED, int ACT>
 cudaError_t go_out(const void* w, const MxArgs& p, cudaStream_t s) {

@@ -21,6 +21,13 @@
 #include "common.cuh"
 
 namespace moe {
+
+// Lets the next kernel of the stream start its set-up as soon as every CTA of
+// this grid has started (it still waits for this grid's end in pdl_wait).
+__device__ __forceinline__ void pdl_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 namespace mx {
 
 constexpr int kBlock = 32;   // columns of one scale

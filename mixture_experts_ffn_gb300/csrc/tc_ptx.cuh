@@ -42,17 +42,13 @@ static __device__ __noinline__ bool wait_bar(uint64_t* b, uint32_t parity, volat
                                       int* status) {
   const uint32_t addr = su32(b);
   if (mbar_try_wait(addr, parity)) return true;
-  // The timer is read only once the first tries have failed: reading it takes
-  // longer than most waits, and a ring's turn passes through several of them.
-  uint64_t t0 = 0;
+  const uint64_t t0 = global_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(addr, parity)) return true;
     if (*abort_flag) return false;
-    if (t0 == 0) {
-      t0 = global_ns();
-    } else if (global_ns() - t0 > kTimeoutNs) {
+    if (global_ns() - t0 > kTimeoutNs) {
       *abort_flag = 1;
       latch_error(status, kDevTimeout);
       return false;

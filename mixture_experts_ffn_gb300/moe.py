@@ -28,6 +28,7 @@ MOE_LAYOUT_PSUM, MOE_LAYOUT_PER_ROW, MOE_LAYOUT_MASKED = 0, 1, 2
 
 MOE_MX_E4M3, MOE_MX_E2M1 = 0, 1
 MOE_QUANT_NONE, MOE_QUANT_MX_E4M3, MOE_QUANT_E4M3_BLOCK128 = 0, 1, 2
+_GATED = (MOE_ACT_SILU_AND_MUL, MOE_ACT_SWIGLU, MOE_ACT_GELU_AND_MUL)
 
 # C entry points and their argument types (mirrors include/moe.h)
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, \
@@ -164,6 +165,10 @@ def _dt(t: torch.Tensor) -> int:
     if t.dtype == torch.float16:
         return MOE_F16
     raise TypeError(f"unsupported dtype {t.dtype}")
+
+
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _cuda(*ts):
@@ -615,12 +620,9 @@ def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_
                       if quant == MOE_QUANT_MX_E4M3 else
                       torch.empty((T, Hp // 128), dtype=torch.float32, device=x.device))
     _check("moe_add_rms_norm",
-           lib.moe_add_rms_norm(x.data_ptr(), None if residual is None else residual.data_ptr(),
-                                weight.data_ptr(), T, H, _dt(x), eps, quant,
-                                None if residual_out is None else residual_out.data_ptr(),
-                                None if out is None else out.data_ptr(),
-                                None if codes is None else codes.data_ptr(),
-                                None if scales is None else scales.data_ptr(), _stream_of(x)))
+           lib.moe_add_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, _dt(x), eps,
+                                quant, _ptr(residual_out), _ptr(out), _ptr(codes), _ptr(scales),
+                                _stream_of(x)))
     return {"residual": residual_out, "out": out, "codes": codes, "scales": scales}
 
 
@@ -638,13 +640,12 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
     lib = load_library()
     _cuda(a, a_scale, w, w_scale, seg_end, bias, row_to_route, out, out_scale)
     R, Kp = a.shape
-    E, N1 = w.shape[0], w.shape[1]
+    E, N1, half = w.shape
     M = R if row_to_route is None else row_to_route.numel()
-    gated = act is not None and act.kind in (MOE_ACT_SILU_AND_MUL, MOE_ACT_SWIGLU,
-                                             MOE_ACT_GELU_AND_MUL)
-    if Kp % 128 or w.shape[2] * 2 != Kp or a_scale.shape != (R, Kp // 32) or \
-            w_scale.shape != (E, N1, Kp // 32) or N1 != (2 * N if gated else N) or \
-            seg_end.numel() != E or (bias is not None and bias.shape != (E, N1)):
+    gated = act is not None and act.kind in _GATED
+    if Kp % 128 or half * 2 != Kp or a_scale.numel() != R * (Kp // 32) or \
+            w_scale.numel() != E * N1 * (Kp // 32) or N1 != (2 * N if gated else N) or \
+            seg_end.numel() != E or (bias is not None and bias.numel() != E * N1):
         raise ValueError("operands are not MX tensors of matching extents")
     if bias is not None and bias.dtype != dtype:
         raise TypeError("bias takes the output's dtype")
@@ -658,14 +659,13 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
         out = torch.empty((M, N), dtype=dtype, device=a.device)
     if ws is None:
         ws = _ws(lib.moe_grouped_gemm_mx_workspace_size(M, N, Kp, E), a.device)
-    dt = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}.get(dtype, MOE_F32)
+    dt = MOE_BF16 if dtype == torch.bfloat16 else MOE_F16 if dtype == torch.float16 else MOE_F32
     _check("moe_grouped_gemm_mx",
-           lib.moe_grouped_gemm_mx(a.data_ptr(), a_scale.data_ptr(), R,
-                                   None if row_to_route is None else row_to_route.data_ptr(),
-                                   top_k, w.data_ptr(), w_scale.data_ptr(), _p(bias),
+           lib.moe_grouped_gemm_mx(a.data_ptr(), a_scale.data_ptr(), R, _ptr(row_to_route), top_k,
+                                   w.data_ptr(), w_scale.data_ptr(), _ptr(bias),
                                    seg_end.data_ptr(), M, N, Kp, E, dt,
                                    None if act is None else ctypes.byref(act), out.data_ptr(),
-                                   _p(out_scale), ws.data_ptr(), ws.numel(), _stream_of(a)))
+                                   _ptr(out_scale), ws.data_ptr(), ws.numel(), _stream_of(a)))
     return (out, out_scale) if mx_out else out
 
 
@@ -684,29 +684,31 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
     _cuda(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale, w_down, w_down_scale,
           correction_bias, expert_ids, b_gate_up, b_down, out)
     T, Hp = hidden.shape
-    E, N1 = w_gate_up.shape[:2]
+    E, N1, half = w_gate_up.shape
     Fp = moe_mx_columns(F)
-    gated = act.kind in (MOE_ACT_SILU_AND_MUL, MOE_ACT_SWIGLU, MOE_ACT_GELU_AND_MUL)
-    if Hp != moe_mx_columns(H) or hidden_scale.shape != (T, Hp // 32) or \
-            N1 != (2 * F if gated else F) or w_gate_up.shape[2] * 2 != Hp or \
-            w_gate_up_scale.shape != (E, N1, Hp // 32) or w_down.shape != (E, H, Fp // 2) or \
-            w_down_scale.shape != (E, H, Fp // 32) or logits.shape != (T, E):
+    if Hp != moe_mx_columns(H) or half * 2 != Hp or N1 != (2 * F if act.kind in _GATED else F) or \
+            hidden_scale.numel() != T * (Hp // 32) or \
+            w_gate_up_scale.numel() != E * N1 * (Hp // 32) or \
+            w_down.numel() != E * H * (Fp // 2) or w_down_scale.numel() != E * H * (Fp // 32) or \
+            logits.numel() != T * E:
         raise ValueError("operands are not MX tensors of matching extents")
-    for b, shape in ((b_gate_up, (E, N1)), (b_down, (E, H))):
-        if b is not None and (b.dtype != dtype or b.shape != shape):
+    for b, n in ((b_gate_up, E * N1), (b_down, E * H)):
+        if b is not None and (b.dtype != dtype or b.numel() != n):
             raise ValueError("a bias is [E, rows] in the output's dtype")
     if out is None:
         out = torch.empty((T, H), dtype=dtype, device=hidden.device)
     if ws is None:
         ws = _ws(lib.moe_workspace_size_mx(T, H, F, E, p.top_k), hidden.device)
+    rp = p if p.dtype == _dt(logits) else _rp(p, logits)
     _check("moe_ffn_forward_mx",
            lib.moe_ffn_forward_mx(hidden.data_ptr(), hidden_scale.data_ptr(), logits.data_ptr(),
                                   w_gate_up.data_ptr(), w_gate_up_scale.data_ptr(),
-                                  w_down.data_ptr(), w_down_scale.data_ptr(), _p(correction_bias),
-                                  _p(expert_ids), _p(b_gate_up), _p(b_down), T, H, F, E, _dt(out),
-                                  ctypes.byref(_rp(p, logits)), ctypes.byref(act), out.data_ptr(),
-                                  _p(topk_weights_out), _p(topk_ids_out), ws.data_ptr(),
-                                  ws.numel(), _stream_of(hidden)))
+                                  w_down.data_ptr(), w_down_scale.data_ptr(),
+                                  _ptr(correction_bias), _ptr(expert_ids), _ptr(b_gate_up),
+                                  _ptr(b_down), T, H, F, E, _dt(out), ctypes.byref(rp),
+                                  ctypes.byref(act), out.data_ptr(), _ptr(topk_weights_out),
+                                  _ptr(topk_ids_out), ws.data_ptr(), ws.numel(),
+                                  _stream_of(hidden)))
     return out
 
 
