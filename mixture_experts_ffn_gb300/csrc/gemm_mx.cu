@@ -938,8 +938,8 @@ cudaError_t go_size(const void* w, const MxArgs& p, cudaStream_t s) {
     return go<16, 2, false, GATED, ACT, MXOUT>(w, p, s);
   }
   if (avg <= 24) return go<64, 2, false, GATED, ACT, MXOUT>(w, p, s);
-  if (avg <= 224) return go<96, 2, false, GATED, ACT, MXOUT>(w, p, s);
-  return go<208, 2, true, GATED, ACT, MXOUT>(w, p, s);
+  if (avg <= 160) return go<96, 2, true, GATED, ACT, MXOUT>(w, p, s);
+  return go<224, 2, true, GATED, ACT, MXOUT>(w, p, s);
 }
 template <bool GATED, int ACT>
 cudaError_t go_out(const void* w, const MxArgs& p, cudaStream_t s) {
@@ -987,12 +987,14 @@ cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const
   //               A plain product whose tiles would not reach every SM takes
   //               128 weight rows a tile instead of 256.
   //   up to 24    64 columns, five stages (2000 rows on 128 experts, gate_up
-  //               2880 x 2880: 201 us, against 220 with 96)
-  //   up to 224   96 columns, four stages, two accumulators (8192 ragged rows,
-  //               gate_up 2880 x 2880: 275 us, 287 with 64, 314 with 208;
-  //               256 rows an expert, 768 x 2048: 126 us, 152 with 64, 134 with 208)
-  //   above       208 columns, one accumulator: the fewest bytes per product
-  //               (1024 rows an expert, 2048 x 7168: 1287 us)
+  //               2880 x 2880: 201 us; 218 with pairs of 96)
+  //   up to 160   96 columns on a pair, two accumulators (8192 ragged rows, gate_up
+  //               2880 x 2880: 273 us, down 148; 287 and 156 with 64, 275 and 152 with
+  //               96 on one CTA, 298 and 164 with 224)
+  //   above       224 columns on a pair, one accumulator: the fewest bytes per
+  //               product (256 rows an expert, 2048 x 2048: 144 us, 160 with 96; 1024
+  //               rows an expert, 2048 x 7168: 1188 us, 1522 with 96, 1322 with 208
+  //               on one CTA, whose token copies and shared-memory reads double)
   switch (act ? act->kind : MOE_ACT_IDENTITY) {
     case MOE_ACT_SILU_AND_MUL: return go_out<true, MOE_ACT_SILU_AND_MUL>(w, p, s);
     case MOE_ACT_SWIGLU: return go_out<true, MOE_ACT_SWIGLU>(w, p, s);
