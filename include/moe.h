@@ -617,12 +617,12 @@ moe_status moe_add_rms_norm(const void* x, const void* residual, const void* wei
  *   w, w_scale   MX e2m1 rows [E, N1, Kp / 2], [E, N1, Kp / 32], N1 = 2N for a
  *                gated act (rows as moe_grouped_gemm_act), N otherwise
  *   bias         [E, N1] dtype or NULL;  act NULL for the plain product
- *   out_scale    NULL: out [M, N] dtype (MOE_BF16 or MOE_F16).  Otherwise out
- *                and out_scale are MX e4m3 rows [M, Np], [M, Np / 32] of the
- *                unrounded act(p): the next product's operand
+ *   out_scale    NULL: out [M, N] dtype.  Otherwise out and out_scale are MX
+ *                e4m3 rows [M, Np], [M, Np / 32] of the unrounded act(p): the
+ *                next product's operand
  *   ws           >= moe_grouped_gemm_mx_workspace_size(M, N, K, E) bytes
  * a and the scales 16-byte, w 32-byte aligned, and out and out_scale 16-byte
- * aligned when MX (MOE_ERR_UNSUPPORTED otherwise, and for MOE_F32).
+ * aligned when MX (MOE_ERR_UNSUPPORTED otherwise).
  * Rows past seg_end[E-1] are not written.  E <= 1024. */
 moe_status moe_grouped_gemm_mx(const void* a, const void* a_scale, int a_rows,
                                const int32_t* row_to_route, int top_k, const void* w,
@@ -634,15 +634,15 @@ size_t moe_grouped_gemm_mx_workspace_size(int M, int N, int K, int E);
 
 /* The routed forward over microscaled operands: moe_ffn_forward with hidden as
  * MX e4m3 rows (moe_add_rms_norm or moe_mx_quantize make them) and both weight
- * stacks as MX e2m1.  Routing, index maps and combine as moe_ffn_forward; the
- * gate_up product reads its rows through row_to_route and writes the gated
- * activation as MX e4m3 rows, the down product writes dtype rows.  Four
- * launches when E <= 512.
+ * stacks as MX e2m1.  Routing and index maps as moe_ffn_forward; the gate_up
+ * product reads its rows through row_to_route and writes the gated activation
+ * as MX e4m3 rows; the down product's rows stay float32 until the combine's one
+ * rounding.  Four launches when E <= 512.
  *   hidden, hidden_scale        [T, Hp], [T, Hp / 32]
  *   w_gate_up, w_gate_up_scale  [E, N1, Hp / 2], [E, N1, Hp / 32]
  *   w_down, w_down_scale        [E, H, Fp / 2], [E, H, Fp / 32]
- *   b_gate_up [E, N1], b_down [E, H] dtype or NULL;  out [T, H] dtype (MOE_BF16
- *   or MOE_F16);  the other arguments as moe_ffn_forward (no MoERouter slice:
+ *   b_gate_up [E, N1], b_down [E, H] dtype or NULL;  out [T, H] dtype;  the
+ *   other arguments as moe_ffn_forward (no MoERouter slice:
  *   p->local_expert_count must be 0);  alignment as moe_grouped_gemm_mx;
  *   ws >= moe_workspace_size_mx(T, H, F, E, K). */
 moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, const void* logits,

@@ -1018,27 +1018,27 @@ moe_status moe_grouped_gemm_mx(const void* a, const void* a_scale, int a_rows,
   if (!mx_gemm_extent_ok(M, N, K, E) || !dtype_ok(dtype) || (act && !act_ok(act)) || a_rows < 0 ||
       (row_to_route ? top_k < 1 : a_rows < M))
     return MOE_ERR_INVALID_ARG;
-  if (dtype == MOE_F32) return MOE_ERR_UNSUPPORTED;
+  const size_t esz = esize(dtype);
   if (!w || !w_scale || !seg_end || (M > 0 && (!out || (a_rows > 0 && (!a || !a_scale)))))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(a_scale) || !aligned(w, 32) || !aligned16(w_scale) ||
-      !aligned(out, out_scale ? 16 : 2) || !aligned16(out_scale))
+      !aligned(out, out_scale ? 16 : esz) || !aligned(bias, esz) || !aligned16(out_scale))
     return MOE_ERR_UNSUPPORTED;
   const size_t need = moe_grouped_gemm_mx_workspace_size(M, N, K, E);
   if (!ws_ok(ws, ws_bytes, need)) return MOE_ERR_WORKSPACE;
   const size_t N1 = act && gated_kind(act->kind) ? 2 * (size_t)N : (size_t)N;
   const size_t Kp = mx_pad(K), Np = mx_pad(N), rows = (size_t)E * N1;
-  Span outs[] = {{out, out_scale ? (size_t)M * Np : (size_t)M * N * 2},
+  Span outs[] = {{out, out_scale ? (size_t)M * Np : (size_t)M * N * esz},
                  {out_scale, (size_t)M * (Np / 32)},
                  {ws, need}};
   Span ins[] = {{a, (size_t)a_rows * Kp},     {a_scale, (size_t)a_rows * (Kp / 32)},
                 {w, rows * (Kp / 2)},         {w_scale, rows * (Kp / 32)},
-                {bias, bias ? rows * 2 : 0},  {seg_end, (size_t)E * 4},
+                {bias, bias ? rows * esz : 0},  {seg_end, (size_t)E * 4},
                 {row_to_route, row_to_route ? (size_t)M * 4 : 0}};
   if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
   if (M == 0) return MOE_OK;
   return cuda_status(launch_gemm_mx(a, a_scale, a_rows, row_to_route, row_to_route ? top_k : 1, w,
-                                    w_scale, bias, seg_end, M, N, K, E, act, dtype == MOE_F16, out,
+                                    w_scale, bias, seg_end, M, N, K, E, act, dtype, dtype, out,
                                     out_scale, static_cast<int*>(ws), stream));
 }
 
@@ -1065,19 +1065,20 @@ moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, cons
   const long long Ml = (long long)T * K;
   if (p->local_expert_count != 0 || !mx_gemm_extent_ok(Ml, H, F, E) || !mx_gemm_extent_ok(Ml, F, H, E))
     return MOE_ERR_INVALID_ARG;
-  if (dtype == MOE_F32) return MOE_ERR_UNSUPPORTED;
+  const size_t esz = esize(dtype);
   if (!w_gate_up || !w_gate_up_scale || !w_down || !w_down_scale ||
       (T > 0 && (!hidden || !hidden_scale || !out)))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(hidden) || !aligned16(hidden_scale) || !aligned(w_gate_up, 32) ||
       !aligned16(w_gate_up_scale) || !aligned(w_down, 32) || !aligned16(w_down_scale) ||
-      !aligned(out, 2))
+      !aligned(out, esz) ||
+      !aligned(b_gate_up, esz) || !aligned(b_down, esz))
     return MOE_ERR_UNSUPPORTED;
   const MxForwardWs L(T, H, F, E, K);
   if (!ws_ok(ws, ws_bytes, L.total)) return MOE_ERR_WORKSPACE;
   const size_t M = (size_t)Ml, N1 = gated_kind(act->kind) ? 2 * (size_t)F : (size_t)F;
   const size_t Hp = mx_pad(H), Fp = mx_pad(F);
-  Span outs[] = {{out, (size_t)T * H * 2}, {topk_weights_out, M * 4}, {topk_ids_out, M * 4},
+  Span outs[] = {{out, (size_t)T * H * esz}, {topk_weights_out, M * 4}, {topk_ids_out, M * 4},
                  {ws, L.total}};
   Span ins[] = {{hidden, (size_t)T * Hp},
                 {hidden_scale, (size_t)T * (Hp / 32)},
@@ -1088,8 +1089,8 @@ moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, cons
                 {w_down_scale, (size_t)E * H * (Fp / 32)},
                 {correction_bias, correction_bias ? (size_t)E * 4 : 0},
                 {expert_ids, expert_ids ? M * 4 : 0},
-                {b_gate_up, b_gate_up ? (size_t)E * N1 * 2 : 0},
-                {b_down, b_down ? (size_t)E * H * 2 : 0}};
+                {b_gate_up, b_gate_up ? (size_t)E * N1 * esz : 0},
+                {b_down, b_down ? (size_t)E * H * esz : 0}};
   if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
   if (T == 0) return MOE_OK;
 
@@ -1100,7 +1101,7 @@ moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, cons
   int32_t* r2r = reinterpret_cast<int32_t*>(base + L.row_to_route);
   int32_t* route_to_row = reinterpret_cast<int32_t*>(base + L.route_to_row);
   int* status = reinterpret_cast<int*>(base);
-  const bool fused_maps = route_permute_ok(E), f16 = dtype == MOE_F16;
+  const bool fused_maps = route_permute_ok(E);
   StageTimer t_route(fused_maps ? "route_permute" : "route", stream);
   cudaError_t err =
       fused_maps ? launch_route_permute(logits, correction_bias, expert_ids, T, E, *p, tw, ti,
@@ -1113,18 +1114,21 @@ moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, cons
   t_route.done();
   StageTimer t_gu("gate_up", stream);
   err = launch_gemm_mx(hidden, hidden_scale, T, r2r, K, w_gate_up, w_gate_up_scale, b_gate_up,
-                       seg_end, (int)M, F, H, E, act, f16, base + L.act, base + L.act_scale, status,
-                       stream);
+                       seg_end, (int)M, F, H, E, act, dtype, dtype, base + L.act, base + L.act_scale,
+                       status, stream);
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   t_gu.done();
   StageTimer t_down("down", stream);
   err = launch_gemm_mx(base + L.act, base + L.act_scale, (int)M, nullptr, 1, w_down, w_down_scale,
-                       b_down, seg_end, (int)M, H, F, E, nullptr, f16, base + L.y, nullptr, status,
-                       stream);
+                       b_down, seg_end, (int)M, H, F, E, nullptr, dtype, MOE_F32, base + L.y, nullptr,
+                       status, stream);
   if (err != cudaSuccess) return MOE_ERR_CUDA;
   t_down.done();
   StageTimer t_comb("combine", stream);
-  err = launch_combine(base + L.y, tw, route_to_row, T, K, H, dtype, 1.0f, out, stream);
+  // routed_scaling_factor is folded into tw by the router
+  const float* y = reinterpret_cast<const float*>(base + L.y);
+  err = dtype == MOE_F32 ? launch_combine(y, tw, route_to_row, T, K, H, dtype, 1.0f, out, stream)
+                         : launch_mx_combine(y, tw, route_to_row, T, K, H, dtype, out, stream);
   t_comb.done();
   return cuda_status(err);
 }

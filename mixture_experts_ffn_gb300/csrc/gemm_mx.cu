@@ -117,12 +117,12 @@ struct MxArgs {
   const void* bias;        // [E, N1] or null
   const int32_t* seg_end;
   const int32_t* grows;    // row_to_route, or null (row m is row m of a)
-  void* out;               // 16-bit [M, Nout], or e4m3 codes [M, Np]
+  void* out;               // [M, Nout], or e4m3 codes [M, Np]
   uint8_t* out_scale;      // [M, Np / 32]
   int* status;
   int M, Nout, N1, Kp, E, a_rows, gdiv;
   int row_step, half_step;  // weight row of output f, half h: f * row_step + h * half_step
-  int f16;                  // bias and 16-bit output: float16, else bfloat16
+  int bias_t, out_t;        // moe_dtype of the bias and (unless MX) the output
   float limit, alpha, beta;
 };
 
@@ -374,11 +374,20 @@ __device__ __forceinline__ void emit16(const float (&v)[16], const MxArgs& p, in
       if (lane == 0) so[(size_t)i * (Np / 32)] = (uint8_t)byte;
     }
   } else if (f < p.Nout) {
-    uint16_t* o = static_cast<uint16_t*>(p.out) + (size_t)m0 * p.Nout + f;
+    const size_t at = (size_t)m0 * p.Nout + f;
+    if (p.out_t == MOE_F32) {
+      float* o = static_cast<float*>(p.out) + at;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < nval)
-        o[(size_t)i * p.Nout] = (uint16_t)(p.f16 ? pack_f16x2(v[i], 0.0f) : pack_bf16x2(v[i], 0.0f));
+      for (int i = 0; i < 16; ++i)
+        if (i < nval) o[(size_t)i * p.Nout] = v[i];
+    } else {
+      uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+      const bool f16 = p.out_t == MOE_F16;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < nval)
+          o[(size_t)i * p.Nout] = (uint16_t)(f16 ? pack_f16x2(v[i], 0.0f) : pack_bf16x2(v[i], 0.0f));
+    }
   }
 }
 
@@ -809,9 +818,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float b[2] = {0.0f, 0.0f};
       const int f0 = t.ft * FT + quad * 32, f = f0 + lane;
       if (p.bias) {
-        const uint16_t* be = static_cast<const uint16_t*>(p.bias) + (size_t)t.e * p.N1;
+        const size_t be = (size_t)t.e * p.N1;
         auto bias_at = [&](int i) {
-          return p.f16 ? __half2float(__ushort_as_half(be[i])) : bf16_lo(be[i]);
+          if (p.bias_t == MOE_F32) return static_cast<const float*>(p.bias)[be + i];
+          const uint16_t u = static_cast<const uint16_t*>(p.bias)[be + i];
+          return p.bias_t == MOE_F16 ? __half2float(__ushort_as_half(u)) : bf16_lo(u);
         };
         if constexpr (GATED) {
           if (f < p.Nout) {
@@ -951,8 +962,8 @@ cudaError_t go_out(const void* w, const MxArgs& p, cudaStream_t s) {
 cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const int32_t* gather_rows,
                            int gather_div, const void* w, const void* w_scale, const void* bias,
                            const int32_t* seg_end, int M, int Nout, int K, int E,
-                           const moe_act_params* act, bool f16, void* out, void* out_scale,
-                           int* status, cudaStream_t s) {
+                           const moe_act_params* act, moe_dtype bias_dt, moe_dtype out_dt, void* out,
+                           void* out_scale, int* status, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
   const bool gate = act && act_is_gated(act->kind);
   const bool inter = gate && act->kind == MOE_ACT_SWIGLU && act->swiglu_fusion == 1;
@@ -980,7 +991,8 @@ cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const
     p.alpha = act->alpha;
     p.beta = act->beta;
   }
-  p.f16 = f16 ? 1 : 0;
+  p.bias_t = bias_dt;
+  p.out_t = out_dt;
   // Token columns of a tile, by the rows an expert that has any gets on
   // average (the host does not know the counts):
   //   up to 8     16 columns, six stages in flight: decode, bound by the weights.

@@ -56,7 +56,7 @@ struct ForwardWs {
 
 // Workspace of the forward over microscaled operands: the permute scratch,
 // routing, index maps, the activation's codes and scales, and the down
-// product's 16-bit rows.
+// product's float32 rows.
 struct MxForwardWs {
   size_t topk_w, topk_ids, seg_end, row_to_route, route_to_row, act, act_scale, y, total;
   MxForwardWs(int T, int H, int F, int E, int K) {
@@ -70,7 +70,7 @@ struct MxForwardWs {
     act = align256(route_to_row + M * 4);
     act_scale = align256(act + M * Fp);
     y = align256(act_scale + M * (Fp / 32));
-    total = align256(y + M * (size_t)H * 2);
+    total = align256(y + M * (size_t)H * 4);
   }
 };
 
@@ -219,12 +219,17 @@ cudaError_t launch_rms_norm(const void* x, const void* residual, const void* wei
 
 // Grouped GEMM of MX e4m3 rows by MX e2m1 weights (gemm_mx.cu).  With
 // gather_rows, row r of the operand is row gather_rows[r] / gather_div of `a`
-// (a_rows rows); out is 16-bit (float16 with f16), or MX e4m3 with out_scale.
+// (a_rows rows); out is out_dt, or MX e4m3 with out_scale; bias is bias_dt.
 cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows,
                            const int32_t* gather_rows, int gather_div, const void* w,
                            const void* w_scale, const void* bias, const int32_t* seg_end, int M,
-                           int Nout, int K, int E, const moe_act_params* act, bool f16, void* out,
-                           void* out_scale, int* status, cudaStream_t s);
+                           int Nout, int K, int E, const moe_act_params* act, moe_dtype bias_dt,
+                           moe_dtype out_dt, void* out, void* out_scale, int* status,
+                           cudaStream_t s);
+
+// launch_combine from float32 rows to a 16-bit output (mx_combine.cu)
+cudaError_t launch_mx_combine(const float* y, const float* w, const int32_t* route_to_row, int T,
+                              int K, int H, moe_dtype dt, void* out, cudaStream_t s);
 
 // indexed per-route decode path (bf16, silu_and_mul, no bias)
 cudaError_t launch_indexed(const void* hidden, const void* w1, const void* w2, const float* w,

@@ -352,7 +352,7 @@ def test_gemm_mx_plain(moe, counts, N, K):
 
 
 @pytest.mark.parametrize("act", ["silu_and_mul", "gelu_and_mul", "relu", "gelu", "silu", "identity"])
-@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("mx_out", [False, True])
 def test_gemm_mx_activations(moe, act, dtype, mx_out):
     run_gemm(moe, [20, 0, 9, 60], 144, 256, act=act, bias=True, dtype=dtype, mx_out=mx_out)
@@ -488,6 +488,8 @@ def layer_inputs(moe, T, H, F, E, k, act, dtype, seed=0):
     (37, 200, 96, 6, 3, "silu_and_mul", torch.float16, "sigmoid"),
     (300, 384, 260, 16, 4, "swiglu", torch.bfloat16, "softmax"),
     (64, 128, 72, 600, 2, "gelu", torch.bfloat16, "sqrt_softplus"),  # separate route and permute
+    (33, 130, 64, 5, 5, "silu_and_mul", torch.bfloat16, "softmax"),  # columns not a multiple of 4
+    (20, 256, 96, 12, 9, "gelu_and_mul", torch.float32, "softmax"),
 ])
 def test_layer_equals_its_stages(moe, T, H, F, E, k, act, dtype, scoring):
     """Bit for bit the staged calls', and the down product's float64 value from the kernels'
@@ -505,13 +507,13 @@ def test_layer_equals_its_stages(moe, T, H, F, E, k, act, dtype, scoring):
     m = moe.moe_permute(ids, E)
     mid = moe.moe_grouped_gemm_mx(*hidden, *w1, m["seg_end"], F, act=ap, bias=b1, dtype=dtype,
                                   row_to_route=m["row_to_route"], top_k=k, mx_out=True)
-    y = moe.moe_grouped_gemm_mx(*mid, *w2, m["seg_end"], H, bias=b2, dtype=dtype)
-    assert torch.equal(out, moe.moe_combine(y, tw, m["route_to_row"]))
+    y = moe.moe_grouped_gemm_mx(*mid, *w2, m["seg_end"], H, bias=b2.float(), dtype=torch.float32)
+    assert torch.equal(out, moe.moe_combine(y, tw, m["route_to_row"]).to(dtype))
     v, d = reference(mid, w2, b2, m["seg_end"], "none", H, False, (0, 1, 0))
     at = m["route_to_row"].long().cpu().numpy().reshape(T, k)
     wt = f64(tw)
     ref = sum(wt[:, j:j + 1] * v[at[:, j]] for j in range(k))
-    tol = sum(np.abs(wt[:, j:j + 1]) * (d[at[:, j]] + (HALF[dtype] + 4 * U * k) * np.abs(v[at[:, j]]))
+    tol = sum(np.abs(wt[:, j:j + 1]) * (d[at[:, j]] + (4 + k) * U * np.abs(v[at[:, j]]))
               for j in range(k))
     assert (np.abs(f64(out) - ref) <= tol * (1 + HALF[dtype]) + HALF[dtype] * np.abs(ref) + TINY[dtype]).all()
 
@@ -534,7 +536,7 @@ def test_layer_after_the_norm_with_fixed_experts(moe):
     m = moe.moe_permute(got, E)
     mid = moe.moe_grouped_gemm_mx(n["codes"], n["scales"], *w1, m["seg_end"], F, act=ap,
                                   row_to_route=m["row_to_route"], top_k=k, mx_out=True)
-    y = moe.moe_grouped_gemm_mx(*mid, *w2, m["seg_end"], H)
-    assert torch.equal(out, moe.moe_combine(y, tw, m["route_to_row"]))
+    y = moe.moe_grouped_gemm_mx(*mid, *w2, m["seg_end"], H, dtype=torch.float32)
+    assert torch.equal(out, moe.moe_combine(y, tw, m["route_to_row"]).to(torch.bfloat16))
     empty = moe.moe_ffn_forward_mx(n["codes"][:0], n["scales"][:0], logits[:0], *w1, *w2, H, F, p, ap)
     assert empty.shape == (0, H)

@@ -116,7 +116,7 @@ def test_gemm_mx_refuses(moe):
                dict(out=None), dict(a=None), dict(asc=None), dict(M=1 << 30, rows=1 << 30),
                dict(act=moe.act_params(9)), dict(act=moe.act_params(1, swiglu_fusion=0))):
         assert g(**kw) == inv, kw
-    for kw in (dict(dt=moe.MOE_F32), dict(a=A(0, 8)), dict(asc=A(1, 4)), dict(w=A(2, 16)),
+    for kw in (dict(dt=moe.MOE_F32, out=A(5, 2)), dict(bias=A(7, 1)), dict(a=A(0, 8)), dict(asc=A(1, 4)), dict(w=A(2, 16)),
                dict(wsc=A(3, 8)), dict(out=A(5, 1)), dict(out=A(5, 8), osc=A(7)),
                dict(osc=A(7, 8))):
         assert g(**kw) == uns, kw
@@ -146,7 +146,7 @@ def test_layer_mx_refuses(moe):
                dict(act=moe.act_params(1, swiglu_fusion=0)),
                dict(p=moe.route_params(2, local_expert_count=4))):
         assert f(**kw) == inv, kw
-    for kw in (dict(dt=moe.MOE_F32), dict(h=A(0, 4)), dict(hs=A(1, 8)), dict(w1=A(3, 16)),
+    for kw in (dict(dt=moe.MOE_F32, out=A(7, 2)), dict(b1=A(9, 1)), dict(h=A(0, 4)), dict(hs=A(1, 8)), dict(w1=A(3, 16)),
                dict(w2=A(5, 16)), dict(s1=A(4, 4)), dict(s2=A(6, 8)), dict(out=A(7, 1))):
         assert f(**kw) == uns, kw
     assert f(wsb=need - 1) == moe.MOE_ERR_WORKSPACE and f(ws=None) == moe.MOE_ERR_WORKSPACE
@@ -158,7 +158,7 @@ def test_layer_mx_refuses(moe):
 def test_workspace_sizes(moe):
     a = moe.moe_workspace_size_mx(2048, 2880, 2880, 128, 4)
     M, Fp = 2048 * 4, 2944
-    assert a >= M * (Fp + Fp // 32 + 2880 * 2) and a % 256 == 0
+    assert a >= M * (Fp + Fp // 32 + 2880 * 4) and a % 256 == 0
     assert moe.moe_workspace_size_mx(-1, 1, 1, 1, 1) == 0
     assert moe.moe_workspace_size_mx(1 << 29, 8, 8, 8, 2) == 0
     assert moe.moe_grouped_gemm_mx_workspace_size(64, 64, 64, 8) >= 256
