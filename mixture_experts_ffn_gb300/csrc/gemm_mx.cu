@@ -1,7 +1,7 @@
 // Grouped GEMM over microscaled operands (mx_dev.cuh): rows of activations in
 // MX e4m3 times expert weights in MX e2m1, over the expert-segmented row
-// layout, with bias, activation and the output rounding (16-bit, or MX e4m3
-// for the next product) in the epilogue.
+// layout, with bias, activation and the output rounding (a 16-bit or float32
+// type, or MX e4m3 for the next product) in the epilogue.
 //
 // Mathematics: p[m, n] = sum over blocks b of 2^(sa[m, b] + sw[n, b]) *
 // (codes of a, block b . codes of w, block b).  tcgen05.mma kind::mxf8f6f4
@@ -21,7 +21,7 @@
 //   warp 0 lane 0 : TMA producer of the weight codes.  The map's type expands
 //                   each 16 packed values (8 bytes) into a 16-byte chunk of
 //                   shared memory, the form the MMA reads 4-bit values in.
-//   warp 1        : TMEM; lane 0 issues the MMAs
+//   warp 1        : TMEM; issues the MMAs
 //   warps 2..3    : cp.async loaders of the token rows (gathered through
 //                   row_to_route when given)
 //   warps 4..7    : both operands' scales, four stages at a time through shared
@@ -36,6 +36,18 @@
 // Stage: 128 columns of K, i.e. four K32 MMA steps; the 4 scale bytes of a
 // row and stage are one 32-bit TMEM cell, step j using byte j of it.
 // Measured back to back, a stage's eight MMAs take max(313, 4 N) cycles.
+// PAIR (cta_group::2): two CTAs share a tile, each with its own weight rows and
+// half the tokens; the leader's MMAs read both CTAs' shared memory.  The peer's
+// token copies reach the leader's barrier through a forwarding thread, the scale
+// warps' and epilogues' arrivals directly.
+//
+// What bounds it (GB300, median of flushed runs): decode (128 rows on 123
+// experts, 2048 x 7168 gate_up) the weights' stream, 300 us for 1.92 GB, 94% of
+// the measured HBM rate; medium batches (64 rows an expert) what the ring holds
+// in flight, 80 KB of packed weights an SM, half its memory going to the gaps of
+// the expanded form: 0.7 of HBM; 1024 rows an expert the MMAs, 1188 us, 0.84 of
+// twice the measured bf16 rate, the rest shared-memory contention and the one
+// accumulator's epilogue.
 // Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
 
@@ -123,6 +135,7 @@ struct MxArgs {
   int M, Nout, N1, Kp, E, a_rows, gdiv;
   int row_step, half_step;  // weight row of output f, half h: f * row_step + h * half_step
   int bias_t, out_t;        // moe_dtype of the bias and (unless MX) the output
+  int even;                 // 16-bit output: Nout is even and out 4-byte aligned
   float limit, alpha, beta;
 };
 
@@ -356,37 +369,69 @@ __device__ __forceinline__ float act_one(float x) {
 }
 
 // The calling warp's 32 output columns f0 + lane for 16 tokens m0 .. (nval of
-// them): 16-bit rows, or MX e4m3 codes with one scale per token.
+// them): rows of out_t, or MX e4m3 codes with one scale per token.  A lane holds
+// one column of every token, memory wants a token's columns together: lanes
+// trade columns (pairs for 16-bit values, fours for codes) until each holds a
+// 32-bit word of a token, so 16 tokens take 8 or 4 store instructions, not 16.
 template <bool MXOUT>
 __device__ __forceinline__ void emit16(const float (&v)[16], const MxArgs& p, int m0, int nval,
                                        int f0, int lane) {
+  const uint32_t all = 0xffffffffu;
   const int f = f0 + lane;
   if constexpr (MXOUT) {
     const int Np = mx::padded(p.Nout);
-    uint8_t* o = static_cast<uint8_t*>(p.out) + (size_t)m0 * Np + f;
-    uint8_t* so = p.out_scale + (size_t)m0 * (Np / 32) + (f0 >> 5);
+    uint32_t r[4] = {0, 0, 0, 0}, mine = 0;  // four tokens' codes a word; scale of token `lane`
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (i >= nval) break;
-      const uint32_t amax = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[i]));
-      const uint32_t byte = mx::scale_byte<false>(amax);
-      o[(size_t)i * Np] = (uint8_t)mx::e4m3x2(mx::scaled(v[i], mx::inv_scale(byte)), 0.0f);
-      if (lane == 0) so[(size_t)i * (Np / 32)] = (uint8_t)byte;
+    for (int i = 0; i < 16; i += 2) {
+      const uint32_t b0 = mx::scale_byte<false>(__reduce_max_sync(all, mx::abs_bits(v[i])));
+      const uint32_t b1 = mx::scale_byte<false>(__reduce_max_sync(all, mx::abs_bits(v[i + 1])));
+      const float s0 = mx::inv_scale(b0), s1 = mx::inv_scale(b1);
+      r[i >> 2] |= mx::e4m3x2(mx::scaled(v[i], s0), mx::scaled(v[i + 1], s1)) << (8 * (i & 3));
+      if (lane == i) mine = b0;
+      if (lane == i + 1) mine = b1;
     }
-  } else if (f < p.Nout) {
-    const size_t at = (size_t)m0 * p.Nout + f;
-    if (p.out_t == MOE_F32) {
-      float* o = static_cast<float*>(p.out) + at;
+    if (lane < nval) p.out_scale[(size_t)(m0 + lane) * (Np / 32) + (f0 >> 5)] = (uint8_t)mine;
+    // 4 x 4 bytes between the lanes of each four: lane 4 q + j ends with columns
+    // 4 q .. 4 q + 3 of token 4 m + j in word m
+    const int j = lane & 3;
+    uint8_t* o = static_cast<uint8_t*>(p.out) + (size_t)(m0 + j) * Np + f0 + (lane & ~3);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      uint32_t w = r[m];
+      const uint32_t x = __shfl_xor_sync(all, w, 1);
+      // bytes (tokens) of my parity, from the even lane then the odd one
+      w = (j & 1) ? __byte_perm(x, w, 0x7351) : __byte_perm(w, x, 0x6240);
+      const uint32_t y = __shfl_xor_sync(all, w, 2);
+      w = (j & 2) ? __byte_perm(y, w, 0x7632) : __byte_perm(w, y, 0x5410);
+      if (4 * m + j < nval) *reinterpret_cast<uint32_t*>(o + (size_t)4 * m * Np) = w;
+    }
+  } else if (p.out_t == MOE_F32) {
+    if (f < p.Nout) {
+      float* o = static_cast<float*>(p.out) + (size_t)m0 * p.Nout + f;
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (i < nval) o[(size_t)i * p.Nout] = v[i];
-    } else {
-      uint16_t* o = static_cast<uint16_t*>(p.out) + at;
-      const bool f16 = p.out_t == MOE_F16;
+    }
+  } else {
+    const bool f16 = p.out_t == MOE_F16;
+    uint16_t* o = static_cast<uint16_t*>(p.out) + (size_t)m0 * p.Nout;
+    if (p.even) {  // words of two columns are aligned
+      const int odd = lane & 1;
+      o += (size_t)odd * p.Nout + (f - odd);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const uint32_t w = f16 ? pack_f16x2(v[i], v[i + 1]) : pack_bf16x2(v[i], v[i + 1]);
+        const uint32_t x = __shfl_xor_sync(all, w, 1);
+        const uint32_t u = odd ? __byte_perm(x, w, 0x7632) : __byte_perm(w, x, 0x5410);
+        if (i + odd < nval && f - odd < p.Nout)
+          *reinterpret_cast<uint32_t*>(o + (size_t)i * p.Nout) = u;
+      }
+    } else if (f < p.Nout) {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (i < nval)
-          o[(size_t)i * p.Nout] = (uint16_t)(f16 ? pack_f16x2(v[i], 0.0f) : pack_bf16x2(v[i], 0.0f));
+          o[(size_t)i * p.Nout + f] =
+              (uint16_t)(f16 ? pack_f16x2(v[i], 0.0f) : pack_bf16x2(v[i], 0.0f));
     }
   }
 }
@@ -948,8 +993,9 @@ cudaError_t go_size(const void* w, const MxArgs& p, cudaStream_t s) {
         return go<16, 1, false, GATED, ACT, MXOUT>(w, p, s);
     return go<16, 2, false, GATED, ACT, MXOUT>(w, p, s);
   }
-  if (avg <= 24) return go<64, 2, false, GATED, ACT, MXOUT>(w, p, s);
-  if (avg <= 160) return go<96, 2, true, GATED, ACT, MXOUT>(w, p, s);
+  if (avg <= 48) return go<64, 2, false, GATED, ACT, MXOUT>(w, p, s);
+  if (avg <= 160 || p.Kp / BK <= (MXOUT ? 28 : 14))
+    return go<96, 2, true, GATED, ACT, MXOUT>(w, p, s);
   return go<224, 2, true, GATED, ACT, MXOUT>(w, p, s);
 }
 template <bool GATED, int ACT>
@@ -993,20 +1039,26 @@ cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const
   }
   p.bias_t = bias_dt;
   p.out_t = out_dt;
+  p.even = Nout % 2 == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
   // Token columns of a tile, by the rows an expert that has any gets on
   // average (the host does not know the counts):
   //   up to 8     16 columns, six stages in flight: decode, bound by the weights.
   //               A plain product whose tiles would not reach every SM takes
   //               128 weight rows a tile instead of 256.
-  //   up to 24    64 columns, five stages (2000 rows on 128 experts, gate_up
-  //               2880 x 2880: 201 us; 218 with pairs of 96)
-  //   up to 160   96 columns on a pair, two accumulators (8192 ragged rows, gate_up
-  //               2880 x 2880: 273 us, down 148; 287 and 156 with 64, 275 and 152 with
-  //               96 on one CTA, 298 and 164 with 224)
+  //   up to 48    64 columns, five stages; above, uneven counts start to need two
+  //               chunks (35 rows an expert on 128 experts, 2880 x 2880: gate_up 210
+  //               us, down 126; 229 and 132 with pairs of 96.  64 rows an expert,
+  //               counts uneven, the whole layer: 467 us, 421 with pairs)
+  //   up to 160   96 columns on a pair, two accumulators (8192 ragged rows, down
+  //               2880 x 2880: 148 us; 156 with 64, 152 with 96 on one CTA, 164
+  //               with 224)
   //   above       224 columns on a pair, one accumulator: the fewest bytes per
-  //               product (256 rows an expert, 2048 x 2048: 144 us, 160 with 96; 1024
-  //               rows an expert, 2048 x 7168: 1188 us, 1522 with 96, 1322 with 208
-  //               on one CTA, whose token copies and shared-memory reads double)
+  //               product (1024 rows an expert, 2048 x 7168: 1188 us, 1522 with 96, 1322
+  //               with 208 on one CTA, whose token copies and shared-memory reads
+  //               double), unless the product is so short that the epilogue, which
+  //               one accumulator does not hide, costs more than that saves (256
+  //               rows an expert, 768 x 2048, MX out: 161 us, 132 with 96; 16-bit out,
+  //               whose epilogue is half as long: 117 and 122)
   switch (act ? act->kind : MOE_ACT_IDENTITY) {
     case MOE_ACT_SILU_AND_MUL: return go_out<true, MOE_ACT_SILU_AND_MUL>(w, p, s);
     case MOE_ACT_SWIGLU: return go_out<true, MOE_ACT_SWIGLU>(w, p, s);
