@@ -1019,7 +1019,7 @@ moe_status moe_grouped_gemm_mx(const void* a, const void* a_scale, int a_rows,
       (row_to_route ? top_k < 1 : a_rows < M))
     return MOE_ERR_INVALID_ARG;
   const size_t esz = esize(dtype);
-  if (!w || !w_scale || !seg_end || (M > 0 && (!out || (a_rows > 0 && (!a || !a_scale)))))
+  if (!w || !w_scale || !seg_end || (M > 0 && (!out || !a || !a_scale)))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(a_scale) || !aligned(w, 32) || !aligned16(w_scale) ||
       !aligned(out, out_scale ? 16 : esz) || !aligned(bias, esz) || !aligned16(out_scale))

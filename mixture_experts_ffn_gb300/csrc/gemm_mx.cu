@@ -328,6 +328,11 @@ __device__ __forceinline__ bool named_and(int id, int threads, bool v) {
       : "memory");
   return r != 0;
 }
+// Rows of expert e: start[e] .. start[e + 1] (start is clamped to [0, M]); a
+// segment end below the one before it makes the expert empty.
+__device__ __forceinline__ int seg_rows(const int* start, int e) {
+  return max(start[e + 1] - start[e], 0);
+}
 template <int NMAX>
 __device__ __forceinline__ MxTile mx_decode(int t, const int* prefix, const int* start, int E) {
   int lo = 0, hi = E - 1;
@@ -335,7 +340,7 @@ __device__ __forceinline__ MxTile mx_decode(int t, const int* prefix, const int*
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
   }
-  const int s = start[lo], n = start[lo + 1] - s;
+  const int s = start[lo], n = seg_rows(start, lo);
   const int ce = (n + NMAX - 1) / NMAX;  // chunks of equal size, rounded up to 16
   const int local = t - prefix[lo];
   MxTile r;
@@ -347,6 +352,43 @@ __device__ __forceinline__ MxTile mx_decode(int t, const int* prefix, const int*
   r.nv = min(per, n - first);  // 0 for a chunk that rounding left empty
   r.N = max(16, (r.nv + 15) & ~15);
   return r;
+}
+
+// Exclusive prefix over the experts of their tiles (chunks of up to NMAX rows,
+// each crossed with n_ftiles output tiles); prefix has E + 1 entries, scratch
+// 33.  The whole block calls it; returns the total.
+template <int NMAX>
+__device__ int mx_tile_prefix(const int* start, int E, int n_ftiles, int* prefix, int* scratch) {
+  const int per = (E + NUM_THREADS - 1) / NUM_THREADS;
+  const int lo = threadIdx.x * per, hi = min(E, lo + per);
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int mine = 0;
+  for (int e = lo; e < hi; ++e) mine += (seg_rows(start, e) + NMAX - 1) / NMAX * n_ftiles;
+  int v = mine;  // inclusive over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += n;
+  }
+  if (lane == 31) scratch[wid] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int acc = 0;
+    for (int w = 0; w < NUM_THREADS / 32; ++w) {
+      const int x = scratch[w];
+      scratch[w] = acc;
+      acc += x;
+    }
+    scratch[32] = acc;
+  }
+  __syncthreads();
+  int run = scratch[wid] + v - mine;
+  for (int e = lo; e < hi; ++e) {
+    prefix[e] = run;
+    run += (seg_rows(start, e) + NMAX - 1) / NMAX * n_ftiles;
+  }
+  if (threadIdx.x == 0) prefix[E] = scratch[32];
+  return scratch[32];  // the caller synchronises before prefix is read
 }
 
 // 16 consecutive fp32 columns of this thread's TMEM lane
@@ -494,13 +536,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int n_ftiles = (p.Nout + FTU - 1) / FTU;
   const int nkb = p.Kp / BK;
   pdl_wait();
-  // every expert's rows start where the one before ends (never before it)
-  for (int e = threadIdx.x; e <= p.E; e += NUM_THREADS) {
-    int s0 = 0, u = 0;
-    if (e > 0) seg_bounds(p.seg_end, e - 1, p.M, 0, s0, u);
-    sh->start[e] = u;
-  }
-  const int total = build_tile_prefix(p.seg_end, p.E, p.M, NMAX, n_ftiles, sh->prefix, sh->scan_tmp);
+  // every expert's rows start where the one before ends
+  for (int e = threadIdx.x; e <= p.E; e += NUM_THREADS)
+    sh->start[e] = e == 0 ? 0 : min(max(p.seg_end[e - 1], 0), p.M);
+  __syncthreads();
+  const int total = mx_tile_prefix<NMAX>(sh->start, p.E, n_ftiles, sh->prefix, sh->scan_tmp);
   tc_fence_before();
   if constexpr (PAIR) cluster_sync(); else __syncthreads();  // barriers, TMEM, tile list
   tc_fence_after();
@@ -897,7 +937,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                               __uint_as_float(r[HALVES - 1][i]) + b[1],
                               p.limit, p.alpha, p.beta);
           // a pair's second output tile may lie past the padded output
-          if (!PAIR || f0 < mx::padded(p.Nout)) emit16<MXOUT>(v, p, t.m0 + c, nval, f0, lane);
+          if (f0 < mx::padded(p.Nout)) emit16<MXOUT>(v, p, t.m0 + c, nval, f0, lane);
         } else {
 #pragma unroll
           for (int h = 0; h < HALVES; ++h) {

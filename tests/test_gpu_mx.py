@@ -432,6 +432,49 @@ def test_gemm_mx_past_32_bit_offsets(moe):
     assert torch.equal(got, moe.moe_grouped_gemm_mx(*few, *one, segments([100]), N))
 
 
+@pytest.mark.parametrize("mx_out", [False, True])
+@pytest.mark.parametrize("ends", [[70, 20, 40, 300], [-5, 10, 5, 64], [500, 900, -3, 2], [0, 0, 0, -1]])
+def test_gemm_mx_clamps_segment_ends(moe, ends, mx_out):
+    """Segment ends outside [0, M] or below the one before are clamped: an expert owns the rows
+    from the end before it to its own, none if that is behind it; nothing else is written."""
+    M, N, K = 64, 144, 256
+    g = gen(M)
+    a = moe.moe_mx_quantize(torch.randn((M, K), generator=g, device="cuda"))
+    w = mx_weights(moe, g, 4, 2 * N, K)
+    seg = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    act = moe.act_params()
+    Np = moe.moe_mx_columns(N)
+    fill = 0x5A
+    out = torch.full((M + 2, Np if mx_out else 2 * N), fill, dtype=torch.uint8, device="cuda")
+    sc = torch.full((M + 2, Np // 32), fill, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    if mx_out:
+        moe.moe_grouped_gemm_mx(*a, *w, seg, N, act=act, mx_out=True, out=out[:M], out_scale=sc[:M],
+                                ws=ws)
+    else:
+        moe.moe_grouped_gemm_mx(*a, *w, seg, N, act=act, out=out[:M].view(torch.bfloat16), ws=ws)
+    assert moe.moe_sync_status(ws) == moe.MOE_OK
+    start = [0] + [min(max(e, 0), M) for e in ends]
+    want = torch.full_like(out, fill)
+    for e in range(4):  # an expert that several ranges reach: each on its own, in expert order
+        lo, hi = start[e], start[e + 1]
+        if hi > lo:
+            one = torch.tensor([hi - lo], dtype=torch.int32, device="cuda")
+            part = (a[0][lo:hi].clone(), a[1][lo:hi].clone())  # aligned copies
+            r = moe.moe_grouped_gemm_mx(*part, w[0][e:e + 1], w[1][e:e + 1], one, N, act=act,
+                                        mx_out=mx_out)
+            if mx_out:
+                want[lo:hi] = r[0].view(torch.uint8)
+            else:
+                want[lo:hi] = r.view(torch.uint8)
+    seen = torch.zeros(M + 2, dtype=torch.int32)
+    for e in range(4):
+        seen[start[e]:max(start[e + 1], start[e])] += 1
+    once = (seen <= 1).cuda()  # rows that two ranges share hold either's result
+    assert torch.equal(out[once], want[once])
+    assert (out[M:] == fill).all() and (sc[M:] == fill).all()
+
+
 def test_gemm_mx_most_experts(moe):
     counts = [i % 3 for i in range(1024)]
     run_gemm(moe, counts, 40, 128)
