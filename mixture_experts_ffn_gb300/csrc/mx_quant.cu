@@ -1,8 +1,11 @@
 // Rows to microscaled floats and back (mx_dev.cuh holds the formats and their
 // scale rules).  One pass: eight consecutive columns a thread, so four
 // neighbouring lanes own a 32-column block and agree on its scale with two
-// shuffles.  Bound by HBM: a bf16 element moves 2 bytes in and 17/16 (e4m3)
-// or 17/32 (e2m1) out.
+// shuffles.  Bound by HBM: a bf16 element moves 2 bytes in and 33/32 (e4m3)
+// or 17/32 (e2m1) out.  184320 x 2880 bf16: to e2m1 257 us, to e4m3 286, back
+// from e2m1 252 (5.2 to 5.7 TB/s, a torch copy in the same harness 5.2); the
+// next item's load is issued before an item is converted (268 and 257 us
+// without), four items a thread in flight were slower (370 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -16,8 +19,7 @@ constexpr int kThreads = 256;
 // Item i: columns 8 (i % ipr) .. of row i / ipr, ipr = Kp / 8 (a multiple of
 // 16, so a block's four lanes never straddle two rows).  A thread's next item
 // is a grid's width on: row and column advance by fixed amounts, so the loop
-// divides nothing (the division was a fifth of its instructions, and the
-// kernel issues nearly as long as it waits for HBM).
+// divides nothing (286 us to e2m1 with a division an item).
 struct Walk {
   uint32_t i, row, col, ipr, step, drow, dcol;
   __device__ __forceinline__ explicit Walk(uint32_t ipr_) {
@@ -57,31 +59,53 @@ __global__ void __launch_bounds__(kThreads)
   // the lanes of a warp leave the loop together: items is a multiple of 16
   // and a block is four lanes, so a shuffle's partners are in or out as one
   const uint32_t mask = 0xfu << (threadIdx.x & 28);
-  for (Walk w((uint32_t)Kp / 8); w.i < items; w.next()) {
-    const T* xr = x + (int64_t)w.row * stride;
-    const int c0 = (int)w.col * 8;
-    float v[8];
-    uint32_t amax = 0;
-    if constexpr (VEC && std::is_same<T, __nv_bfloat16>::value) {
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (c0 < K) u = __ldcs(reinterpret_cast<const uint4*>(xr + c0));
-      amax = amax_bf16x8(u);
-      v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
-      v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
-    } else {
-      mx::load8<T, VEC>(xr, c0, K, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, mx::abs_bits(v[j]));
-    }
+  auto finish = [&](uint32_t i, float (&v)[8], uint32_t amax) {
     amax = max(amax, __shfl_xor_sync(mask, amax, 1));
     amax = max(amax, __shfl_xor_sync(mask, amax, 2));
     const uint32_t byte = mx::scale_byte<E2M1>(amax);
     mx::scale8(v, mx::inv_scale(byte));
     if constexpr (E2M1)
-      reinterpret_cast<uint32_t*>(codes)[w.i] = mx::e2m1x8(v);
+      reinterpret_cast<uint32_t*>(codes)[i] = mx::e2m1x8(v);
     else
-      reinterpret_cast<uint2*>(codes)[w.i] = mx::e4m3x8(v);
-    if ((threadIdx.x & 3) == 0) scales[w.i >> 2] = (uint8_t)byte;
+      reinterpret_cast<uint2*>(codes)[i] = mx::e4m3x8(v);
+    if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+  };
+  Walk w((uint32_t)Kp / 8);
+  if constexpr (VEC && sizeof(T) == 2) {
+    // the next item's 16 bytes are in flight while this one is converted
+    auto fetch = [&]() {
+      const int c0 = (int)w.col * 8;
+      return w.i < items && c0 < K
+                 ? __ldcs(reinterpret_cast<const uint4*>(x + (int64_t)w.row * stride + c0))
+                 : make_uint4(0, 0, 0, 0);
+    };
+    uint4 next = fetch();
+    while (w.i < items) {
+      const uint4 u = next;
+      const uint32_t i = w.i;
+      w.next();
+      next = fetch();
+      constexpr bool F16 = std::is_same<T, __half>::value;
+      float v[8] = {lo16<F16>(u.x), hi16<F16>(u.x), lo16<F16>(u.y), hi16<F16>(u.y),
+                    lo16<F16>(u.z), hi16<F16>(u.z), lo16<F16>(u.w), hi16<F16>(u.w)};
+      uint32_t amax = 0;
+      if constexpr (F16) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = max(amax, mx::abs_bits(v[j]));
+      } else {
+        amax = amax_bf16x8(u);
+      }
+      finish(i, v, amax);
+    }
+  } else {
+    for (; w.i < items; w.next()) {
+      float v[8];
+      mx::load8<T, VEC>(x + (int64_t)w.row * stride, (int)w.col * 8, K, v);
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max(amax, mx::abs_bits(v[j]));
+      finish(w.i, v, amax);
+    }
   }
 }
 
@@ -91,15 +115,26 @@ __global__ void __launch_bounds__(kThreads)
                          uint32_t items, int K, int Kp, T* __restrict__ out) {
   pdl_launch();
   pdl_wait();
-  for (Walk w((uint32_t)Kp / 8); w.i < items; w.next()) {
-    const int c0 = (int)w.col * 8;
-    if (c0 >= K) continue;
-    const float s = mx::scale_value(scales[w.i >> 2]);
-    uint2 q;
+  Walk w((uint32_t)Kp / 8);
+  uint2 next = make_uint2(0, 0);
+  uint32_t next_byte = 0;
+  auto fetch = [&]() {  // the next item's codes and scale, in flight while this one is converted
+    if (w.i >= items) return;
     if constexpr (E2M1)
-      q.x = reinterpret_cast<const uint32_t*>(codes)[w.i];
+      next.x = __ldcs(reinterpret_cast<const uint32_t*>(codes) + w.i);
     else
-      q = reinterpret_cast<const uint2*>(codes)[w.i];
+      next = __ldcs(reinterpret_cast<const uint2*>(codes) + w.i);
+    next_byte = scales[w.i >> 2];
+  };
+  fetch();
+  while (w.i < items) {
+    const uint2 q = next;
+    const float s = mx::scale_value(next_byte);
+    const int c0 = (int)w.col * 8;
+    T* o = out + (int64_t)w.row * K;
+    w.next();
+    fetch();
+    if (c0 >= K) continue;
     float v[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -113,7 +148,7 @@ __global__ void __launch_bounds__(kThreads)
       v[2 * j] = f.x * s;
       v[2 * j + 1] = f.y * s;
     }
-    mx::store8<T, VEC>(out + (int64_t)w.row * K, c0, K, v);
+    mx::store8<T, VEC>(o, c0, K, v);
   }
 }
 
