@@ -171,6 +171,12 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _fits(t, n: int, size: int, what: str):
+    """t (given by the caller) holds n elements of `size` bytes."""
+    if t is not None and (t.numel() != n or t.element_size() != size):
+        raise ValueError(f"{what} takes {n} elements of {size} bytes")
+
+
 def _cuda(*ts):
     for t in ts:
         if t is not None:
@@ -566,6 +572,8 @@ def moe_mx_quantize(x, format: int = MOE_MX_E4M3, codes=None, scales=None):
     if scales is None:
         scales = torch.empty((*lead, Kp // 32), dtype=torch.float8_e8m0fnu, device=x.device)
     _cuda(codes, scales)
+    _fits(codes, rows * (Kp // 2 if format == MOE_MX_E2M1 else Kp), 1, "codes")
+    _fits(scales, rows * (Kp // 32), 1, "scales")
     _check("moe_mx_quantize",
            lib.moe_mx_quantize(x.data_ptr(), rows, K, stride, _dt(x), format, codes.data_ptr(),
                                scales.data_ptr(), _stream_of(x)))
@@ -583,11 +591,16 @@ def moe_mx_dequantize(codes, scales, K: int, format=None, dtype=torch.bfloat16, 
     if codes.shape[-1] != (Kp // 2 if format == MOE_MX_E2M1 else Kp) or \
             scales.shape[-1] * 32 != Kp or codes.shape[:-1] != scales.shape[:-1]:
         raise ValueError("codes and scales are not an MX tensor of K columns")
+    rows = scales.numel() // (Kp // 32)
+    _fits(codes, codes.numel(), 1, "codes")
+    _fits(scales, scales.numel(), 1, "scales")
     if out is None:
         out = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
+    else:
+        _cuda(out)
+        _fits(out, rows * K, out.element_size(), "out")
     _check("moe_mx_dequantize",
-           lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), scales.numel() // (Kp // 32),
-                                 K, format, _dt(out), out.data_ptr(), _stream_of(codes)))
+           lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), rows, K, format, _dt(out), out.data_ptr(), _stream_of(codes)))
     return out
 
 
@@ -609,10 +622,20 @@ def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_
         out = torch.empty_like(x)
     elif out is False:
         out = None
+    else:
+        _cuda(out)
+        _fits(out, T * H, x.element_size(), "out")
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(x)
+    else:
+        _fits(residual_out, T * H, x.element_size(), "residual_out")
     if quant != MOE_QUANT_NONE:
         Hp = moe_mx_columns(H)
+        _fits(codes, T * Hp, 1, "codes")
+        if quant == MOE_QUANT_MX_E4M3:
+            _fits(scales, T * (Hp // 32), 1, "scales")
+        else:
+            _fits(scales, T * (Hp // 128), 4, "scales")
         if codes is None:
             codes = torch.empty((T, Hp), dtype=torch.float8_e4m3fn, device=x.device)
         if scales is None:
@@ -649,14 +672,22 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
         raise ValueError("operands are not MX tensors of matching extents")
     if bias is not None and bias.dtype != dtype:
         raise TypeError("bias takes the output's dtype")
+    if not a.element_size() == a_scale.element_size() == w.element_size() == \
+            w_scale.element_size() == 1 or seg_end.dtype != torch.int32 or \
+            (row_to_route is not None and row_to_route.dtype != torch.int32):
+        raise TypeError("codes and scales are bytes, seg_end and row_to_route int32")
     if mx_out:
         Np = moe_mx_columns(N)
+        _fits(out, M * Np, 1, "out")
+        _fits(out_scale, M * (Np // 32), 1, "out_scale")
         if out is None:
             out = torch.empty((M, Np), dtype=torch.float8_e4m3fn, device=a.device)
         if out_scale is None:
             out_scale = torch.empty((M, Np // 32), dtype=torch.float8_e8m0fnu, device=a.device)
     elif out is None:
         out = torch.empty((M, N), dtype=dtype, device=a.device)
+    else:
+        _fits(out, M * N, 4 if dtype == torch.float32 else 2, "out")
     if ws is None:
         ws = _ws(lib.moe_grouped_gemm_mx_workspace_size(M, N, Kp, E), a.device)
     dt = MOE_BF16 if dtype == torch.bfloat16 else MOE_F16 if dtype == torch.float16 else MOE_F32
@@ -695,8 +726,18 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
     for b, n in ((b_gate_up, E * N1), (b_down, E * H)):
         if b is not None and (b.dtype != dtype or b.numel() != n):
             raise ValueError("a bias is [E, rows] in the output's dtype")
+    if not hidden.element_size() == hidden_scale.element_size() == w_gate_up.element_size() == \
+            w_gate_up_scale.element_size() == w_down.element_size() == \
+            w_down_scale.element_size() == 1:
+        raise TypeError("codes and scales are bytes")
+    _fits(correction_bias, E, 4, "correction_bias")
+    _fits(expert_ids, T * p.top_k, 4, "expert_ids")
+    _fits(topk_weights_out, T * p.top_k, 4, "topk_weights_out")
+    _fits(topk_ids_out, T * p.top_k, 4, "topk_ids_out")
     if out is None:
         out = torch.empty((T, H), dtype=dtype, device=hidden.device)
+    elif out.dtype != dtype or out.numel() != T * H:
+        raise ValueError("out is [T, H] in dtype")
     if ws is None:
         ws = _ws(lib.moe_workspace_size_mx(T, H, F, E, p.top_k), hidden.device)
     rp = p if p.dtype == _dt(logits) else _rp(p, logits)

@@ -583,3 +583,45 @@ def test_layer_after_the_norm_with_fixed_experts(moe):
     assert torch.equal(out, moe.moe_combine(y, tw, m["route_to_row"]).to(torch.bfloat16))
     empty = moe.moe_ffn_forward_mx(n["codes"][:0], n["scales"][:0], logits[:0], *w1, *w2, H, F, p, ap)
     assert empty.shape == (0, H)
+
+
+# ------------------------------------------------------------------ the binding's refusals
+def test_binding_refuses_mismatched_tensors(moe):
+    g = gen(2)
+    x = torch.randn((8, 256), generator=g, device="cuda").to(torch.bfloat16)
+    one = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    a = moe.moe_mx_quantize(x)
+    w = mx_weights(moe, g, 2, 64, 256)
+    seg = segments([3, 5])
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    bad = [
+        lambda: moe.moe_mx_quantize(x, codes=small),
+        lambda: moe.moe_mx_quantize(x, scales=small),
+        lambda: moe.moe_mx_quantize(x.t()),
+        lambda: moe.moe_mx_dequantize(*a, 300),
+        lambda: moe.moe_mx_dequantize(*a, 256, out=small),
+        lambda: moe.moe_add_rms_norm(x, one, out=small),
+        lambda: moe.moe_add_rms_norm(x, one, quant=1, codes=small),
+        lambda: moe.moe_add_rms_norm(x, one, quant=2, scales=small),
+        lambda: moe.moe_add_rms_norm(x, one.float()),
+        lambda: moe.moe_add_rms_norm(x, one[:128]),
+        lambda: moe.moe_add_rms_norm(x, one, residual=x[:4]),
+        lambda: moe.moe_add_rms_norm(x, one, residual=x, residual_out=small),
+        lambda: moe.moe_grouped_gemm_mx(*a, *w, seg, 65),
+        lambda: moe.moe_grouped_gemm_mx(*a, *w, seg, 64, act=moe.act_params()),
+        lambda: moe.moe_grouped_gemm_mx(*a, *w, seg[:1], 64),
+        lambda: moe.moe_grouped_gemm_mx(*a, *w, seg.long(), 64),
+        lambda: moe.moe_grouped_gemm_mx(x, a[1], *w, seg, 64),
+        lambda: moe.moe_grouped_gemm_mx(*a, *w, seg, 64, out=small),
+        lambda: moe.moe_grouped_gemm_mx(*a, *w, seg, 64, mx_out=True, out=small),
+        lambda: moe.moe_grouped_gemm_mx(*a, *w, seg, 64, bias=torch.zeros((2, 64), device="cuda")),
+        lambda: moe.moe_ffn_forward_mx(*a, torch.zeros((8, 2), device="cuda"), *w, *w, 256, 64,
+                                       moe.route_params(1), moe.act_params()),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises((ValueError, TypeError)):
+            f()
+            raise AssertionError(f"call {i} was accepted")
+    with pytest.raises(moe.MoEError) as e:  # scales off a 16-byte boundary
+        moe.moe_grouped_gemm_mx(a[0][1:], a[1].view(torch.uint8)[1:], *w, segments([3, 4]), 64)
+    assert e.value.status == moe.MOE_ERR_UNSUPPORTED
