@@ -3,7 +3,7 @@
 // and rounded once.  Keeping y in float32 leaves the layer a single rounding
 // of its output (error 1.7e-3 of the result in bfloat16; 2.4e-3 with y rounded
 // too) for 2 more bytes a value of y: 2048 x 4 routes of 2880 columns, 94 MB,
-// stay inside the L2.  Bound by that traffic: y once in, out once.
+// mostly stay inside the L2.  Bound by that traffic: y once in, out once.
 #include <algorithm>
 #include <type_traits>
 

@@ -564,16 +564,18 @@ def moe_mx_quantize(x, format: int = MOE_MX_E4M3, codes=None, scales=None):
         raise ValueError("moe_mx_quantize takes contiguous rows")
     Kp = moe_mx_columns(K)
     rows = x.numel() // K if K else 0
-    lead = x.shape[:-1]
+    lead, wide = x.shape[:-1], Kp // 2 if format == MOE_MX_E2M1 else Kp
     if codes is None:
-        codes = (torch.empty((*lead, Kp // 2), dtype=torch.uint8, device=x.device)
-                 if format == MOE_MX_E2M1 else
-                 torch.empty((*lead, Kp), dtype=torch.float8_e4m3fn, device=x.device))
+        codes = torch.empty((*lead, wide), device=x.device,
+                            dtype=torch.uint8 if format == MOE_MX_E2M1 else torch.float8_e4m3fn)
+    else:
+        _cuda(codes)
+        _fits(codes, rows * wide, 1, "codes")
     if scales is None:
         scales = torch.empty((*lead, Kp // 32), dtype=torch.float8_e8m0fnu, device=x.device)
-    _cuda(codes, scales)
-    _fits(codes, rows * (Kp // 2 if format == MOE_MX_E2M1 else Kp), 1, "codes")
-    _fits(scales, rows * (Kp // 32), 1, "scales")
+    else:
+        _cuda(scales)
+        _fits(scales, rows * (Kp // 32), 1, "scales")
     _check("moe_mx_quantize",
            lib.moe_mx_quantize(x.data_ptr(), rows, K, stride, _dt(x), format, codes.data_ptr(),
                                scales.data_ptr(), _stream_of(x)))
@@ -625,23 +627,21 @@ def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_
     else:
         _cuda(out)
         _fits(out, T * H, x.element_size(), "out")
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
-    else:
+    if residual_out is not None:
         _fits(residual_out, T * H, x.element_size(), "residual_out")
+    elif residual is not None:
+        residual_out = torch.empty_like(x)
     if quant != MOE_QUANT_NONE:
-        Hp = moe_mx_columns(H)
-        _fits(codes, T * Hp, 1, "codes")
-        if quant == MOE_QUANT_MX_E4M3:
-            _fits(scales, T * (Hp // 32), 1, "scales")
-        else:
-            _fits(scales, T * (Hp // 128), 4, "scales")
+        Hp, mx = moe_mx_columns(H), quant == MOE_QUANT_MX_E4M3
         if codes is None:
             codes = torch.empty((T, Hp), dtype=torch.float8_e4m3fn, device=x.device)
+        else:
+            _fits(codes, T * Hp, 1, "codes")
         if scales is None:
-            scales = (torch.empty((T, Hp // 32), dtype=torch.float8_e8m0fnu, device=x.device)
-                      if quant == MOE_QUANT_MX_E4M3 else
-                      torch.empty((T, Hp // 128), dtype=torch.float32, device=x.device))
+            scales = torch.empty((T, Hp // (32 if mx else 128)), device=x.device,
+                                 dtype=torch.float8_e8m0fnu if mx else torch.float32)
+        else:
+            _fits(scales, T * (Hp // (32 if mx else 128)), 1 if mx else 4, "scales")
     _check("moe_add_rms_norm",
            lib.moe_add_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, _dt(x), eps,
                                 quant, _ptr(residual_out), _ptr(out), _ptr(codes), _ptr(scales),
