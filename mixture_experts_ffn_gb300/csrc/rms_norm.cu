@@ -7,8 +7,8 @@
 // The mean is taken over the ROUNDED h, so the result is the norm of the
 // residual stream that is stored, and equal to adding first and normalising
 // later.  The codes come from the float32 y, not from its rounded copy: one
-// rounding instead of two.  Squares are summed in float32, eight columns a
-// thread at a time, then across the row's threads in a fixed order.
+// rounding instead of two.  Squares are summed in float32, a chain for each of
+// a thread's eight columns, then across lanes and warps in a fixed order.
 //
 // Bound by HBM: x and r in, h, y and the codes out, each once; a row stays in
 // registers between the sum and the scaling.  8192 x 7168 bf16, all outputs:
@@ -33,27 +33,42 @@ struct NormArgs {
   float eps;
 };
 
-// Sum over the `warps` warps of a row group (every thread gets it).
-__device__ __forceinline__ float group_sum(float v, float* red, int warps, int warp, int lane) {
-  v = warp_sum(v);
-  if (warps == 1) return v;
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  float s = lane < warps ? red[lane] : 0.0f;
-  return warp_sum(s);
-}
-
-// 1 / sqrt(m) as hi + lo: one Newton step on rsqrtf's value, its residual
-// 1 - m hi^2 taken from the products' exact errors.  An 8-bit code next to a tie
-// goes by the last bits of y; with a plain float32 root and two rounded products
-// more codes fell on the other side than in 64 bits.
-struct Root {
+// A sum as hi + lo; add keeps the rounding error of hi (Knuth's two-sum).
+struct Two {
   float hi, lo;
 };
-__device__ __forceinline__ Root inv_root(float m) {
-  Root r;
-  r.hi = rsqrtf(m);
-  const float t = m * r.hi, e = fmaf(-t, r.hi, 1.0f) - fmaf(m, r.hi, -t) * r.hi;
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  return {s, a.lo + b.lo + ((a.hi - (s - t)) + (b.hi - t))};
+}
+// Sum over the `warps` warps of a row group (every thread gets it): plain
+// float32 inside a warp, whose sum is a small part of the row's, with the
+// rounding errors kept across warps, where they would count in full.
+__device__ __forceinline__ Two group_sum(float v, float* red, int warps, int warp, int lane) {
+  v = warp_sum(v);
+  if (warps == 1) return {v, 0.0f};
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  int span = 2;  // lanes that hold one copy of all the warps' sums
+  while (span < warps) span *= 2;
+  const int at = lane & (span - 1);
+  Two s{at < warps ? red[at] : 0.0f, 0.0f};
+  for (int o = span / 2; o > 0; o >>= 1)
+    s = add(s, Two{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)});
+  return s;
+}
+
+// 1 / sqrt(sum / n + eps) as hi + lo: one Newton step on rsqrtf's value, its
+// residual 1 - m hi^2 taken from the products' exact errors.  An 8-bit code next
+// to a tie goes by the last bits of y: with a plain float32 mean and root and two
+// rounded products more codes fell on the other side than 64 bits put them.
+__device__ __forceinline__ Two inv_root(Two sum, float n, float eps) {
+  const float q = sum.hi / n;
+  const Two m = add(Two{q, (fmaf(-q, n, sum.hi) + sum.lo) / n}, Two{eps, 0.0f});
+  Two r;
+  r.hi = rsqrtf(m.hi);
+  const float t = m.hi * r.hi;
+  const float e = fmaf(-t, r.hi, 1.0f) - (fmaf(m.hi, r.hi, -t) + m.lo * r.hi) * r.hi;
   const float lo = 0.5f * r.hi * e;
   r.lo = isfinite(lo) ? lo : 0.0f;  // m zero, infinite or NaN: hi alone
   return r;
@@ -77,7 +92,6 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024)
   const T* x = static_cast<const T*>(p.x) + (size_t)row * H;
   const T* r = p.r ? static_cast<const T*>(p.r) + (size_t)row * H : nullptr;
   float v[ITEMS][8];
-  float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) mx::load8<T, VEC>(x, (t0 + i * nthr) * 8, H, v[i]);
   if (r) {
@@ -92,12 +106,16 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024)
       mx::store8<T, VEC>(h, (t0 + i * nthr) * 8, H, v[i]);
     }
   }
+  float ss[8];
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i)
+  for (int j = 0; j < 8; ++j) {
+    ss[j] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-  ss = group_sum(ss, red, nthr >> 5, warp, lane);
-  const Root root = inv_root(ss / (float)H + p.eps);
+    for (int i = 0; i < ITEMS; ++i) ss[j] = fmaf(v[i][j], v[i][j], ss[j]);
+  }
+  const float mine = ((ss[0] + ss[1]) + (ss[2] + ss[3])) + ((ss[4] + ss[5]) + (ss[6] + ss[7]));
+  const Two sum = group_sum(mine, red, nthr >> 5, warp, lane);
+  const Two root = inv_root(sum, (float)H, p.eps);
   T* y = p.y ? static_cast<T*>(p.y) + (size_t)row * H : nullptr;
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
