@@ -157,14 +157,18 @@ def _stream_of(t: torch.Tensor) -> int:
     return _raw_stream(t.device.index)
 
 
-def _dt(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+def _dtype(d: torch.dtype) -> int:
+    if d == torch.bfloat16:
         return MOE_BF16
-    if t.dtype == torch.float32:
+    if d == torch.float32:
         return MOE_F32
-    if t.dtype == torch.float16:
+    if d == torch.float16:
         return MOE_F16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    raise TypeError(f"unsupported dtype {d}")
+
+
+def _dt(t: torch.Tensor) -> int:
+    return _dtype(t.dtype)
 
 
 def _ptr(t) -> Optional[int]:
@@ -659,9 +663,11 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
     """Grouped GEMM of MX e4m3 rows a [R, Kp] by MX e2m1 weights w [E, N1, Kp / 2]
     over the tight layout; row m is a[row_to_route[m] // top_k] when row_to_route
     is given.  Returns out [M, N] in dtype, or with mx_out the MX e4m3 rows
-    (codes [M, Np], scales [M, Np / 32])."""
+    (codes [M, Np], scales [M, Np / 32]).  dtype, the type of out and of the
+    bias, is bfloat16, float16 or float32."""
     lib = load_library()
     _cuda(a, a_scale, w, w_scale, seg_end, bias, row_to_route, out, out_scale)
+    dt = _dtype(dtype)
     R, Kp = a.shape
     E, N1, half = w.shape
     M = R if row_to_route is None else row_to_route.numel()
@@ -690,7 +696,6 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
         _fits(out, M * N, 4 if dtype == torch.float32 else 2, "out")
     if ws is None:
         ws = _ws(lib.moe_grouped_gemm_mx_workspace_size(M, N, Kp, E), a.device)
-    dt = MOE_BF16 if dtype == torch.bfloat16 else MOE_F16 if dtype == torch.float16 else MOE_F32
     _check("moe_grouped_gemm_mx",
            lib.moe_grouped_gemm_mx(a.data_ptr(), a_scale.data_ptr(), R, _ptr(row_to_route), top_k,
                                    w.data_ptr(), w_scale.data_ptr(), _ptr(bias),

@@ -1,0 +1,80 @@
+"""The Python binding's checks of the microscaled operators, on the CPU: the
+library behind the binding is a stand-in that records the calls it gets, so a
+call that must be refused is seen to get no further, and no kernel runs."""
+import pytest
+import torch
+
+
+class Recorder:
+    """Stands in for libmoe.so: every entry point returns MOE_OK, a workspace
+    size 4096."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            self.calls.append((name, args))
+            return 4096 if "workspace_size" in name else 0
+
+        return entry
+
+    def launched(self):
+        return [n for n, _ in self.calls if "workspace_size" not in n]
+
+
+@pytest.fixture
+def moe(monkeypatch):
+    from mixture_experts_ffn_gb300 import moe as m
+
+    def as_if_on_the_gpu(*ts):  # the binding's own check but for the device
+        for t in ts:
+            if t is not None and (t.is_meta or not t.is_contiguous()):
+                raise ValueError("libmoe takes contiguous CUDA tensors only")
+
+    rec = Recorder()
+    monkeypatch.setattr(m, "load_library", lambda: rec)
+    monkeypatch.setattr(m, "_cuda", as_if_on_the_gpu)
+    monkeypatch.setattr(m, "_stream_of", lambda t: 0)
+    m.recorder = rec
+    yield m
+    del m.recorder
+
+
+def u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+E, N, K, M = 2, 64, 256, 8
+
+
+def product(moe, **kw):
+    """A product's call with every argument right but those in kw."""
+    args = dict(a=u8(M, K), a_scale=u8(M, K // 32), w=u8(E, N, K // 2), w_scale=u8(E, N, K // 32),
+                seg_end=torch.tensor([3, M], dtype=torch.int32), N=N)
+    args.update(kw)
+    return moe.moe_grouped_gemm_mx(**args)
+
+
+def refused(moe, call, error=(TypeError, ValueError)):
+    before = len(moe.recorder.launched())
+    with pytest.raises(error):
+        call()
+    assert len(moe.recorder.launched()) == before, "the library was called"
+
+
+def test_the_right_calls_pass(moe):
+    for dt in (torch.bfloat16, torch.float16, torch.float32):
+        assert product(moe, dtype=dt).dtype == dt
+        product(moe, dtype=dt, mx_out=True, bias=torch.zeros((E, N), dtype=dt))
+    assert moe.recorder.launched() == ["moe_grouped_gemm_mx"] * 6
+
+
+@pytest.mark.parametrize("mx_out", [False, True])
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.float8_e4m3fn, torch.int16, torch.int32,
+                                   torch.float64, torch.complex64])
+def test_product_refuses_output_types_it_does_not_write(moe, dtype, mx_out):
+    """The kernel writes bf16, f16 or f32 (4 bytes); a buffer of another type holds less, or other
+    numbers."""
+    refused(moe, lambda: product(moe, dtype=dtype, mx_out=mx_out), TypeError)
+    refused(moe, lambda: product(moe, dtype=dtype, out=torch.zeros((M, N), dtype=dtype)), TypeError)
