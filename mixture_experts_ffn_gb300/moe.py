@@ -690,6 +690,8 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
             out = torch.empty((M, Np), dtype=torch.float8_e4m3fn, device=a.device)
         if out_scale is None:
             out_scale = torch.empty((M, Np // 32), dtype=torch.float8_e8m0fnu, device=a.device)
+    elif out_scale is not None:  # to the library a scale buffer asks for MX rows
+        raise ValueError("out_scale goes with mx_out")
     elif out is None:
         out = torch.empty((M, N), dtype=dtype, device=a.device)
     else:

@@ -78,3 +78,11 @@ def test_product_refuses_output_types_it_does_not_write(moe, dtype, mx_out):
     numbers."""
     refused(moe, lambda: product(moe, dtype=dtype, mx_out=mx_out), TypeError)
     refused(moe, lambda: product(moe, dtype=dtype, out=torch.zeros((M, N), dtype=dtype)), TypeError)
+
+
+def test_product_refuses_an_output_scale_without_mx_output(moe):
+    """The C entry takes a scale buffer as the request for MX rows: it would write [M, Np] codes into
+    the [M, N] output (128 bytes a row where N = 1 in bf16 has 2) and scales past a short buffer."""
+    for osc in (u8(1), u8(M, 4)):
+        refused(moe, lambda: product(moe, out_scale=osc), ValueError)
+    product(moe, mx_out=True, out=u8(M, 128), out_scale=u8(M, 4))
