@@ -181,6 +181,12 @@ def _fits(t, n: int, size: int, what: str):
         raise ValueError(f"{what} takes {n} elements of {size} bytes")
 
 
+def _typed(t, dtype: torch.dtype, what: str):
+    """t (given by the caller, or None) is of the type the library reads or writes there."""
+    if t is not None and t.dtype != dtype:
+        raise TypeError(f"{what} takes {dtype}")
+
+
 def _cuda(*ts):
     for t in ts:
         if t is not None:
@@ -630,8 +636,10 @@ def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_
         out = None
     else:
         _cuda(out)
+        _typed(out, x.dtype, "out")
         _fits(out, T * H, x.element_size(), "out")
     if residual_out is not None:
+        _typed(residual_out, x.dtype, "residual_out")
         _fits(residual_out, T * H, x.element_size(), "residual_out")
     elif residual is not None:
         residual_out = torch.empty_like(x)
@@ -645,6 +653,8 @@ def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_
             scales = torch.empty((T, Hp // (32 if mx else 128)), device=x.device,
                                  dtype=torch.float8_e8m0fnu if mx else torch.float32)
         else:
+            if not mx:
+                _typed(scales, torch.float32, "scales")
             _fits(scales, T * (Hp // (32 if mx else 128)), 1 if mx else 4, "scales")
     _check("moe_add_rms_norm",
            lib.moe_add_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, _dt(x), eps,
@@ -695,7 +705,8 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
     elif out is None:
         out = torch.empty((M, N), dtype=dtype, device=a.device)
     else:
-        _fits(out, M * N, 4 if dtype == torch.float32 else 2, "out")
+        _typed(out, dtype, "out")
+        _fits(out, M * N, out.element_size(), "out")
     if ws is None:
         ws = _ws(lib.moe_grouped_gemm_mx_workspace_size(M, N, Kp, E), a.device)
     _check("moe_grouped_gemm_mx",

@@ -86,3 +86,32 @@ def test_product_refuses_an_output_scale_without_mx_output(moe):
     for osc in (u8(1), u8(M, 4)):
         refused(moe, lambda: product(moe, out_scale=osc), ValueError)
     product(moe, mx_out=True, out=u8(M, 128), out_scale=u8(M, 4))
+
+
+T, H = 4, 256
+
+
+def norm(moe, dtype=torch.bfloat16, residual=False, **kw):
+    x = torch.zeros((T, H), dtype=dtype)
+    return moe.moe_add_rms_norm(x, torch.ones(H, dtype=dtype),
+                                residual=torch.zeros_like(x) if residual else None, **kw)
+
+
+def test_outputs_of_another_type_of_the_same_size_are_refused(moe):
+    """The kernels write the type the call asks for: the bits of one 16-bit type read as another are
+    other numbers."""
+    h16, i16 = torch.zeros((M, N), dtype=torch.float16), torch.zeros((M, N), dtype=torch.int16)
+    i32 = torch.zeros((M, N), dtype=torch.int32)
+    product(moe, dtype=torch.float16, out=h16)
+    refused(moe, lambda: product(moe, out=h16))
+    refused(moe, lambda: product(moe, out=i16))
+    refused(moe, lambda: product(moe, dtype=torch.float32, out=i32))
+    for dt, other in ((torch.bfloat16, torch.float16), (torch.float16, torch.bfloat16),
+                      (torch.float32, torch.int32)):
+        right, wrong = torch.zeros((T, H), dtype=dt), torch.zeros((T, H), dtype=other)
+        norm(moe, dt, out=right)
+        refused(moe, lambda: norm(moe, dt, out=wrong))
+        norm(moe, dt, residual=True, residual_out=right)
+        refused(moe, lambda: norm(moe, dt, residual=True, residual_out=wrong))
+    refused(moe, lambda: norm(moe, quant=moe.MOE_QUANT_E4M3_BLOCK128,
+                              scales=torch.zeros((T, H // 128), dtype=torch.int32)))
