@@ -676,7 +676,7 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
     (codes [M, Np], scales [M, Np / 32]).  dtype, the type of out and of the
     bias, is bfloat16, float16 or float32."""
     lib = load_library()
-    _cuda(a, a_scale, w, w_scale, seg_end, bias, row_to_route, out, out_scale)
+    _cuda(a, a_scale, w, w_scale, seg_end, bias, row_to_route, out, out_scale, ws)
     dt = _dtype(dtype)
     R, Kp = a.shape
     E, N1, half = w.shape
@@ -731,7 +731,7 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
     e2m1 [E, N1, Hp / 2] and [E, H, Fp / 2]; returns out [T, H] in dtype."""
     lib = load_library()
     _cuda(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale, w_down, w_down_scale,
-          correction_bias, expert_ids, b_gate_up, b_down, out)
+          correction_bias, expert_ids, b_gate_up, b_down, out, topk_weights_out, topk_ids_out, ws)
     T, Hp = hidden.shape
     E, N1, half = w_gate_up.shape
     Fp = moe_mx_columns(F)

@@ -115,3 +115,43 @@ def test_outputs_of_another_type_of_the_same_size_are_refused(moe):
         refused(moe, lambda: norm(moe, dt, residual=True, residual_out=wrong))
     refused(moe, lambda: norm(moe, quant=moe.MOE_QUANT_E4M3_BLOCK128,
                               scales=torch.zeros((T, H // 128), dtype=torch.int32)))
+
+
+TOPK, F = 2, 96
+
+
+def layer(moe, **kw):
+    """The layer's call with every argument right but those in kw."""
+    fp = moe.moe_mx_columns(F)
+    args = dict(hidden=u8(T, H), hidden_scale=u8(T, H // 32), logits=torch.zeros((T, E)),
+                w_gate_up=u8(E, 2 * F, H // 2), w_gate_up_scale=u8(E, 2 * F, H // 32),
+                w_down=u8(E, H, fp // 2), w_down_scale=u8(E, H, fp // 32), H=H, F=F,
+                p=moe.route_params(TOPK), act=moe.act_params())
+    args.update(kw)
+    return moe.moe_ffn_forward_mx(**args)
+
+
+def every_other(*shape, dtype=torch.float32):
+    """A view of this shape of every other element."""
+    return torch.zeros((*shape[:-1], 2 * shape[-1]), dtype=dtype)[..., ::2]
+
+
+def elsewhere(*shape, dtype=torch.float32):
+    """A tensor whose memory the GPU must not be handed (on the CPU: a meta tensor)."""
+    return torch.zeros(shape, dtype=dtype, device="meta")
+
+
+def test_every_buffer_the_library_writes_is_checked(moe):
+    """Workspaces and the routing outputs too: a strided view's elements lie apart, and a host
+    tensor's address is none of the GPU's."""
+    i32 = torch.int32
+    layer(moe, ws=u8(4096), topk_weights_out=torch.zeros((T, TOPK)),
+          topk_ids_out=torch.zeros((T, TOPK), dtype=i32))
+    for make in (every_other, elsewhere):
+        refused(moe, lambda: layer(moe, topk_weights_out=make(T, TOPK)))
+        refused(moe, lambda: layer(moe, topk_ids_out=make(T, TOPK, dtype=i32)))
+        refused(moe, lambda: layer(moe, ws=make(4096, dtype=torch.uint8)))
+        refused(moe, lambda: layer(moe, out=make(T, H, dtype=torch.bfloat16)))
+        refused(moe, lambda: product(moe, ws=make(4096, dtype=torch.uint8)))
+        refused(moe, lambda: product(moe, out=make(M, N, dtype=torch.bfloat16)))
+        refused(moe, lambda: norm(moe, out=make(T, H, dtype=torch.bfloat16)))
