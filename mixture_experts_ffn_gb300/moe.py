@@ -748,6 +748,10 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
             w_gate_up_scale.element_size() == w_down.element_size() == \
             w_down_scale.element_size() == 1:
         raise TypeError("codes and scales are bytes")
+    _typed(correction_bias, torch.float32, "correction_bias")
+    _typed(expert_ids, torch.int32, "expert_ids")
+    _typed(topk_weights_out, torch.float32, "topk_weights_out")
+    _typed(topk_ids_out, torch.int32, "topk_ids_out")
     _fits(correction_bias, E, 4, "correction_bias")
     _fits(expert_ids, T * p.top_k, 4, "expert_ids")
     _fits(topk_weights_out, T * p.top_k, 4, "topk_weights_out")

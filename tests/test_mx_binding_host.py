@@ -155,3 +155,12 @@ def test_every_buffer_the_library_writes_is_checked(moe):
         refused(moe, lambda: product(moe, ws=make(4096, dtype=torch.uint8)))
         refused(moe, lambda: product(moe, out=make(M, N, dtype=torch.bfloat16)))
         refused(moe, lambda: norm(moe, out=make(T, H, dtype=torch.bfloat16)))
+
+
+def test_layer_refuses_routing_tensors_of_another_type(moe):
+    f, i = torch.zeros((T, TOPK)), torch.zeros((T, TOPK), dtype=torch.int32)
+    layer(moe, expert_ids=i, topk_weights_out=f, topk_ids_out=i, correction_bias=torch.zeros(E))
+    refused(moe, lambda: layer(moe, expert_ids=f), TypeError)
+    refused(moe, lambda: layer(moe, topk_weights_out=i), TypeError)
+    refused(moe, lambda: layer(moe, topk_ids_out=f), TypeError)
+    refused(moe, lambda: layer(moe, correction_bias=torch.zeros(E, dtype=torch.int32)), TypeError)
