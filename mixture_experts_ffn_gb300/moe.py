@@ -175,10 +175,10 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _fits(t, n: int, size: int, what: str):
-    """t (given by the caller) holds n elements of `size` bytes."""
-    if t is not None and (t.numel() != n or t.element_size() != size):
-        raise ValueError(f"{what} takes {n} elements of {size} bytes")
+def _fits(t, shape: tuple, size: int, what: str):
+    """t (given by the caller, or None) has this shape, in elements of `size` bytes."""
+    if t is not None and (t.shape != shape or t.element_size() != size):
+        raise ValueError(f"{what} is {list(shape)} in elements of {size} bytes")
 
 
 def _typed(t, dtype: torch.dtype, what: str):
@@ -580,12 +580,12 @@ def moe_mx_quantize(x, format: int = MOE_MX_E4M3, codes=None, scales=None):
                             dtype=torch.uint8 if format == MOE_MX_E2M1 else torch.float8_e4m3fn)
     else:
         _cuda(codes)
-        _fits(codes, rows * wide, 1, "codes")
+        _fits(codes, (*lead, wide), 1, "codes")
     if scales is None:
         scales = torch.empty((*lead, Kp // 32), dtype=torch.float8_e8m0fnu, device=x.device)
     else:
         _cuda(scales)
-        _fits(scales, rows * (Kp // 32), 1, "scales")
+        _fits(scales, (*lead, Kp // 32), 1, "scales")
     _check("moe_mx_quantize",
            lib.moe_mx_quantize(x.data_ptr(), rows, K, stride, _dt(x), format, codes.data_ptr(),
                                scales.data_ptr(), _stream_of(x)))
@@ -604,13 +604,13 @@ def moe_mx_dequantize(codes, scales, K: int, format=None, dtype=torch.bfloat16, 
             scales.shape[-1] * 32 != Kp or codes.shape[:-1] != scales.shape[:-1]:
         raise ValueError("codes and scales are not an MX tensor of K columns")
     rows = scales.numel() // (Kp // 32)
-    _fits(codes, codes.numel(), 1, "codes")
-    _fits(scales, scales.numel(), 1, "scales")
+    _fits(codes, codes.shape, 1, "codes")
+    _fits(scales, scales.shape, 1, "scales")
     if out is None:
         out = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
     else:
         _cuda(out)
-        _fits(out, rows * K, out.element_size(), "out")
+        _fits(out, (*codes.shape[:-1], K), out.element_size(), "out")
     _check("moe_mx_dequantize",
            lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), rows, K, format, _dt(out), out.data_ptr(), _stream_of(codes)))
     return out
@@ -637,10 +637,10 @@ def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_
     else:
         _cuda(out)
         _typed(out, x.dtype, "out")
-        _fits(out, T * H, x.element_size(), "out")
+        _fits(out, x.shape, x.element_size(), "out")
     if residual_out is not None:
         _typed(residual_out, x.dtype, "residual_out")
-        _fits(residual_out, T * H, x.element_size(), "residual_out")
+        _fits(residual_out, x.shape, x.element_size(), "residual_out")
     elif residual is not None:
         residual_out = torch.empty_like(x)
     if quant != MOE_QUANT_NONE:
@@ -648,14 +648,14 @@ def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_
         if codes is None:
             codes = torch.empty((T, Hp), dtype=torch.float8_e4m3fn, device=x.device)
         else:
-            _fits(codes, T * Hp, 1, "codes")
+            _fits(codes, (T, Hp), 1, "codes")
         if scales is None:
             scales = torch.empty((T, Hp // (32 if mx else 128)), device=x.device,
                                  dtype=torch.float8_e8m0fnu if mx else torch.float32)
         else:
             if not mx:
                 _typed(scales, torch.float32, "scales")
-            _fits(scales, T * (Hp // (32 if mx else 128)), 1 if mx else 4, "scales")
+            _fits(scales, (T, Hp // (32 if mx else 128)), 1 if mx else 4, "scales")
     _check("moe_add_rms_norm",
            lib.moe_add_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, _dt(x), eps,
                                 quant, _ptr(residual_out), _ptr(out), _ptr(codes), _ptr(scales),
@@ -682,9 +682,9 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
     E, N1, half = w.shape
     M = R if row_to_route is None else row_to_route.numel()
     gated = act is not None and act.kind in _GATED
-    if Kp % 128 or half * 2 != Kp or a_scale.numel() != R * (Kp // 32) or \
-            w_scale.numel() != E * N1 * (Kp // 32) or N1 != (2 * N if gated else N) or \
-            seg_end.numel() != E or (bias is not None and bias.numel() != E * N1):
+    if Kp % 128 or half * 2 != Kp or a_scale.shape != (R, Kp // 32) or \
+            w_scale.shape != (E, N1, Kp // 32) or N1 != (2 * N if gated else N) or \
+            seg_end.numel() != E or (bias is not None and bias.shape != (E, N1)):
         raise ValueError("operands are not MX tensors of matching extents")
     if bias is not None and bias.dtype != dtype:
         raise TypeError("bias takes the output's dtype")
@@ -694,8 +694,8 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
         raise TypeError("codes and scales are bytes, seg_end and row_to_route int32")
     if mx_out:
         Np = moe_mx_columns(N)
-        _fits(out, M * Np, 1, "out")
-        _fits(out_scale, M * (Np // 32), 1, "out_scale")
+        _fits(out, (M, Np), 1, "out")
+        _fits(out_scale, (M, Np // 32), 1, "out_scale")
         if out is None:
             out = torch.empty((M, Np), dtype=torch.float8_e4m3fn, device=a.device)
         if out_scale is None:
@@ -706,7 +706,7 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
         out = torch.empty((M, N), dtype=dtype, device=a.device)
     else:
         _typed(out, dtype, "out")
-        _fits(out, M * N, out.element_size(), "out")
+        _fits(out, (M, N), out.element_size(), "out")
     if ws is None:
         ws = _ws(lib.moe_grouped_gemm_mx_workspace_size(M, N, Kp, E), a.device)
     _check("moe_grouped_gemm_mx",
@@ -736,13 +736,12 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
     E, N1, half = w_gate_up.shape
     Fp = moe_mx_columns(F)
     if Hp != moe_mx_columns(H) or half * 2 != Hp or N1 != (2 * F if act.kind in _GATED else F) or \
-            hidden_scale.numel() != T * (Hp // 32) or \
-            w_gate_up_scale.numel() != E * N1 * (Hp // 32) or \
-            w_down.numel() != E * H * (Fp // 2) or w_down_scale.numel() != E * H * (Fp // 32) or \
-            logits.numel() != T * E:
+            hidden_scale.shape != (T, Hp // 32) or w_gate_up_scale.shape != (E, N1, Hp // 32) or \
+            w_down.shape != (E, H, Fp // 2) or w_down_scale.shape != (E, H, Fp // 32) or \
+            logits.shape != (T, E):
         raise ValueError("operands are not MX tensors of matching extents")
-    for b, n in ((b_gate_up, E * N1), (b_down, E * H)):
-        if b is not None and (b.dtype != dtype or b.numel() != n):
+    for b, shape in ((b_gate_up, (E, N1)), (b_down, (E, H))):
+        if b is not None and (b.dtype != dtype or b.shape != shape):
             raise ValueError("a bias is [E, rows] in the output's dtype")
     if not hidden.element_size() == hidden_scale.element_size() == w_gate_up.element_size() == \
             w_gate_up_scale.element_size() == w_down.element_size() == \
@@ -752,13 +751,13 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
     _typed(expert_ids, torch.int32, "expert_ids")
     _typed(topk_weights_out, torch.float32, "topk_weights_out")
     _typed(topk_ids_out, torch.int32, "topk_ids_out")
-    _fits(correction_bias, E, 4, "correction_bias")
-    _fits(expert_ids, T * p.top_k, 4, "expert_ids")
-    _fits(topk_weights_out, T * p.top_k, 4, "topk_weights_out")
-    _fits(topk_ids_out, T * p.top_k, 4, "topk_ids_out")
+    _fits(correction_bias, (E,), 4, "correction_bias")
+    _fits(expert_ids, (T, p.top_k), 4, "expert_ids")
+    _fits(topk_weights_out, (T, p.top_k), 4, "topk_weights_out")
+    _fits(topk_ids_out, (T, p.top_k), 4, "topk_ids_out")
     if out is None:
         out = torch.empty((T, H), dtype=dtype, device=hidden.device)
-    elif out.dtype != dtype or out.numel() != T * H:
+    elif out.dtype != dtype or out.shape != (T, H):
         raise ValueError("out is [T, H] in dtype")
     if ws is None:
         ws = _ws(lib.moe_workspace_size_mx(T, H, F, E, p.top_k), hidden.device)

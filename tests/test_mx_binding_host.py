@@ -164,3 +164,32 @@ def test_layer_refuses_routing_tensors_of_another_type(moe):
     refused(moe, lambda: layer(moe, topk_weights_out=i), TypeError)
     refused(moe, lambda: layer(moe, topk_ids_out=f), TypeError)
     refused(moe, lambda: layer(moe, correction_bias=torch.zeros(E, dtype=torch.int32)), TypeError)
+
+
+def test_tensors_of_the_right_count_and_the_wrong_shape_are_refused(moe):
+    """Axes exchanged, the elements are the right number in the wrong order."""
+    i32 = torch.int32
+    fp = moe.moe_mx_columns(F)
+    for kw in (dict(a_scale=u8(K // 32, M)), dict(w_scale=u8(E, K // 32, N)),
+               dict(w_scale=u8(N, E, K // 32)), dict(bias=torch.zeros((N, E), dtype=torch.bfloat16)),
+               dict(out=torch.zeros((N, M), dtype=torch.bfloat16)),
+               dict(mx_out=True, out=u8(128, M)), dict(mx_out=True, out_scale=u8(4, M))):
+        refused(moe, lambda: product(moe, **kw), ValueError)
+    for kw in (dict(hidden_scale=u8(H // 32, T)), dict(logits=torch.zeros((E, T))),
+               dict(w_gate_up_scale=u8(2 * F, E, H // 32)), dict(w_down=u8(H, E, fp // 2)),
+               dict(w_down=u8(E, fp // 2, H)), dict(w_down_scale=u8(E, fp // 32, H)),
+               dict(b_gate_up=torch.zeros((2 * F, E), dtype=torch.bfloat16)),
+               dict(b_down=torch.zeros((H, E), dtype=torch.bfloat16)),
+               dict(expert_ids=torch.zeros((TOPK, T), dtype=i32)),
+               dict(topk_ids_out=torch.zeros((TOPK, T), dtype=i32)),
+               dict(topk_weights_out=torch.zeros((TOPK, T))),
+               dict(out=torch.zeros((H, T), dtype=torch.bfloat16))):
+        refused(moe, lambda: layer(moe, **kw), ValueError)
+    for kw in (dict(out=torch.zeros((H, T), dtype=torch.bfloat16)),
+               dict(residual=True, residual_out=torch.zeros((H, T), dtype=torch.bfloat16)),
+               dict(quant=1, codes=u8(H, T)), dict(quant=1, scales=u8(H // 32, T)),
+               dict(quant=2, scales=torch.zeros((H // 128, T)))):
+        refused(moe, lambda: norm(moe, **kw), ValueError)
+    codes, scales = u8(T, H), u8(T, H // 32)
+    moe.moe_mx_dequantize(codes, scales, H, out=torch.zeros((T, H)))
+    refused(moe, lambda: moe.moe_mx_dequantize(codes, scales, H, out=torch.zeros((H, T))), ValueError)
