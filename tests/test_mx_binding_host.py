@@ -45,7 +45,7 @@ def u8(*shape):
     return torch.zeros(shape, dtype=torch.uint8)
 
 
-E, N, K, M = 2, 64, 256, 8
+E, N, K, M = 2, 64, 384, 8
 
 
 def product(moe, **kw):
