@@ -29,6 +29,10 @@ MOE_LAYOUT_PSUM, MOE_LAYOUT_PER_ROW, MOE_LAYOUT_MASKED = 0, 1, 2
 MOE_MX_E4M3, MOE_MX_E2M1 = 0, 1
 MOE_QUANT_NONE, MOE_QUANT_MX_E4M3, MOE_QUANT_E4M3_BLOCK128 = 0, 1, 2
 _GATED = (MOE_ACT_SILU_AND_MUL, MOE_ACT_SWIGLU, MOE_ACT_GELU_AND_MUL)
+# types that MX codes and scales are taken in: bytes, or the format's own
+_E4M3 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
+_E2M1 = (torch.uint8, torch.int8, getattr(torch, "float4_e2m1fn_x2", torch.uint8))
+_E8M0 = (torch.float8_e8m0fnu, torch.uint8, torch.int8)
 
 # C entry points and their argument types (mirrors include/moe.h)
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, \
@@ -187,11 +191,21 @@ def _typed(t, dtype: torch.dtype, what: str):
         raise TypeError(f"{what} takes {dtype}")
 
 
+def _coded(t, types: tuple, what: str):
+    """t (given by the caller, or None) holds codes or scales of one MX format."""
+    if t is not None and t.dtype not in types:
+        raise TypeError(f"{what} takes {types[0]} or bytes, not {t.dtype}")
+
+
+def _on_gpu(t):
+    if not t.is_cuda:
+        raise ValueError("libmoe takes CUDA tensors only")
+
+
 def _cuda(*ts):
     for t in ts:
         if t is not None:
-            if not t.is_cuda:
-                raise ValueError("libmoe takes CUDA tensors only")
+            _on_gpu(t)
             if not t.is_contiguous():
                 raise ValueError("libmoe takes contiguous tensors only")
 
@@ -563,8 +577,7 @@ def moe_mx_quantize(x, format: int = MOE_MX_E4M3, codes=None, scales=None):
     [..., Kp / 32] float8_e8m0fnu, Kp = moe_mx_columns(K).  A 2-D x may have any
     row stride >= K; other shapes are contiguous."""
     lib = load_library()
-    if not x.is_cuda:
-        raise ValueError("libmoe takes CUDA tensors only")
+    _on_gpu(x)
     K = x.shape[-1]
     if x.dim() == 2 and x.shape[0] > 1 and x.stride(1) == 1 and x.stride(0) >= K:
         stride = x.stride(0)
@@ -580,11 +593,13 @@ def moe_mx_quantize(x, format: int = MOE_MX_E4M3, codes=None, scales=None):
                             dtype=torch.uint8 if format == MOE_MX_E2M1 else torch.float8_e4m3fn)
     else:
         _cuda(codes)
+        _coded(codes, _E2M1 if format == MOE_MX_E2M1 else _E4M3, "codes")
         _fits(codes, (*lead, wide), 1, "codes")
     if scales is None:
         scales = torch.empty((*lead, Kp // 32), dtype=torch.float8_e8m0fnu, device=x.device)
     else:
         _cuda(scales)
+        _coded(scales, _E8M0, "scales")
         _fits(scales, (*lead, Kp // 32), 1, "scales")
     _check("moe_mx_quantize",
            lib.moe_mx_quantize(x.data_ptr(), rows, K, stride, _dt(x), format, codes.data_ptr(),
@@ -604,15 +619,16 @@ def moe_mx_dequantize(codes, scales, K: int, format=None, dtype=torch.bfloat16, 
             scales.shape[-1] * 32 != Kp or codes.shape[:-1] != scales.shape[:-1]:
         raise ValueError("codes and scales are not an MX tensor of K columns")
     rows = scales.numel() // (Kp // 32)
-    _fits(codes, codes.shape, 1, "codes")
-    _fits(scales, scales.shape, 1, "scales")
+    _coded(codes, _E2M1 if format == MOE_MX_E2M1 else _E4M3, "codes")
+    _coded(scales, _E8M0, "scales")
     if out is None:
         out = torch.empty((*codes.shape[:-1], K), dtype=dtype, device=codes.device)
     else:
         _cuda(out)
         _fits(out, (*codes.shape[:-1], K), out.element_size(), "out")
     _check("moe_mx_dequantize",
-           lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), rows, K, format, _dt(out), out.data_ptr(), _stream_of(codes)))
+           lib.moe_mx_dequantize(codes.data_ptr(), scales.data_ptr(), rows, K, format, _dt(out),
+                                 out.data_ptr(), _stream_of(codes)))
     return out
 
 
@@ -648,13 +664,13 @@ def moe_add_rms_norm(x, weight, residual=None, eps=1e-6, quant: int = MOE_QUANT_
         if codes is None:
             codes = torch.empty((T, Hp), dtype=torch.float8_e4m3fn, device=x.device)
         else:
+            _coded(codes, _E4M3, "codes")
             _fits(codes, (T, Hp), 1, "codes")
         if scales is None:
             scales = torch.empty((T, Hp // (32 if mx else 128)), device=x.device,
                                  dtype=torch.float8_e8m0fnu if mx else torch.float32)
         else:
-            if not mx:
-                _typed(scales, torch.float32, "scales")
+            _coded(scales, _E8M0 if mx else (torch.float32,), "scales")
             _fits(scales, (T, Hp // (32 if mx else 128)), 1 if mx else 4, "scales")
     _check("moe_add_rms_norm",
            lib.moe_add_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), T, H, _dt(x), eps,
@@ -688,12 +704,14 @@ def moe_grouped_gemm_mx(a, a_scale, w, w_scale, seg_end, N: int, act: Optional[A
         raise ValueError("operands are not MX tensors of matching extents")
     if bias is not None and bias.dtype != dtype:
         raise TypeError("bias takes the output's dtype")
-    if not a.element_size() == a_scale.element_size() == w.element_size() == \
-            w_scale.element_size() == 1 or seg_end.dtype != torch.int32 or \
+    if a.dtype not in _E4M3 or a_scale.dtype not in _E8M0 or w.dtype not in _E2M1 or \
+            w_scale.dtype not in _E8M0 or seg_end.dtype != torch.int32 or \
             (row_to_route is not None and row_to_route.dtype != torch.int32):
-        raise TypeError("codes and scales are bytes, seg_end and row_to_route int32")
+        raise TypeError("a is e4m3, w e2m1, the scales e8m0 (or bytes), seg_end and row_to_route int32")
     if mx_out:
         Np = moe_mx_columns(N)
+        _coded(out, _E4M3, "out")
+        _coded(out_scale, _E8M0, "out_scale")
         _fits(out, (M, Np), 1, "out")
         _fits(out_scale, (M, Np // 32), 1, "out_scale")
         if out is None:
@@ -743,10 +761,10 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
     for b, shape in ((b_gate_up, (E, N1)), (b_down, (E, H))):
         if b is not None and (b.dtype != dtype or b.shape != shape):
             raise ValueError("a bias is [E, rows] in the output's dtype")
-    if not hidden.element_size() == hidden_scale.element_size() == w_gate_up.element_size() == \
-            w_gate_up_scale.element_size() == w_down.element_size() == \
-            w_down_scale.element_size() == 1:
-        raise TypeError("codes and scales are bytes")
+    if hidden.dtype not in _E4M3 or hidden_scale.dtype not in _E8M0 or \
+            w_gate_up.dtype not in _E2M1 or w_gate_up_scale.dtype not in _E8M0 or \
+            w_down.dtype not in _E2M1 or w_down_scale.dtype not in _E8M0:
+        raise TypeError("hidden is e4m3, the weights e2m1 and the scales e8m0 (or bytes)")
     _typed(correction_bias, torch.float32, "correction_bias")
     _typed(expert_ids, torch.int32, "expert_ids")
     _typed(topk_weights_out, torch.float32, "topk_weights_out")

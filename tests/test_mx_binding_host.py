@@ -27,14 +27,13 @@ class Recorder:
 def moe(monkeypatch):
     from mixture_experts_ffn_gb300 import moe as m
 
-    def as_if_on_the_gpu(*ts):  # the binding's own check but for the device
-        for t in ts:
-            if t is not None and (t.is_meta or not t.is_contiguous()):
-                raise ValueError("libmoe takes contiguous CUDA tensors only")
+    def as_if_on_the_gpu(t):  # the binding's check of the device: a meta tensor fails it
+        if t.is_meta:
+            raise ValueError("libmoe takes CUDA tensors only")
 
     rec = Recorder()
     monkeypatch.setattr(m, "load_library", lambda: rec)
-    monkeypatch.setattr(m, "_cuda", as_if_on_the_gpu)
+    monkeypatch.setattr(m, "_on_gpu", as_if_on_the_gpu)
     monkeypatch.setattr(m, "_stream_of", lambda t: 0)
     m.recorder = rec
     yield m
@@ -193,3 +192,34 @@ def test_tensors_of_the_right_count_and_the_wrong_shape_are_refused(moe):
     codes, scales = u8(T, H), u8(T, H // 32)
     moe.moe_mx_dequantize(codes, scales, H, out=torch.zeros((T, H)))
     refused(moe, lambda: moe.moe_mx_dequantize(codes, scales, H, out=torch.zeros((H, T))), ValueError)
+
+
+def test_codes_and_scales_of_another_format_are_refused(moe):
+    """Bytes (uint8, int8) or the format's own type: an e5m2 tensor's bytes are not e4m3 codes, nor
+    e4m3 values power-of-two scales."""
+    e4, e5, e8 = torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu
+    i8 = torch.int8
+    product(moe, a=u8(M, K).view(e4), a_scale=u8(M, K // 32).view(e8), w_scale=u8(E, N, K // 32).view(i8))
+    product(moe, mx_out=True, out=u8(M, 128).view(e4), out_scale=u8(M, 4).view(e8))
+    for kw in (dict(a=u8(M, K).view(e5)), dict(a=u8(M, K).view(e8)), dict(a=u8(M, K).bool()),
+               dict(a_scale=u8(M, K // 32).view(e4)), dict(w=u8(E, N, K // 2).view(e4)),
+               dict(w_scale=u8(E, N, K // 32).view(e4)),
+               dict(mx_out=True, out=u8(M, 128).view(e5)),
+               dict(mx_out=True, out_scale=u8(M, 4).view(e4))):
+        refused(moe, lambda: product(moe, **kw), TypeError)
+    fp = moe.moe_mx_columns(F)
+    for kw in (dict(hidden=u8(T, H).view(e5)), dict(hidden_scale=u8(T, H // 32).view(e4)),
+               dict(w_gate_up=u8(E, 2 * F, H // 2).view(e4)),
+               dict(w_gate_up_scale=u8(E, 2 * F, H // 32).view(e5)),
+               dict(w_down=u8(E, H, fp // 2).view(e4)), dict(w_down_scale=u8(E, H, fp // 32).view(e4))):
+        refused(moe, lambda: layer(moe, **kw), TypeError)
+    x = torch.zeros((T, H))
+    for fmt, wide in ((moe.MOE_MX_E4M3, H), (moe.MOE_MX_E2M1, H // 2)):
+        moe.moe_mx_quantize(x, fmt, codes=u8(T, wide), scales=u8(T, H // 32))
+        refused(moe, lambda: moe.moe_mx_quantize(x, fmt, codes=u8(T, wide).view(e5)), TypeError)
+        refused(moe, lambda: moe.moe_mx_quantize(x, fmt, scales=u8(T, H // 32).view(e4)), TypeError)
+        refused(moe, lambda: moe.moe_mx_dequantize(u8(T, wide).view(e5), u8(T, H // 32), H), TypeError)
+        refused(moe, lambda: moe.moe_mx_dequantize(u8(T, wide), u8(T, H // 32).view(e4), H), TypeError)
+    refused(moe, lambda: moe.moe_mx_quantize(x, moe.MOE_MX_E2M1, codes=u8(T, H // 2).view(e4)), TypeError)
+    refused(moe, lambda: norm(moe, quant=1, codes=u8(T, H).view(e5)), TypeError)
+    refused(moe, lambda: norm(moe, quant=1, scales=u8(T, H // 32).view(e4)), TypeError)
