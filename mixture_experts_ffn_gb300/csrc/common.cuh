@@ -67,6 +67,20 @@ __device__ __forceinline__ float hi16(uint32_t v) {
 }
 
 // ---------------------------------------------------------------- math
+// Minimum and maximum that keep a NaN: fminf and fmaxf return the other
+// operand, so a clamp would turn the product of a non-finite row into a bound.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float relu_f(float x) { return max_nan(x, 0.0f); }
+
 __device__ __forceinline__ float sigmoidf_(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // silu(g) * u  (silu_and_mul)
@@ -84,7 +98,7 @@ __host__ __device__ constexpr bool act_is_gated(int kind) {
 
 // non-gated activation of one value (identity, relu, gelu, silu)
 __device__ __forceinline__ float act_plain(int kind, float x) {
-  return kind == MOE_ACT_RELU ? fmaxf(x, 0.0f)
+  return kind == MOE_ACT_RELU ? relu_f(x)
          : kind == MOE_ACT_GELU ? gelu_f(x)
          : kind == MOE_ACT_SILU ? x * sigmoidf_(x)
                                 : x;
@@ -93,8 +107,8 @@ __device__ __forceinline__ float act_plain(int kind, float x) {
 // clamped SwiGLU; limit <= 0 disables both clamps
 __device__ __forceinline__ float swiglu_f(float g, float l, float limit, float alpha, float beta) {
   if (limit > 0.0f) {
-    g = fminf(g, limit);
-    l = fmaxf(fminf(l, limit), -limit);
+    g = min_nan(g, limit);
+    l = max_nan(min_nan(l, limit), -limit);
   }
   return g * sigmoidf_(alpha * g) * (l + beta);
 }

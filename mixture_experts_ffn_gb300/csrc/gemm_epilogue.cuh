@@ -44,8 +44,8 @@ __device__ __forceinline__ float gated(float g, float u, float limit, float alph
     return gelu_f(g) * u;
   } else {
     if (limit > 0.0f) {
-      g = fminf(g, limit);
-      u = fmaxf(fminf(u, limit), -limit);
+      g = min_nan(g, limit);
+      u = max_nan(min_nan(u, limit), -limit);
     }
     return g * fast_sigmoid(alpha * g) * (u + beta);
   }
@@ -139,7 +139,7 @@ __device__ __forceinline__ void drain_cols(uint32_t tbase, int wrow0, int m_end,
       }
       if constexpr (ACT == MOE_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = fmaxf(v[i], 0.0f);
+        for (int i = 0; i < 32; ++i) v[i] = relu_f(v[i]);
       } else if constexpr (ACT == MOE_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i]);

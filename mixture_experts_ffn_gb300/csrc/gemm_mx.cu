@@ -404,7 +404,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 
 template <int ACT>
 __device__ __forceinline__ float act_one(float x) {
-  if constexpr (ACT == MOE_ACT_RELU) return fmaxf(x, 0.0f);
+  if constexpr (ACT == MOE_ACT_RELU) return relu_f(x);
   else if constexpr (ACT == MOE_ACT_GELU) return gelu_f(x);
   else if constexpr (ACT == MOE_ACT_SILU) return x * fast_sigmoid(x);
   else return x;

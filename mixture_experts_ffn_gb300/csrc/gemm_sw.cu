@@ -363,7 +363,7 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint16_t v) {
 
 template <int ACT>
 __device__ __forceinline__ float act1(float x) {
-  if constexpr (ACT == MOE_ACT_RELU) return fmaxf(x, 0.0f);
+  if constexpr (ACT == MOE_ACT_RELU) return relu_f(x);
   else if constexpr (ACT == MOE_ACT_GELU) return gelu_f(x);
   else if constexpr (ACT == MOE_ACT_SILU) return x * fast_sigmoid(x);
   else return x;
