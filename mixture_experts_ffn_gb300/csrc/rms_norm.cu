@@ -122,18 +122,27 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024)
     const int item = t0 + i * nthr, c0 = item * 8;
     float w[8];
     mx::load8<T, VEC>(static_cast<const T*>(p.w), c0, H, w);
+    uint32_t amax = 0;  // bits of the largest magnitude; a NaN's are above infinity's
+    float z[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       // h * root * w with one rounding: the product's own error rides along
       const float a = v[i][j] * root.hi;
       const float lo = fmaf(v[i][j], root.lo, fmaf(v[i][j], root.hi, -a));
-      v[i][j] = fmaf(a, w[j], lo * w[j]);
+      z[j] = fmaf(a, w[j], lo * w[j]);
+      amax = max(amax, mx::abs_bits(z[j]));
     }
+    if (amax > mx::kInfBits) {
+      // an infinite w or root leaves no error to carry (0 * inf, inf - inf):
+      // the product alone, NaN where that is one
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (isnan(z[j])) z[j] = v[i][j] * root.hi * w[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = z[j];
     if (y) mx::store8<T, VEC>(y, c0, H, v[i]);
     if constexpr (QUANT != kQuantNone) {
-      uint32_t amax = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, mx::abs_bits(v[i][j]));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       if constexpr (QUANT == kQuantMx) {

@@ -1,5 +1,5 @@
 """Edges of the microscaled operators on the GPU: NaN through the clamped and
-rectified activations."""
+rectified activations, infinite weights and mean squares of zero in the norm."""
 import pytest
 import torch
 
@@ -95,3 +95,49 @@ def test_unscaled_products_and_swiglu_keep_nan(moe, counts, dtype):
     want = torch.zeros((8, F), dtype=torch.bool, device="cuda")
     want[2, 3], want[4, 5] = True, True
     assert torch.equal(torch.isnan(out), want)
+
+
+# ------------------------------------------------------------------ norm: infinities
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,H", [(5, 320), (400, 64), (3, 2880)])
+def test_norm_infinite_weight_gives_infinities(moe, T, H, dtype):
+    """h * root * inf is an infinity of h's sign (NaN where h is zero); a NaN weight gives NaN; the
+    other columns are as without."""
+    g = gen(T + H)
+    x = torch.randn((T, H), generator=g, device="cuda").to(dtype)
+    x[0, 40] = 0
+    w = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(dtype)
+    plain = moe.moe_add_rms_norm(x, w)["out"]
+    w2 = w.clone()
+    w2[40], w2[41], w2[H - 1] = float("inf"), float("nan"), float("-inf")
+    y = moe.moe_add_rms_norm(x, w2)["out"]
+    assert torch.isnan(y[0, 40]) and torch.isnan(y[:, 41]).all()
+    assert torch.equal(y[1:, 40], torch.sign(x[1:, 40]) * float("inf"))
+    assert torch.equal(y[:, H - 1], torch.sign(x[:, H - 1]) * float("-inf"))
+    rest = torch.ones(H, dtype=torch.bool, device="cuda")
+    rest[[40, 41, H - 1]] = False
+    assert torch.equal(y[:, rest], plain[:, rest])
+
+
+def test_norm_of_a_mean_square_of_zero(moe):
+    """In float32 squares below 2^-149 are zero: without eps the root is infinite, and h times it an
+    infinity of h's sign, NaN where h is zero."""
+    x = torch.zeros((4, 256), device="cuda")
+    x[0], x[1, ::2], x[2, 5] = 1e-30, -1e-30, 1.0
+    w = torch.ones(256, device="cuda")
+    y = moe.moe_add_rms_norm(x, w, eps=0.0)["out"]
+    assert (y[0] == float("inf")).all()
+    assert (y[1, ::2] == float("-inf")).all() and torch.isnan(y[1, 1::2]).all()
+    assert y[2, 5] == 16.0 and (y[2, 6:] == 0).all()
+    assert torch.isnan(y[3]).all()
+    # with eps the rows are finite
+    assert torch.isfinite(moe.moe_add_rms_norm(x, w, eps=1e-6)["out"]).all()
+
+
+def test_norm_of_rows_whose_squares_overflow(moe):
+    """A mean square past float32 is infinite, its root zero: zeros of h's sign, NaN for an infinite
+    h."""
+    x = torch.full((2, 160), 1e30, device="cuda")
+    x[1, 3] = float("inf")
+    y = moe.moe_add_rms_norm(x, torch.ones(160, device="cuda"))["out"]
+    assert (y[0] == 0).all() and torch.isnan(y[1, 3]) and (y[1, 4:] == 0).all()
