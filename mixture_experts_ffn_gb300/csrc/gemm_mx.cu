@@ -256,24 +256,41 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
-// arrival on a barrier of either CTA of the pair (shared::cluster address),
-// released at CTA scope: a cluster-scope release would wait for every copy this
-// SM has in flight, and what it orders is this SM's own shared memory (after
-// the proxy fence) and TMEM (after the tcgen05 fence)
+// The CTAs of a pair synchronise at cluster scope.  What they order is the SMs'
+// own shared memory (after the proxy fence) and TMEM (after the tcgen05 fence),
+// so release and acquire are fences restricted to shared memory around relaxed
+// operations on the barrier: an unrestricted release at this scope also waits for
+// the SM's copies from global memory, a microsecond a stage (8192 ragged rows,
+// 2880 x 2880: 138 us, 322 with it; 65536 rows, 2048 x 7168: 1377 and 1599).
+//
+// arrival on a barrier of either CTA of the pair (shared::cluster address)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-               : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+      : "memory");
 }
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "@p fence.acquire.sync_restrict::shared::cluster.cluster;\n\t}"
       : "=r"(ok)
       : "r"(addr), "r"(parity)
       : "memory");
   return ok != 0;
+}
+// Wait for a barrier that the other CTA of a pair arrives on too, or whose commit
+// the other CTA issued.  Once wait_bar has seen the phase, the second try returns
+// at once (the next phase waits for the caller).
+template <bool PAIR>
+__device__ __forceinline__ bool wait_pair(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+                                          int* status) {
+  if constexpr (!PAIR) return wait_fast(b, parity, abort_flag, status);
+  if (mbar_try_wait_cluster(su32(b), parity)) return true;
+  return wait_bar(b, parity, abort_flag, status) && mbar_try_wait_cluster(su32(b), parity);
 }
 // a load into this CTA's shared memory that completes on a barrier of the
 // pair's leader (shared::cluster address)
@@ -570,7 +587,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       bool ok = true;
       auto take = [&](int freed) {  // waits for the stage; freed: the slot it was to free
-        if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) return false;
+        if (!wait_pair<PAIR>(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) return false;
         if (freed >= 0) {
           tc_fence_after();
           tc_fence_before();
@@ -651,7 +668,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int tile = unit; tile < total && ok; tile += units) {
       const MxTile t = decode(tile);
       if (t.nv == 0) continue;
-      ok = __all_sync(0xffffffffu, wait_fast(&sh->tempty[acc], aphase ^ 1u, abort_flag, p.status));
+      ok = __all_sync(0xffffffffu,
+                      wait_pair<PAIR>(&sh->tempty[acc], aphase ^ 1u, abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tm0 + (uint32_t)(acc * C::ACC_COLS);
@@ -727,7 +745,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         at[i] = (uint32_t)max(m, 0) * (uint32_t)nkb;
       }
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) { ok = false; break; }
+        if (!wait_pair<PAIR>(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
         const uint32_t dst = su32(smem + (size_t)stage * C::STAGE_BYTES) + dst0;
 #pragma unroll
         for (int i = 0; i < RI; ++i)
@@ -919,7 +940,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (HALVES == 2 && f + 128 < p.Nout) b[1] = bias_at(f + 128);
         }
       }
-      if (!wait_fast(&sh->tfull[acc], aphase, abort_flag, p.status)) break;
+      if (!wait_pair<PAIR>(&sh->tfull[acc], aphase, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t base = lanes + (uint32_t)(acc * C::ACC_COLS);
 #pragma unroll 1
