@@ -87,29 +87,6 @@ struct Fp8Shared {
 constexpr size_t kSmemBytes = (size_t)STAGES * STAGE_BYTES + OUT_BYTES + sizeof(Fp8Shared) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t d;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(saddr), "r"(rank));
-  return d;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile(
-      "barrier.cluster.arrive.release.aligned;\n\t"
-      "barrier.cluster.wait.acquire.aligned;" ::
-          : "memory");
-}
-// arrival on a barrier of either CTA of the pair (shared::cluster address),
-// released at CTA scope: it orders this thread's earlier tcgen05 loads (after
-// tcgen05.fence::before_thread_sync) without waiting for the SM's copies
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-               : "memory");
-}
 // A TMA load into this CTA's shared memory that completes on the leader's
 // barrier (shared::cluster address); coordinates innermost first.
 __device__ __forceinline__ void tma2_3d(void* dst, const CUtensorMap* m, uint32_t bar, int c0,
@@ -331,7 +308,7 @@ __global__ void __launch_bounds__(NUM_THREADS)
           sa1 = in_slab ? __ldg(sa + kb + 2) : 0.f;
           sb1 = col_ok ? __ldg(sb + kb + 2) : 0.f;
         }
-        if (!wait_fast(&sh->pfull[pb], pph, abort_flag, status)) { ok = false; break; }
+        if (!wait_pair(&sh->pfull[pb], pph, abort_flag, status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t taddr =
             tmem_base + lane_addr + (uint32_t)(pb * BN + half * kColsPerWarp);
@@ -391,7 +368,7 @@ __global__ void __launch_bounds__(NUM_THREADS)
         for (int tile = pair; tile < total && ok; tile += npairs) {
           const MaskedTile st = decode_masked(tile, sh->prefix, counts, E, max_m);
           for (int kb = 0; kb < nkb; ++kb) {
-            if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, status)) { ok = false; break; }
+            if (!wait_pair(&sh->empty[stage], phase ^ 1u, abort_flag, status)) { ok = false; break; }
             uint8_t* a_dst = smem + (size_t)stage * STAGE_BYTES;
             const uint32_t bar = map_to_rank(su32(&sh->full[stage]), 0);
             if (leader) mbar_expect_tx(&sh->full[stage], 2 * STAGE_BYTES);
@@ -418,8 +395,8 @@ __global__ void __launch_bounds__(NUM_THREADS)
         const uint64_t bdesc0 = sw128_desc(su32(smem + A_BYTES));
         for (int tile = pair; tile < total && ok; tile += npairs) {
           for (int kb = 0; kb < nkb; ++kb) {
-            if (!wait_fast(&sh->pempty[pb], pph ^ 1u, abort_flag, status)) { ok = false; break; }
-            if (!wait_fast(&sh->full[stage], phase, abort_flag, status)) { ok = false; break; }
+            if (!wait_pair(&sh->pempty[pb], pph ^ 1u, abort_flag, status)) { ok = false; break; }
+            if (!wait_pair(&sh->full[stage], phase, abort_flag, status)) { ok = false; break; }
             tc_fence_after();
             const uint64_t off = (uint64_t)((stage * STAGE_BYTES) >> 4);
             umma2_fp8_block(tmem_base + (uint32_t)(pb * BN), adesc0 + off, bdesc0 + off,

@@ -143,33 +143,6 @@ constexpr size_t kSmemBytes =
     (size_t)kRingBytes + kOutBufs * OUT_BUF_BYTES + sizeof(SwShared) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t d;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(saddr), "r"(rank));
-  return d;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile(
-      "barrier.cluster.arrive.release.aligned;\n\t"
-      "barrier.cluster.wait.acquire.aligned;" ::
-          : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(addr), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // Bounded wait, acquiring at cluster scope (the entry may have been written
 // by the peer CTA); false on abort or timeout.
 __device__ __noinline__ bool wait_cluster(uint64_t* b, uint32_t parity, volatile int* abort_flag,
@@ -543,11 +516,6 @@ struct SwRoles {
   static constexpr int NBUF = EPI_GROUPS > 1 ? 1 : 2;  // staging buffers per epilogue warp
 };
 
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-               : "memory");
-}
-
 // Token-row boxes of 32, 64 and 128 rows x one K atom: 2-D maps [rows][K] of
 // the rows' source.
 struct TokMaps {
@@ -689,7 +657,7 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
         const uint32_t tx =
             (uint32_t)A_BYTES + (TOK == kTokTiled ? (uint32_t)KA * (32u << bsel) * BK * 2 : 0u);
         for (int ks = 0; ks < nks; ++ks) {
-          if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, status)) { ok = false; break; }
+          if (!wait_pair(&sh->empty[stage], phase ^ 1u, abort_flag, status)) { ok = false; break; }
           uint8_t* a_dst = smem + (size_t)stage * STAGE_BYTES;
           uint8_t* b_dst = a_dst + A_BYTES;
           const uint32_t bar = map_to_rank(su32(&sh->full[stage]), 0);
@@ -746,11 +714,11 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
         const uint32_t idesc = idesc_sw(2 * ROWS, st.N, F16 ? 1 : 0);  // M256 per MMA
         // token atoms h rows apart (16-byte descriptor units)
         const uint32_t b_atom16 = (uint32_t)((32 << tok_box_sel(st.N >> 1)) * BK * 2) >> 4;
-        if (!wait_fast(&sh->tempty[acc], aphase ^ 1u, abort_flag, status)) { ok = false; break; }
+        if (!wait_pair(&sh->tempty[acc], aphase ^ 1u, abort_flag, status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * NMAX);
         for (int ks = 0; ks < nks; ++ks) {
-          if (!wait_fast(&sh->full[stage], phase, abort_flag, status)) { ok = false; break; }
+          if (!wait_pair(&sh->full[stage], phase, abort_flag, status)) { ok = false; break; }
           // cp.async rows of this CTA were written through the generic proxy;
           // the MMA reads them through the async proxy (the peer's forwarder
           // fences the peer's rows)
@@ -779,9 +747,7 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
       if (lane == 0 && !leader) {
         // -------------------------------------------- forwarder (peer)
         // the peer's rows of a stage have landed: order them for the async
-        // proxy and pass one arrival to the leader's full barrier (released
-        // at CTA scope: a cluster-scope release would wait for every copy
-        // this SM has in flight)
+        // proxy and pass one arrival to the leader's full barrier
         int stage = 0;
         uint32_t phase = 0;
         const uint32_t full_remote0 = map_to_rank(su32(&sh->full[0]), 0);
@@ -791,7 +757,7 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
           for (int ks = 0; ks < nks; ++ks) {
             if (!wait_fast(&sh->afull[stage], phase, abort_flag, status)) { ok = false; break; }
             fence_proxy_async_smem();
-            mbar_arrive_remote_cta(full_remote0 + (uint32_t)(stage * sizeof(uint64_t)));
+            mbar_arrive_cluster(full_remote0 + (uint32_t)(stage * sizeof(uint64_t)));
             if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           }
         }
@@ -838,7 +804,7 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
         src[i] = asrc + (size_t)t * K + ch * 8;
       }
       for (int ks = 0; ks < nks; ++ks) {
-        if (!wait_fast(&sh->empty[stage], phase ^ 1u, abort_flag, status)) { ok = false; break; }
+        if (!wait_pair(&sh->empty[stage], phase ^ 1u, abort_flag, status)) { ok = false; break; }
         const uint32_t b_dst = su32(smem + (size_t)stage * STAGE_BYTES + A_BYTES) + dst0;
 #pragma unroll
         for (int a = 0; a < KA; ++a) {
@@ -878,7 +844,7 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
       const int tile = next_tile(j);
       if (tile >= total) break;
       const SwTile st = decode(tile);
-      if (!wait_fast(&sh->tfull[acc], aphase, abort_flag, status)) break;
+      if (!wait_pair(&sh->tfull[acc], aphase, abort_flag, status)) break;
       tc_fence_after();
       const __nv_bfloat16* be = bias ? bias + (size_t)st.e * N1 : nullptr;
       const uint32_t tq = tmem_base + ((uint32_t)(quad * 32) << 16);
@@ -904,11 +870,10 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
                                      obufs, obuf, lane);
         }
       }
-      // the drain's TMEM loads have completed (tcgen05.wait::ld): a CTA-scope
-      // release orders them before the leader's next MMAs (a cluster-scope
-      // one would also wait for every copy this SM has in flight)
+      // the drain's TMEM loads have completed (tcgen05.wait::ld) and are
+      // ordered before the leader's next MMAs
       tc_fence_before();
-      mbar_arrive_remote_cta(tempty_remote[acc]);
+      mbar_arrive_cluster(tempty_remote[acc]);
       if (++acc == NACC) { acc = 0; aphase ^= 1u; }
     }
     if (lane == 0) bulk_wait_all();  // every staged box written before the pair exits
