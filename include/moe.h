@@ -569,8 +569,10 @@ typedef enum moe_mx_format { MOE_MX_E4M3 = 0, MOE_MX_E2M1 = 1 } moe_mx_format;
 moe_status moe_mx_quantize(const void* x, int64_t rows, int K, int64_t row_stride,
                            moe_dtype dtype, int format, void* codes, void* scales,
                            cudaStream_t stream);
-/* out [rows, K] dtype = codes * scales (exact in bf16 and f32; rounded, and
- * infinite past its range, in f16).  codes and scales as above. */
+/* out [rows, K] dtype = codes * scales, rounded once to nearest, infinite past
+ * the type's range, NaN under a NaN scale.  Exact in f32 below 2^128, and in
+ * bf16 there from 2^-133 on (e4m3 codes under the smallest scales reach
+ * 2^-136).  codes and scales as above. */
 moe_status moe_mx_dequantize(const void* codes, const void* scales, int64_t rows, int K,
                              int format, moe_dtype dtype, void* out, cudaStream_t stream);
 
@@ -579,6 +581,7 @@ moe_status moe_mx_dequantize(const void* codes, const void* scales, int64_t rows
  * operands of the quantised products).  Per row t, in float32:
  *   h = round(x[t] + residual[t]) to dtype, or x[t] without a residual
  *   y = h * rsqrt(mean(h^2) + eps) * weight
+ *       (infinities and NaN as that product of float32 values has them)
  *   residual_out[t] = h;  out[t] = round(y) to dtype
  *   codes, scales: y (not its rounded copy) as
  *     MOE_QUANT_MX_E4M3         an MX e4m3 row (above), or
@@ -609,7 +612,9 @@ moe_status moe_add_rms_norm(const void* x, const void* residual, const void* wei
  * [seg_end[e-1], seg_end[e]):
  *   p = a_row(m) . w[e, n, :] (+ bias[e, n])   in fp32, scales applied per block
  *   out[m, j] = act(p)_j
- * on the tensor cores (kind::mxf8f6f4, scales applied in the MMA).
+ * on the tensor cores (kind::mxf8f6f4, scales applied in the MMA).  A NaN in p
+ * is a NaN of every act.  The sigmoid is the fast exponential and quotient for
+ * every dtype, f32 too: within 2^-16 of the value.
  *   a, a_scale   MX e4m3 rows [a_rows, Kp], [a_rows, Kp / 32]
  *   row_to_route [M] i32: row m of the operand is a[row_to_route[m] / top_k]
  *                (an entry outside [0, a_rows * top_k) gives a zero row); NULL:

@@ -41,13 +41,15 @@
 // token copies reach the leader's barrier through a forwarding thread, the scale
 // warps' and epilogues' arrivals directly.
 //
-// What bounds it (GB300, median of flushed runs): decode (128 rows on 123
-// experts, 2048 x 7168 gate_up) the weights' stream, 300 us for 1.92 GB, 94% of
-// the measured HBM rate; medium batches (64 rows an expert) what the ring holds
-// in flight, 80 KB of packed weights an SM, half its memory going to the gaps of
-// the expanded form: 0.7 of HBM; 1024 rows an expert the MMAs, 1188 us, 0.84 of
-// twice the measured bf16 rate, the rest shared-memory contention and the one
-// accumulator's epilogue.
+// What bounds it (GB300, median of single launches, L2 flushed): decode (one row
+// on each of 128 experts, 2048 x 7168 gate_up) the weights' stream, 318 us for
+// 2.0 GB, 0.93 of the measured HBM rate; medium batches (8192 ragged rows on 128
+// experts, 2880 x 2880 down: 142 us, 0.66 of HBM) what the ring holds in flight,
+// 80 KB of packed weights an SM, half its memory going to the gaps of the expanded
+// form, and the weights of experts of several chunks, read again a chunk; many rows
+// (65536 ragged ones on 64 experts, 2048 x 7168 gate_up) the MMAs, 1254 us, 0.79 of
+// twice the measured bf16 rate (one after another 1367: the power cap), the rest
+// shared-memory contention and the one accumulator's epilogue.
 // Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
 
@@ -1050,24 +1052,31 @@ cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const
   p.out_t = out_dt;
   p.even = Nout % 2 == 0 && (reinterpret_cast<uintptr_t>(out) & 3) == 0;
   // Token columns of a tile, by the rows an expert that has any gets on
-  // average (the host does not know the counts):
-  //   up to 8     16 columns, six stages in flight: decode, bound by the weights.
-  //               A plain product whose tiles would not reach every SM takes
-  //               128 weight rows a tile instead of 256.
-  //   up to 48    64 columns, five stages; above, uneven counts start to need two
-  //               chunks (35 rows an expert on 128 experts, 2880 x 2880: gate_up 210
-  //               us, down 126; 229 and 132 with pairs of 96.  64 rows an expert,
-  //               counts uneven, the whole layer: 467 us, 421 with pairs)
-  //   up to 160   96 columns on a pair, two accumulators (8192 ragged rows, down
-  //               2880 x 2880: 148 us; 156 with 64, 152 with 96 on one CTA, 164
-  //               with 224)
+  // average (the host does not know the counts; us, single launches, L2 flushed):
+  //   up to 8     16 columns, six stages in flight: decode, bound by the weights (one
+  //               row on each of 128 experts, 2048 x 7168 gate_up: 318, 324 with 64
+  //               columns).  Uneven counts soon need two chunks of 16 (24 rows on each
+  //               of 32 experts, 2880 x 2880 gate_up: 91, 70 with 64).  A plain product
+  //               whose tiles would not reach every SM takes 128 weight rows a tile
+  //               instead of 256.
+  //   up to 48    64 columns, five stages (2661 ragged rows on 128 experts, 768 x 2048:
+  //               56, 58 with pairs of 96, 70 with 16).  Above, uneven counts start to
+  //               need two chunks (8192 ragged rows on 128 experts, 2880 x 2880 down:
+  //               152, 142 with pairs of 96), although even ones of up to 64 do not
+  //               (64 rows on each of 64 experts: 76, 80 with pairs)
+  //   up to 160   96 columns on a pair, two accumulators (the 8192 rows: 142; 146 with
+  //               96 on one CTA, 162 with 224 on a pair)
   //   above       224 columns on a pair, one accumulator: the fewest bytes per
-  //               product (1024 rows an expert, 2048 x 7168: 1188 us, 1522 with 96, 1322
-  //               with 208 on one CTA, whose token copies and shared-memory reads
+  //               product (65536 ragged rows, 2048 x 7168 gate_up: 1254, 1506 with 96,
+  //               1342 with 208 on one CTA, whose token copies and shared-memory reads
   //               double), unless the product is so short that the epilogue, which
-  //               one accumulator does not hide, costs more than that saves (256
-  //               rows an expert, 768 x 2048, MX out: 161 us, 132 with 96; 16-bit out,
-  //               whose epilogue is half as long: 117 and 122)
+  //               one accumulator does not hide, costs more than that saves.  1024 rows
+  //               on each of 16 experts, 2048 outputs, gated, 224 columns against 96:
+  //               MX out 232 and 226 at 28 stages of K, 242 and 244 at 29; 16-bit out,
+  //               whose epilogue is half as long, 136 and 134 at 14, 140 and 138 at
+  //               15, 160 and 163 at 20.  512 rows: MX out equal at 28, 16-bit out 62
+  //               and 64 at 14.  Where rows just fill chunks of 96 (256 an expert), 96
+  //               stays ahead at every length (by 11 to 20% with 16-bit out).
   switch (act ? act->kind : MOE_ACT_IDENTITY) {
     case MOE_ACT_SILU_AND_MUL: return go_out<true, MOE_ACT_SILU_AND_MUL>(w, p, s);
     case MOE_ACT_SWIGLU: return go_out<true, MOE_ACT_SWIGLU>(w, p, s);

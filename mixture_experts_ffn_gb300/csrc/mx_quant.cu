@@ -2,10 +2,10 @@
 // scale rules).  One pass: eight consecutive columns a thread, so four
 // neighbouring lanes own a 32-column block and agree on its scale with two
 // shuffles.  Bound by HBM: a bf16 element moves 2 bytes in and 33/32 (e4m3)
-// or 17/32 (e2m1) out.  184320 x 2880 bf16: to e2m1 257 us, to e4m3 286, back
-// from e2m1 252 (5.2 to 5.7 TB/s, a torch copy in the same harness 5.2); the
-// next item's load is issued before an item is converted (268 and 257 us
-// without), four items a thread in flight were slower (370 us).
+// or 17/32 (e2m1) out.  184320 x 2880 bf16: to e2m1 242 us, to e4m3 271, back
+// from e2m1 236, from e4m3 263 (5.5 to 6.1 TB/s); the next item's load is issued
+// before an item is converted (4% faster), four items a thread in flight were
+// slower (by 30%).
 #include <algorithm>
 #include <type_traits>
 
@@ -19,7 +19,7 @@ constexpr int kThreads = 256;
 // Item i: columns 8 (i % ipr) .. of row i / ipr, ipr = Kp / 8 (a multiple of
 // 16, so a block's four lanes never straddle two rows).  A thread's next item
 // is a grid's width on: row and column advance by fixed amounts, so the loop
-// divides nothing (286 us to e2m1 with a division an item).
+// divides nothing (6% of the time to e2m1).
 struct Walk {
   uint32_t i, row, col, ipr, step, drow, dcol;
   __device__ __forceinline__ explicit Walk(uint32_t ipr_) {

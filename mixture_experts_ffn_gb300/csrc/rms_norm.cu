@@ -10,10 +10,12 @@
 // rounding instead of two.  Squares are summed in float32, a chain for each of
 // a thread's eight columns, then across lanes and warps in a fixed order.
 //
-// Bound by HBM: x and r in, h, y and the codes out, each once; a row stays in
-// registers between the sum and the scaling.  8192 x 7168 bf16, all outputs:
-// 89 us for 530 MB, 6.0 TB/s, 0.88 of the measured copy rate (85 us with a plain
-// float32 root and products); one row of 7168: 5.5 us, launch latency.
+// Bound by HBM: x and r in, h, y and the codes out, each once; a row of up to
+// 32768 columns stays in registers between the sum and the scaling.  8192 x 7168
+// bf16, all outputs: 90 us for 530 MB, 5.9 TB/s, 0.87 of the measured copy rate;
+// one row of 7168: 5.3 us, launch latency.  Wider rows have eight groups of eight
+// columns a thread, which do not fit the registers of 1024 threads: 1024 x 65536
+// takes 351 us (1.7 TB/s), 1024 x 32768 67 (4.5).
 #include <algorithm>
 #include <type_traits>
 
@@ -178,10 +180,13 @@ cudaError_t go(const NormArgs& p, int threads, cudaStream_t s) {
   return e;
 }
 
-// Threads of a row: short rows (up to 1024 columns) take a warp each, eight
-// to a CTA.  Longer ones take a CTA each: with enough rows to fill the GPU,
-// four groups of eight columns a thread keep more bytes in flight per thread;
-// with fewer rows than SMs, one group a thread shortens the one row's path.
+// Threads of a row (bf16, residual, MX out; us, L2 flushed): short rows (up to
+// 1024 columns) take a warp each, eight to a CTA (8192 x 256: 15.5, 17.6 with a
+// CTA a row).  Longer ones take a CTA each.  Rows for every SM: four groups of
+// eight columns a thread keep more bytes in flight per thread (8192 x 7168: 91,
+// 140 with one group; 1000 x 2880: 12.4 and 14.4).  Fewer rows than SMs: one
+// group a thread shortens the one row's path (one row of 7168: 8.4, 10.4 with
+// four; 16 x 2880: 9.3 and 9.4).
 template <typename T, int QUANT, bool VEC>
 cudaError_t pick(const NormArgs& p, cudaStream_t s) {
   const int items = p.Hp / 8;
