@@ -151,7 +151,7 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # None: a CPU build of torch
 
 
 def _stream_of(t: torch.Tensor) -> int:

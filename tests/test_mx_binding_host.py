@@ -1,6 +1,10 @@
 """The Python binding's checks of the microscaled operators, on the CPU: the
 library behind the binding is a stand-in that records the calls it gets, so a
 call that must be refused is seen to get no further, and no kernel runs."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -223,3 +227,15 @@ def test_codes_and_scales_of_another_format_are_refused(moe):
     refused(moe, lambda: moe.moe_mx_quantize(x, moe.MOE_MX_E2M1, codes=u8(T, H // 2).view(e4)), TypeError)
     refused(moe, lambda: norm(moe, quant=1, codes=u8(T, H).view(e5)), TypeError)
     refused(moe, lambda: norm(moe, quant=1, scales=u8(T, H // 32).view(e4)), TypeError)
+
+
+def test_the_binding_imports_without_a_cuda_build_of_torch():
+    """A torch built for the CPU has no stream handles to ask for; the binding is imported there all
+    the same (build checks, workspace sizes)."""
+    code = ("import torch\n"
+            "del torch._C._cuda_getCurrentRawStream\n"
+            "from mixture_experts_ffn_gb300 import moe\n"
+            "assert moe.moe_mx_columns(2880) == 2944\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root)
+    assert r.returncode == 0, r.stderr
