@@ -32,7 +32,7 @@ _GATED = (MOE_ACT_SILU_AND_MUL, MOE_ACT_SWIGLU, MOE_ACT_GELU_AND_MUL)
 # types that MX codes and scales are taken in: bytes, or the format's own
 _E4M3 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
 _E2M1 = (torch.uint8, torch.int8, getattr(torch, "float4_e2m1fn_x2", torch.uint8))
-_E8M0 = (torch.float8_e8m0fnu, torch.uint8, torch.int8)
+_E8M0 = (getattr(torch, "float8_e8m0fnu", torch.uint8), torch.uint8, torch.int8)
 
 # C entry points and their argument types (mirrors include/moe.h)
 _vp, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, \
