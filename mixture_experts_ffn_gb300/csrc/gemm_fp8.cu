@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(NUM_THREADS)
           sa1 = in_slab ? __ldg(sa + kb + 2) : 0.f;
           sb1 = col_ok ? __ldg(sb + kb + 2) : 0.f;
         }
-        if (!wait_pair(&sh->pfull[pb], pph, abort_flag, status)) { ok = false; break; }
+        if (!wait_pair_tmem(&sh->pfull[pb], pph, abort_flag, status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t taddr =
             tmem_base + lane_addr + (uint32_t)(pb * BN + half * kColsPerWarp);
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(NUM_THREADS)
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(pb ? pempty_leader1 : pempty_leader0);
+            if (lane == 0) mbar_arrive_cluster_tmem(pb ? pempty_leader1 : pempty_leader0);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -395,8 +395,8 @@ __global__ void __launch_bounds__(NUM_THREADS)
         const uint64_t bdesc0 = sw128_desc(su32(smem + A_BYTES));
         for (int tile = pair; tile < total && ok; tile += npairs) {
           for (int kb = 0; kb < nkb; ++kb) {
-            if (!wait_pair(&sh->pempty[pb], pph ^ 1u, abort_flag, status)) { ok = false; break; }
-            if (!wait_pair(&sh->full[stage], phase, abort_flag, status)) { ok = false; break; }
+            if (!wait_pair_tmem(&sh->pempty[pb], pph ^ 1u, abort_flag, status)) { ok = false; break; }
+            if (!wait_fast(&sh->full[stage], phase, abort_flag, status)) { ok = false; break; }
             tc_fence_after();
             const uint64_t off = (uint64_t)((stage * STAGE_BYTES) >> 4);
             umma2_fp8_block(tmem_base + (uint32_t)(pb * BN), adesc0 + off, bdesc0 + off,

@@ -609,9 +609,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t phase = 0, aphase = 0, sphase = 0;
     bool ok = true, any = false;
     const uint64_t ad0 = sw128_desc(su32(smem));
-    // a pair's barriers take arrivals of both CTAs: acquire at cluster scope
-    auto try_full = [&](uint64_t* b, uint32_t parity) {
-      return PAIR ? mbar_try_wait_cluster(su32(b), parity) : mbar_try_wait(su32(b), parity);
+    // a pair's barriers take arrivals of both CTAs: cluster scope
+    auto try_full = [&](uint32_t parity) {
+      const uint32_t b = su32(&sh->full[stage]);
+      return PAIR ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity);
+    };
+    auto try_scales = [&](uint32_t parity) {
+      const uint32_t b = su32(&sh->sfull[slot]);
+      return PAIR ? mbar_try_wait_cluster<false>(b, parity) : mbar_try_wait(b, parity);
     };
     // warp reductions leave their result in a uniform register
     const uint32_t tm0 = __reduce_max_sync(0xffffffffu, tmem);
@@ -619,7 +624,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const MxTile t = decode(tile);
       if (t.nv == 0) continue;
       ok = __all_sync(0xffffffffu,
-                      wait_pair<PAIR>(&sh->tempty[acc], aphase ^ 1u, abort_flag, p.status));
+                      wait_pair_tmem<PAIR>(&sh->tempty[acc], aphase ^ 1u, abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tm0 + (uint32_t)(acc * C::ACC_COLS);
@@ -627,15 +632,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int kb = 0; kb < nkb; ++kb) {
         // both barriers tried at once, the slow paths only when one is not there yet
         const bool first = kb % C::TG == 0;
-        const bool f0 = try_full(&sh->full[stage], phase);
-        const bool f1 = !first || try_full(&sh->sfull[slot], sphase);
+        const bool f0 = try_full(phase);
+        const bool f1 = !first || try_scales(sphase);
         if (!__all_sync(0xffffffffu, f0 && f1)) {
           ok = wait_bar(&sh->full[stage], phase, abort_flag, p.status);
           if (first) ok = wait_bar(&sh->sfull[slot], sphase, abort_flag, p.status) && ok;
           // done, so these return at once; they order the peer's writes
           if (PAIR && ok) {
-            ok = try_full(&sh->full[stage], phase);
-            if (first) ok = try_full(&sh->sfull[slot], sphase) && ok;
+            ok = try_full(phase);
+            if (first) ok = try_scales(sphase) && ok;
           }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -847,7 +852,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               __syncwarp();
               if (lane == 0) {
                 if constexpr (PAIR)
-                  mbar_arrive_cluster(map_to_rank(su32(&sh->sfull[slot]), 0));
+                  mbar_arrive_cluster_tmem(map_to_rank(su32(&sh->sfull[slot]), 0));
                 else
                   mbar_arrive(&sh->sfull[slot]);
               }
@@ -890,7 +895,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (HALVES == 2 && f + 128 < p.Nout) b[1] = bias_at(f + 128);
         }
       }
-      if (!wait_pair<PAIR>(&sh->tfull[acc], aphase, abort_flag, p.status)) break;
+      if (!wait_pair_tmem<PAIR>(&sh->tfull[acc], aphase, abort_flag, p.status)) break;
       tc_fence_after();
       const uint32_t base = lanes + (uint32_t)(acc * C::ACC_COLS);
 #pragma unroll 1
@@ -924,7 +929,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         if constexpr (PAIR)
-          mbar_arrive_cluster(map_to_rank(su32(&sh->tempty[acc]), 0));
+          mbar_arrive_cluster_tmem(map_to_rank(su32(&sh->tempty[acc]), 0));
         else
           mbar_arrive(&sh->tempty[acc]);
       }

@@ -714,11 +714,11 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
         const uint32_t idesc = idesc_sw(2 * ROWS, st.N, F16 ? 1 : 0);  // M256 per MMA
         // token atoms h rows apart (16-byte descriptor units)
         const uint32_t b_atom16 = (uint32_t)((32 << tok_box_sel(st.N >> 1)) * BK * 2) >> 4;
-        if (!wait_pair(&sh->tempty[acc], aphase ^ 1u, abort_flag, status)) { ok = false; break; }
+        if (!wait_pair_tmem(&sh->tempty[acc], aphase ^ 1u, abort_flag, status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * NMAX);
         for (int ks = 0; ks < nks; ++ks) {
-          if (!wait_pair(&sh->full[stage], phase, abort_flag, status)) { ok = false; break; }
+          if (!wait_pair<TOK == kTokCpAsync>(&sh->full[stage], phase, abort_flag, status)) { ok = false; break; }
           // cp.async rows of this CTA were written through the generic proxy;
           // the MMA reads them through the async proxy (the peer's forwarder
           // fences the peer's rows)
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
       const int tile = next_tile(j);
       if (tile >= total) break;
       const SwTile st = decode(tile);
-      if (!wait_pair(&sh->tfull[acc], aphase, abort_flag, status)) break;
+      if (!wait_pair_tmem(&sh->tfull[acc], aphase, abort_flag, status)) break;
       tc_fence_after();
       const __nv_bfloat16* be = bias ? bias + (size_t)st.e * N1 : nullptr;
       const uint32_t tq = tmem_base + ((uint32_t)(quad * 32) << 16);
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
       // the drain's TMEM loads have completed (tcgen05.wait::ld) and are
       // ordered before the leader's next MMAs
       tc_fence_before();
-      mbar_arrive_cluster(tempty_remote[acc]);
+      mbar_arrive_cluster_tmem(tempty_remote[acc]);
       if (++acc == NACC) { acc = 0; aphase ^= 1u; }
     }
     if (lane == 0) bulk_wait_all();  // every staged box written before the pair exits

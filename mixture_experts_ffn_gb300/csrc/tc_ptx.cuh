@@ -80,41 +80,64 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
-// The CTAs of a pair synchronise at cluster scope.  What they order is the SMs'
-// own shared memory (after the proxy fence) and TMEM (after the tcgen05 fence),
-// so release and acquire are fences restricted to shared memory around relaxed
-// operations on the barrier: an unrestricted release at this scope also waits for
-// the SM's copies from global memory, a microsecond a stage (gemm_mx.cu, 8192
-// ragged rows, 2880 x 2880: 138 us, 322 with it).
+// The CTAs of a pair synchronise at cluster scope, in two ways.
+//  TMEM (a drained accumulator, stored scales): tcgen05 fences around relaxed
+//    operations on the barrier, before the arrival and after the wait.
+//  Shared memory (the peer's token rows, a stage that MMAs have read): release and
+//    acquire fences restricted to shared memory around them.  An unrestricted
+//    release at this scope also waits for the SM's copies from global memory, a
+//    microsecond a stage (gemm_mx.cu, 8192 ragged rows, 2880 x 2880: 138 us, 322
+//    with it).
 //
-// arrival on a barrier of either CTA of the pair (shared::cluster address)
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
-  asm volatile(
-      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
-      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
-      : "memory");
+// arrivals on a barrier of either CTA of the pair (shared::cluster address): after
+// tc_fence_before, and after this thread saw shared memory written
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+               : "memory");
 }
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  mbar_arrive_cluster_tmem(bar_cluster);
+}
+template <bool ACQUIRE = true>
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t"
-      "@p fence.acquire.sync_restrict::shared::cluster.cluster;\n\t}"
-      : "=r"(ok)
-      : "r"(addr), "r"(parity)
-      : "memory");
+  if constexpr (ACQUIRE)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "@p fence.acquire.sync_restrict::shared::cluster.cluster;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity)
+        : "memory");
   return ok != 0;
 }
 // Wait for a barrier that the other CTA of a pair arrives on too, or whose commit
-// the other CTA issued.  Once wait_bar has seen the phase, the second try returns
-// at once (the next phase waits for the caller).
-template <bool PAIR = true>
+// the other CTA issued; ACQUIRE: it hands over shared memory, else TMEM alone (the
+// caller goes on with tc_fence_after).  Once wait_bar has seen the phase, the
+// second try returns at once (the next phase waits for the caller).
+template <bool PAIR = true, bool ACQUIRE = true>
 __device__ __forceinline__ bool wait_pair(uint64_t* b, uint32_t parity, volatile int* abort_flag,
                                           int* status) {
   if constexpr (!PAIR) return wait_fast(b, parity, abort_flag, status);
-  if (mbar_try_wait_cluster(su32(b), parity)) return true;
-  return wait_bar(b, parity, abort_flag, status) && mbar_try_wait_cluster(su32(b), parity);
+  if (mbar_try_wait_cluster<ACQUIRE>(su32(b), parity)) return true;
+  return wait_bar(b, parity, abort_flag, status) &&
+         mbar_try_wait_cluster<ACQUIRE>(su32(b), parity);
+}
+// ... one that hands over TMEM alone
+template <bool PAIR = true>
+__device__ __forceinline__ bool wait_pair_tmem(uint64_t* b, uint32_t parity,
+                                               volatile int* abort_flag, int* status) {
+  return wait_pair<PAIR, false>(b, parity, abort_flag, status);
 }
 
 // Bounded wait used while draining after an abort (ignores the abort flag).
