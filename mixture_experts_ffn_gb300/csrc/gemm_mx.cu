@@ -609,15 +609,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t phase = 0, aphase = 0, sphase = 0;
     bool ok = true, any = false;
     const uint64_t ad0 = sw128_desc(su32(smem));
-    // a pair's barriers take arrivals of both CTAs: cluster scope
-    auto try_full = [&](uint32_t parity) {
-      const uint32_t b = su32(&sh->full[stage]);
-      return PAIR ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity);
-    };
-    auto try_scales = [&](uint32_t parity) {
-      const uint32_t b = su32(&sh->sfull[slot]);
-      return PAIR ? mbar_try_wait_cluster<false>(b, parity) : mbar_try_wait(b, parity);
-    };
+    // a pair's barriers take arrivals of both CTAs
+    constexpr int kRows = PAIR ? kWaitShared : kWaitCta, kScales = PAIR ? kWaitTmem : kWaitCta;
     // warp reductions leave their result in a uniform register
     const uint32_t tm0 = __reduce_max_sync(0xffffffffu, tmem);
     for (int tile = unit; tile < total && ok; tile += units) {
@@ -632,16 +625,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int kb = 0; kb < nkb; ++kb) {
         // both barriers tried at once, the slow paths only when one is not there yet
         const bool first = kb % C::TG == 0;
-        const bool f0 = try_full(phase);
-        const bool f1 = !first || try_scales(sphase);
+        const bool f0 = try_wait<kRows>(su32(&sh->full[stage]), phase);
+        const bool f1 = !first || try_wait<kScales>(su32(&sh->sfull[slot]), sphase);
         if (!__all_sync(0xffffffffu, f0 && f1)) {
-          ok = wait_bar(&sh->full[stage], phase, abort_flag, p.status);
-          if (first) ok = wait_bar(&sh->sfull[slot], sphase, abort_flag, p.status) && ok;
-          // done, so these return at once; they order the peer's writes
-          if (PAIR && ok) {
-            ok = try_full(phase);
-            if (first) ok = try_scales(sphase) && ok;
-          }
+          ok = wait_bar<kRows>(&sh->full[stage], phase, abort_flag, p.status);
+          if (first) ok = wait_bar<kScales>(&sh->sfull[slot], sphase, abort_flag, p.status) && ok;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }

@@ -37,31 +37,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t addr, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait for the phase of parity `parity`; false on abort or timeout.
-static __device__ __noinline__ bool wait_bar(uint64_t* b, uint32_t parity, volatile int* abort_flag,
-                                      int* status) {
-  const uint32_t addr = su32(b);
-  if (mbar_try_wait(addr, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(addr, parity)) return true;
-    if (*abort_flag) return false;
-    if (global_ns() - t0 > kTimeoutNs) {
-      *abort_flag = 1;
-      latch_error(status, kDevTimeout);
-      return false;
-    }
-  }
-}
-// Fast path inline (no call, no register save/restore when the phase is
-// already complete); the bounded spin stays out of line.
-__device__ __forceinline__ bool wait_fast(uint64_t* b, uint32_t parity, volatile int* abort_flag,
-                                          int* status) {
-  if (mbar_try_wait(su32(b), parity)) return true;
-  return wait_bar(b, parity, abort_flag, status);
-}
 
 // ---------------------------------------------------------------- pairs of CTAs
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -121,23 +96,52 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t pa
         : "memory");
   return ok != 0;
 }
-// Wait for a barrier that the other CTA of a pair arrives on too, or whose commit
-// the other CTA issued; ACQUIRE: it hands over shared memory, else TMEM alone (the
-// caller goes on with tc_fence_after).  Once wait_bar has seen the phase, the
-// second try returns at once (the next phase waits for the caller).
-template <bool PAIR = true, bool ACQUIRE = true>
+// How a wait orders what comes after it: after this CTA's accesses; after the TMEM
+// (by the caller's tc_fence_after) or the shared memory of both CTAs of a pair.
+enum WaitKind { kWaitCta, kWaitTmem, kWaitShared };
+template <int W>
+__device__ __forceinline__ bool try_wait(uint32_t addr, uint32_t parity) {
+  if constexpr (W == kWaitCta) return mbar_try_wait(addr, parity);
+  else return mbar_try_wait_cluster<W == kWaitShared>(addr, parity);
+}
+// Bounded wait for the phase of parity `parity`; false on abort or timeout.
+template <int W = kWaitCta>
+static __device__ __noinline__ bool wait_bar(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+                                      int* status) {
+  const uint32_t addr = su32(b);
+  if (try_wait<W>(addr, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (try_wait<W>(addr, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kTimeoutNs) {
+      *abort_flag = 1;
+      latch_error(status, kDevTimeout);
+      return false;
+    }
+  }
+}
+// Fast path inline (no call, no register save/restore when the phase is
+// already complete); the bounded spin stays out of line.
+template <int W = kWaitCta>
+__device__ __forceinline__ bool wait_fast(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+                                          int* status) {
+  if (try_wait<W>(su32(b), parity)) return true;
+  return wait_bar<W>(b, parity, abort_flag, status);
+}
+// Waits for a barrier that the other CTA of a pair arrives on too, or whose commit
+// the other CTA issued, and that hands over shared memory, or TMEM alone.
+template <bool PAIR = true>
 __device__ __forceinline__ bool wait_pair(uint64_t* b, uint32_t parity, volatile int* abort_flag,
                                           int* status) {
-  if constexpr (!PAIR) return wait_fast(b, parity, abort_flag, status);
-  if (mbar_try_wait_cluster<ACQUIRE>(su32(b), parity)) return true;
-  return wait_bar(b, parity, abort_flag, status) &&
-         mbar_try_wait_cluster<ACQUIRE>(su32(b), parity);
+  return wait_fast<PAIR ? kWaitShared : kWaitCta>(b, parity, abort_flag, status);
 }
-// ... one that hands over TMEM alone
 template <bool PAIR = true>
 __device__ __forceinline__ bool wait_pair_tmem(uint64_t* b, uint32_t parity,
                                                volatile int* abort_flag, int* status) {
-  return wait_pair<PAIR, false>(b, parity, abort_flag, status);
+  return wait_fast<PAIR ? kWaitTmem : kWaitCta>(b, parity, abort_flag, status);
 }
 
 // Bounded wait used while draining after an abort (ignores the abort flag).
