@@ -42,13 +42,13 @@
 // warps' and epilogues' arrivals directly.
 //
 // What bounds it (GB300, median of single launches, L2 flushed): decode (one row
-// on each of 128 experts, 2048 x 7168 gate_up) the weights' stream, 318 us for
-// 2.0 GB, 0.93 of the measured HBM rate; medium batches (8192 ragged rows on 128
+// on each of 128 experts, 2048 x 7168 gate_up) the weights' stream, 312 us for
+// 2.0 GB, 0.94 of the measured HBM rate; medium batches (8192 ragged rows on 128
 // experts, 2880 x 2880 down: 142 us, 0.66 of HBM) what the ring holds in flight,
 // 80 KB of packed weights an SM, half its memory going to the gaps of the expanded
 // form, and the weights of experts of several chunks, read again a chunk; many rows
-// (65536 ragged ones on 64 experts, 2048 x 7168 gate_up) the MMAs, 1254 us, 0.79 of
-// twice the measured bf16 rate (one after another 1367: the power cap), the rest
+// (65536 ragged ones on 64 experts, 2048 x 7168 gate_up) the MMAs, 1156 us, 0.86 of
+// twice the measured bf16 rate (one after another 1324: the power cap), the rest
 // shared-memory contention and the one accumulator's epilogue.
 // Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
@@ -241,6 +241,16 @@ __device__ __forceinline__ void mx_commit_elect(uint32_t bar) {
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
             bar)
         : "memory");
+}
+// Wait for a stage's release, which a pair's leader commits to both CTAs: polled as a
+// barrier of this CTA alone, then acquired at cluster scope.  Polling at that scope
+// takes longer (1024 rows on each of 16 experts, 2048 x 1920 gate_up, 16-bit out: 148
+// us, 128 so; 2048 x 7168: 325 and 310).
+template <bool PAIR>
+__device__ __forceinline__ bool wait_stage(uint64_t* b, uint32_t parity, volatile int* abort_flag,
+                                           int* status) {
+  return wait_fast(b, parity, abort_flag, status) &&
+         (!PAIR || try_wait<kWaitShared>(su32(b), parity));
 }
 // a load into this CTA's shared memory that completes on a barrier of the
 // pair's leader (shared::cluster address)
@@ -537,7 +547,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       bool ok = true;
       auto take = [&](int freed) {  // waits for the stage; freed: the slot it was to free
-        if (!wait_pair<PAIR>(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) return false;
+        if (!wait_stage<PAIR>(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) return false;
         if (freed >= 0) {
           tc_fence_after();
           tc_fence_before();
@@ -688,7 +698,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         at[i] = (uint32_t)max(m, 0) * (uint32_t)nkb;
       }
       for (int kb = 0; kb < nkb; ++kb) {
-        if (!wait_pair<PAIR>(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) {
+        if (!wait_stage<PAIR>(&sh->empty[stage], phase ^ 1u, abort_flag, p.status)) {
           ok = false;
           break;
         }
@@ -1047,29 +1057,31 @@ cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows, const
   // Token columns of a tile, by the rows an expert that has any gets on
   // average (the host does not know the counts; us, single launches, L2 flushed):
   //   up to 8     16 columns, six stages in flight: decode, bound by the weights (one
-  //               row on each of 128 experts, 2048 x 7168 gate_up: 318, 324 with 64
+  //               row on each of 128 experts, 2048 x 7168 gate_up: 312, 314 with 64
   //               columns).  Uneven counts soon need two chunks of 16 (24 rows on each
-  //               of 32 experts, 2880 x 2880 gate_up: 91, 70 with 64).  A plain product
+  //               of 32 experts, 2880 x 2880 gate_up: 91, 68 with 64).  A plain product
   //               whose tiles would not reach every SM takes 128 weight rows a tile
   //               instead of 256.
   //   up to 48    64 columns, five stages (2661 ragged rows on 128 experts, 768 x 2048:
-  //               56, 58 with pairs of 96, 70 with 16).  Above, uneven counts start to
+  //               56, 58 with pairs of 96, 64 with 16).  Above, uneven counts start to
   //               need two chunks (8192 ragged rows on 128 experts, 2880 x 2880 down:
   //               152, 142 with pairs of 96), although even ones of up to 64 do not
-  //               (64 rows on each of 64 experts: 76, 80 with pairs)
+  //               (64 rows on each of 64 experts: 74, 79 with pairs)
   //   up to 160   96 columns on a pair, two accumulators (the 8192 rows: 142; 146 with
   //               96 on one CTA, 162 with 224 on a pair)
   //   above       224 columns on a pair, one accumulator: the fewest bytes per
-  //               product (65536 ragged rows, 2048 x 7168 gate_up: 1254, 1506 with 96,
-  //               1342 with 208 on one CTA, whose token copies and shared-memory reads
+  //               product (65536 ragged rows, 2048 x 7168 gate_up: 1156, 1494 with 96,
+  //               1293 with 208 on one CTA, whose token copies and shared-memory reads
   //               double), unless the product is so short that the epilogue, which
-  //               one accumulator does not hide, costs more than that saves.  1024 rows
-  //               on each of 16 experts, 2048 outputs, gated, 224 columns against 96:
-  //               MX out 232 and 226 at 28 stages of K, 242 and 244 at 29; 16-bit out,
-  //               whose epilogue is half as long, 136 and 134 at 14, 140 and 138 at
-  //               15, 160 and 163 at 20.  512 rows: MX out equal at 28, 16-bit out 62
-  //               and 64 at 14.  Where rows just fill chunks of 96 (256 an expert), 96
-  //               stays ahead at every length (by 11 to 20% with 16-bit out).
+  //               one accumulator does not hide, costs more than that saves: up to 28
+  //               stages of K with MX out (1024 rows on each of 16 experts, 2048 outputs,
+  //               gated: 234 and 224 with 96 at 28 stages, 244 and 242 at 29, 357 and 394
+  //               at 56; 512 rows, 768 outputs: 105 and 103 at 28, 109 and 111 at 29), up
+  //               to 14 with 16-bit out, whose epilogue is half as long.  There the
+  //               lengths at which the two cross lie apart: rows that just fill chunks
+  //               of 96 stay ahead with 96 (256 an expert, 768 outputs: 70 and 64 at 14
+  //               stages, 181 and 177 at 56), others are ahead with 224 from 6 stages on
+  //               (1024 an expert, 2048 outputs: 87 and 89 at 6, 124 and 132 at 14).
   switch (act ? act->kind : MOE_ACT_IDENTITY) {
     case MOE_ACT_SILU_AND_MUL: return go_out<true, MOE_ACT_SILU_AND_MUL>(w, p, s);
     case MOE_ACT_SWIGLU: return go_out<true, MOE_ACT_SWIGLU>(w, p, s);
