@@ -662,6 +662,98 @@ moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, cons
 size_t moe_workspace_size_mx(int T, int H, int F, int E, int K);
 
 /* ------------------------------------------------------------------------ */
+/* Gradients of the layer's stages (an addition; the pages describe the forward
+ * pass).  A training step runs
+ *   moe_route_permute, moe_permute_gather (x), moe_grouped_gemm (p = x w1^T + b1,
+ *   no activation), moe_act_checkpoint (a = act(p)), moe_grouped_gemm_down (y),
+ *   moe_combine
+ * and back
+ *   moe_combine_backward (d_y, d_topk_weights), moe_grouped_gemm_dgrad (d_a),
+ *   moe_act_backward (d_p, and a again), moe_grouped_gemm_wgrad (d_w2, d_b2 of
+ *   d_y and a; d_w1, d_b1 of d_p and x), moe_grouped_gemm_dgrad (d_x),
+ *   moe_permute_backward (d_hidden), moe_route_backward (d_logits).
+ * Sums are float32 and in a fixed order (every call repeats itself bit for bit);
+ * each result is rounded once. */
+
+/* Gradient of moe_combine, out[t] = scale * sum_k w[t,k] y[route_to_row[t*K+k]]:
+ *   d_expert_out[row(t,k)] = scale * w[t,k] * d_out[t]
+ *   d_topk_weights[t,k] = scale * <d_out[t], expert_out[row(t,k)]>
+ * Either output may be NULL, and then its own input (topk_weights, expert_out) too.
+ *   d_out [T, H] dtype;  expert_out [T*K, H] dtype;  topk_weights [T, K] f32;
+ *   route_to_row [T*K] i32, its entries distinct (moe_permute's are);
+ *   d_expert_out [T*K, H] dtype out;  d_topk_weights [T, K] f32 out.
+ * Rows of d_expert_out that no route names are not written; a route whose entry
+ * is outside [0, T*K) gets a zero weight gradient and writes no row. */
+moe_status moe_combine_backward(const void* d_out, const void* expert_out,
+                                const float* topk_weights, const int32_t* route_to_row, int T,
+                                int K, int H, moe_dtype dtype, float scale, void* d_expert_out,
+                                float* d_topk_weights, cudaStream_t stream);
+
+/* Gradient of the permutation, expert_input[route_to_row[t*K+k]] = hidden[t]:
+ *   d_hidden[t] = sum_k d_expert_input[route_to_row[t*K+k]], in float32 in order
+ * of k.  An entry outside [0, T*K) adds nothing.
+ *   d_expert_input [T*K, H] dtype;  route_to_row [T*K] i32;  d_hidden [T, H] dtype. */
+moe_status moe_permute_backward(const void* d_expert_input, const int32_t* route_to_row, int T,
+                                int K, int H, moe_dtype dtype, void* d_hidden,
+                                cudaStream_t stream);
+
+/* The activation of a product's rows p and an 8-bit checkpoint of p, in one pass:
+ *   out[m] = act(p[m]) (act as moe_grouped_gemm_act's, of the unquantised p)
+ *   codes, scales: p[m] as an MX e4m3 row (moe_mx_quantize's codes and scales)
+ *   p [M, N1] dtype, N1 = 2F for a gated act (halves, or pairs for SwiGLU fusion
+ *   1), F otherwise;  out [M, F] dtype or NULL;
+ *   codes [M, N1p], scales [M, N1p / 32], N1p = N1 rounded up to 128;
+ *   seg_end [E] i32 or NULL (then E is ignored).
+ * With seg_end, rows at and past seg_end[E-1] are neither read nor written.
+ * codes and scales 16-byte aligned (MOE_ERR_UNSUPPORTED otherwise);
+ * M * N1p < 2^34. */
+moe_status moe_act_checkpoint(const void* p, const int32_t* seg_end, int M, int F, int E,
+                              moe_dtype dtype, const moe_act_params* act, void* out, void* codes,
+                              void* scales, cudaStream_t stream);
+
+/* Gradient of the activation, with its argument from the checkpoint (scales
+ * given: p holds e4m3 codes) or as it was (scales NULL: p [M, N1] dtype):
+ *   d_p[m] = d_out[m] * act'(p[m]);  out[m] = act(p[m])
+ * A clamp passes the gradient up to and at its bound and stops it past it; relu
+ * passes it for p > 0.  A NaN of p gives NaN.
+ *   d_out [M, F] dtype;  d_p [M, N1] dtype out;  out [M, F] dtype or NULL;
+ *   p, scales, seg_end, alignment and extents as moe_act_checkpoint. */
+moe_status moe_act_backward(const void* p, const void* scales, const void* d_out,
+                            const int32_t* seg_end, int M, int F, int E, moe_dtype dtype,
+                            const moe_act_params* act, void* d_p, void* out, cudaStream_t stream);
+
+/* Gradients of a grouped product out[m] = a[m] . w[e]^T + bias[e] over the tight
+ * layout (moe_grouped_gemm with MOE_LAYOUT_PSUM and no act, moe_grouped_gemm_down):
+ *   dgrad  d_a[m, k] = sum_n d_out[m, n] w[e, n, k] for the rows m of expert e
+ *   wgrad  d_w[e, n, k] = sum_m d_out[m, n] a[m, k],  d_bias[e, n] = sum_m d_out[m, n]
+ *          over the rows m of expert e; zeros for an expert without rows
+ *   d_out [M, N] dtype;  a, d_a [M, K] dtype;  w, d_w [E, N, K] dtype;
+ *   d_bias [E, N] dtype or NULL;  seg_end [E] i32 as moe_grouped_gemm_act;
+ *   ws >= MOE_STATUS_BYTES bytes (dgrad), moe_grouped_gemm_wgrad_workspace_size (wgrad).
+ * Rows past seg_end[E-1] are neither read nor written.  Every element of d_w and
+ * d_bias is written.  16-bit operands run on the tensor cores when N % 8 == 0,
+ * K % 8 == 0 and the operands and results are 16-byte aligned; float32 and other
+ * shapes in float32 FMA.  E <= 1024. */
+moe_status moe_grouped_gemm_dgrad(const void* d_out, const void* w, const int32_t* seg_end, int M,
+                                  int N, int K, int E, moe_dtype dtype, void* d_a, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream);
+moe_status moe_grouped_gemm_wgrad(const void* d_out, const void* a, const int32_t* seg_end, int M,
+                                  int N, int K, int E, moe_dtype dtype, void* d_w, void* d_bias,
+                                  void* ws, size_t ws_bytes, cudaStream_t stream);
+size_t moe_grouped_gemm_wgrad_workspace_size(int M, int N, int K, int E);
+
+/* Gradient of moe_route's topk_weights with respect to the logits, for the ids
+ * that it chose or was given (an id may come twice); scoring, renormalisation and
+ * the scaling factor from p.  Selection, bias and groups have no gradient, and
+ * the MoERouter outputs none here (p->local_expert_count must be 0).
+ *   logits [T, E] p->dtype;  topk_ids [T, K] i32;  d_topk_weights [T, K] f32;
+ *   d_logits [T, E] p->dtype out, zero where an expert was not chosen and has no
+ *   part in a sum.  An id outside [0, E) takes no part. */
+moe_status moe_route_backward(const void* logits, const int32_t* topk_ids,
+                              const float* d_topk_weights, int T, int E,
+                              const moe_route_params* p, void* d_logits, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Shared expert [TileOPs, SharedExpertMLPFwdOp]: the dense gated MLP applied
  * to every token,
  *     out = down(silu(hidden @ gate^T) * (hidden @ up^T)),

@@ -1133,6 +1133,143 @@ moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, cons
   return cuda_status(err);
 }
 
+// ---------------------------------------------------------------- gradients
+moe_status moe_combine_backward(const void* d_out, const void* expert_out,
+                                const float* topk_weights, const int32_t* route_to_row, int T,
+                                int K, int H, moe_dtype dtype, float scale, void* d_expert_out,
+                                float* d_topk_weights, cudaStream_t stream) {
+  if (T < 0 || K < 1 || H < 1 || !dtype_ok(dtype) || (long long)T * K >= (1LL << 31))
+    return MOE_ERR_INVALID_ARG;
+  if (!d_expert_out && !d_topk_weights && T > 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!d_out || !route_to_row || (d_topk_weights && !expert_out) || (d_expert_out && !topk_weights))
+    return MOE_ERR_INVALID_ARG;
+  const size_t esz = esize(dtype), M = (size_t)T * K;
+  for (const void* ptr : {d_out, expert_out, (const void*)d_expert_out})
+    if (!aligned(ptr, esz)) return MOE_ERR_INVALID_ARG;
+  Span outs[] = {{d_expert_out, M * H * esz}, {d_topk_weights, M * 4}};
+  Span ins[] = {{d_out, (size_t)T * H * esz}, {d_topk_weights ? expert_out : nullptr, M * H * esz},
+                {d_expert_out ? topk_weights : nullptr, M * 4}, {route_to_row, M * 4}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  return cuda_status(launch_combine_backward(d_out, expert_out, topk_weights, route_to_row, T, K, H,
+                                             dtype, scale, d_expert_out, d_topk_weights, stream));
+}
+
+moe_status moe_permute_backward(const void* d_expert_input, const int32_t* route_to_row, int T,
+                                int K, int H, moe_dtype dtype, void* d_hidden,
+                                cudaStream_t stream) {
+  if (T < 0 || K < 1 || H < 1 || !dtype_ok(dtype) || (long long)T * K >= (1LL << 31))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!d_expert_input || !route_to_row || !d_hidden) return MOE_ERR_INVALID_ARG;
+  const size_t esz = esize(dtype), M = (size_t)T * K;
+  if (!aligned(d_expert_input, esz) || !aligned(d_hidden, esz)) return MOE_ERR_INVALID_ARG;
+  Span outs[] = {{d_hidden, (size_t)T * H * esz}};
+  Span ins[] = {{d_expert_input, M * H * esz}, {route_to_row, M * 4}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  return cuda_status(
+      launch_permute_backward(d_expert_input, route_to_row, T, K, H, dtype, d_hidden, stream));
+}
+
+moe_status moe_act_checkpoint(const void* p, const int32_t* seg_end, int M, int F, int E,
+                              moe_dtype dtype, const moe_act_params* act, void* out, void* codes,
+                              void* scales, cudaStream_t stream) {
+  if (M < 0 || F < 1 || F > (1 << 23) || (seg_end && E < 1) || !dtype_ok(dtype) || !act_ok(act))
+    return MOE_ERR_INVALID_ARG;
+  const int N1 = gated_kind(act->kind) ? 2 * F : F;
+  if (!mx_extent_ok(M, N1)) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  const size_t esz = esize(dtype), Np = mx_pad(N1);
+  if (!p || !codes || !scales || !aligned(p, esz) || !aligned(out, esz)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(codes) || !aligned16(scales)) return MOE_ERR_UNSUPPORTED;
+  Span outs[] = {{out, (size_t)M * F * esz}, {codes, M * Np}, {scales, M * Np / 32}};
+  Span ins[] = {{p, (size_t)M * N1 * esz}, {seg_end, (size_t)E * 4}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  return cuda_status(
+      launch_act_checkpoint(p, seg_end, E, M, F, dtype, *act, out, codes, scales, stream));
+}
+
+moe_status moe_act_backward(const void* p, const void* scales, const void* d_out,
+                            const int32_t* seg_end, int M, int F, int E, moe_dtype dtype,
+                            const moe_act_params* act, void* d_p, void* out, cudaStream_t stream) {
+  if (M < 0 || F < 1 || F > (1 << 23) || (seg_end && E < 1) || !dtype_ok(dtype) || !act_ok(act))
+    return MOE_ERR_INVALID_ARG;
+  const int N1 = gated_kind(act->kind) ? 2 * F : F;
+  if (!mx_extent_ok(M, N1)) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  const size_t esz = esize(dtype), Np = mx_pad(N1), n = (size_t)M * N1 * esz, f = (size_t)M * F * esz;
+  if (!p || !d_out || !d_p || !aligned(d_out, esz) || !aligned(d_p, esz) || !aligned(out, esz) ||
+      (!scales && !aligned(p, esz)))
+    return MOE_ERR_INVALID_ARG;
+  if (scales && (!aligned16(p) || !aligned16(scales))) return MOE_ERR_UNSUPPORTED;
+  Span outs[] = {{d_p, n}, {out, f}};
+  Span ins[] = {{p, scales ? M * Np : n}, {scales, M * Np / 32}, {d_out, f},
+                {seg_end, (size_t)E * 4}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  return cuda_status(
+      launch_act_backward(p, scales, d_out, seg_end, E, M, F, dtype, *act, d_p, out, stream));
+}
+
+moe_status moe_grouped_gemm_dgrad(const void* d_out, const void* w, const int32_t* seg_end, int M,
+                                  int N, int K, int E, moe_dtype dtype, void* d_a, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream) {
+  if (!mx_gemm_extent_ok(M, N, K, E) || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+  const size_t esz = esize(dtype);
+  if (!seg_end || !w || (M > 0 && (!d_out || !d_a))) return MOE_ERR_INVALID_ARG;
+  for (const void* ptr : {d_out, w, (const void*)d_a})
+    if (!aligned(ptr, esz)) return MOE_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, MOE_STATUS_BYTES)) return MOE_ERR_WORKSPACE;
+  Span outs[] = {{d_a, (size_t)M * K * esz}, {ws, MOE_STATUS_BYTES}};
+  Span ins[] = {{d_out, (size_t)M * N * esz}, {w, (size_t)E * N * K * esz},
+                {seg_end, (size_t)E * 4}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  if (M == 0) return MOE_OK;
+  return cuda_status(launch_dgrad_simt(d_out, w, seg_end, M, N, K, E, dtype, d_a, stream));
+}
+
+size_t moe_grouped_gemm_wgrad_workspace_size(int M, int N, int K, int E) {
+  if (!mx_gemm_extent_ok(M, N, K, E)) return 0;
+  return MOE_STATUS_BYTES;
+}
+
+moe_status moe_grouped_gemm_wgrad(const void* d_out, const void* a, const int32_t* seg_end, int M,
+                                  int N, int K, int E, moe_dtype dtype, void* d_w, void* d_bias,
+                                  void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!mx_gemm_extent_ok(M, N, K, E) || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
+  const size_t esz = esize(dtype);
+  if (!seg_end || !d_w || (M > 0 && (!d_out || !a))) return MOE_ERR_INVALID_ARG;
+  for (const void* ptr : {d_out, a, (const void*)d_w, (const void*)d_bias})
+    if (!aligned(ptr, esz)) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe_grouped_gemm_wgrad_workspace_size(M, N, K, E);
+  if (!ws_ok(ws, ws_bytes, need)) return MOE_ERR_WORKSPACE;
+  Span outs[] = {{d_w, (size_t)E * N * K * esz}, {d_bias, (size_t)E * N * esz}, {ws, need}};
+  Span ins[] = {{d_out, (size_t)M * N * esz}, {a, (size_t)M * K * esz}, {seg_end, (size_t)E * 4}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  if (d_bias) {
+    const cudaError_t e = launch_bias_grad(d_out, seg_end, M, N, E, dtype, d_bias, stream);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  return cuda_status(launch_wgrad_simt(d_out, a, seg_end, M, N, K, E, dtype, d_w, stream));
+}
+
+moe_status moe_route_backward(const void* logits, const int32_t* topk_ids,
+                              const float* d_topk_weights, int T, int E,
+                              const moe_route_params* p, void* d_logits, cudaStream_t stream) {
+  const moe_status st =
+      check_route(logits, nullptr, T, E, p, d_topk_weights, topk_ids, nullptr, nullptr);
+  if (st != MOE_OK) return st;
+  if (p->local_expert_count != 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!d_logits || !aligned(logits, rsz(p)) || !aligned(d_logits, rsz(p)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t TK = (size_t)T * p->top_k, n = (size_t)T * E * rsz(p);
+  Span outs[] = {{d_logits, n}};
+  Span ins[] = {{logits, n}, {topk_ids, TK * 4}, {d_topk_weights, TK * 4}};
+  if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  return cuda_status(
+      launch_route_backward(logits, topk_ids, d_topk_weights, T, E, *p, d_logits, stream));
+}
+
 size_t moe_workspace_size_host(int T, int H, int F, int E, int K, moe_dtype dtype) {
   size_t base = moe_workspace_size(T, H, F, E, K, dtype);
   if (base == 0) return 0;

@@ -231,6 +231,32 @@ cudaError_t launch_gemm_mx(const void* a, const void* a_scale, int a_rows,
 cudaError_t launch_mx_combine(const float* y, const float* w, const int32_t* route_to_row, int T,
                               int K, int H, moe_dtype dt, void* out, cudaStream_t s);
 
+// ---- gradients
+// d_y and d_w may be null (combine_backward.cu)
+cudaError_t launch_combine_backward(const void* d_out, const void* y, const float* w,
+                                    const int32_t* route_to_row, int T, int K, int H, moe_dtype dt,
+                                    float scale, void* d_y, float* d_w, cudaStream_t s);
+// sums of a token's K rows (permute.cu: the combine with weights of one)
+cudaError_t launch_permute_backward(const void* d_x, const int32_t* route_to_row, int T, int K,
+                                    int H, moe_dtype dt, void* d_hidden, cudaStream_t s);
+// seg_end null: all M rows; out may be null; scales null: p is of type dt (act_backward.cu)
+cudaError_t launch_act_checkpoint(const void* p, const int32_t* seg_end, int E, int M, int F,
+                                  moe_dtype dt, const moe_act_params& act, void* out, void* codes,
+                                  void* scales, cudaStream_t s);
+cudaError_t launch_act_backward(const void* p, const void* scales, const void* d_out,
+                                const int32_t* seg_end, int E, int M, int F, moe_dtype dt,
+                                const moe_act_params& act, void* d_p, void* out, cudaStream_t s);
+// float32 FMA gradients of a grouped product (gemm_grad_simt.cu)
+cudaError_t launch_dgrad_simt(const void* d, const void* w, const int32_t* seg_end, int M, int N,
+                              int K, int E, moe_dtype dt, void* d_a, cudaStream_t s);
+cudaError_t launch_wgrad_simt(const void* d, const void* a, const int32_t* seg_end, int M, int N,
+                              int K, int E, moe_dtype dt, void* d_w, cudaStream_t s);
+cudaError_t launch_bias_grad(const void* d, const int32_t* seg_end, int M, int N, int E,
+                             moe_dtype dt, void* d_bias, cudaStream_t s);
+cudaError_t launch_route_backward(const void* logits, const int32_t* ids, const float* d_w, int T,
+                                  int E, const moe_route_params& p, void* d_logits,
+                                  cudaStream_t s);
+
 // indexed per-route decode path (bf16, silu_and_mul, no bias)
 cudaError_t launch_indexed(const void* hidden, const void* w1, const void* w2, const float* w,
                            const int32_t* ids, int T, int H, int F, int E, int K, float scale,

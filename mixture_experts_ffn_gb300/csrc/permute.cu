@@ -177,11 +177,12 @@ __global__ void __launch_bounds__(256) perm_gather(const char* __restrict__ hidd
   }
 }
 
-// out[t] = scale * sum_k w[t,k] * y[route_to_row[t*K+k]], fixed k order, fp32.
+// out[t] = scale * sum_k w[t,k] * y[route_to_row[t*K+k]], fixed k order, fp32;
+// without WEIGHTED the plain sum of the rows (the permutation's gradient).
 // One item = VEC consecutive columns of one token; persistent grid-stride
 // threads take items i, i + stride, ..., so that each thread keeps several
 // rows' loads in flight and no block is launched for a few loads only.
-template <typename T, int VEC>
+template <typename T, int VEC, bool WEIGHTED>
 __device__ __forceinline__ void combine_item(const T* __restrict__ y, const float* __restrict__ w,
                                              const int32_t* __restrict__ r2r, int K, int H,
                                              int M, float scale, T* __restrict__ out, int t,
@@ -191,7 +192,7 @@ __device__ __forceinline__ void combine_item(const T* __restrict__ y, const floa
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
   const int32_t* rr = r2r + (size_t)t * K;
-  const float* ww = w + (size_t)t * K;
+  const float* ww = WEIGHTED ? w + (size_t)t * K : nullptr;
   for (int k0 = 0; k0 < K; k0 += 8) {
     // all index and weight loads of the group first, then the row loads
     int row[8];
@@ -200,7 +201,8 @@ __device__ __forceinline__ void combine_item(const T* __restrict__ y, const floa
     for (int j = 0; j < 8; ++j) {
       const bool in = k0 + j < K;
       row[j] = in ? __ldg(rr + k0 + j) : -1;
-      wk[j] = in ? __ldg(ww + k0 + j) : 0.f;
+      if constexpr (WEIGHTED) wk[j] = in ? __ldg(ww + k0 + j) : 0.f;
+      else wk[j] = 1.f;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -247,7 +249,7 @@ __device__ __forceinline__ void combine_item(const T* __restrict__ y, const floa
   }
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool WEIGHTED = true>
 __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ y,
                                                       const float* __restrict__ w,
                                                       const int32_t* __restrict__ r2r, int Tn,
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const T* __restrict__ y,
   const long long stride = (long long)gridDim.x * blockDim.x;
   for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < items; i += stride) {
     const int t = (int)(i / nvec), v = (int)(i - (long long)t * nvec);
-    combine_item<T, VEC>(y, w, r2r, K, H, M, scale, out, t, v, tscale);
+    combine_item<T, VEC, WEIGHTED>(y, w, r2r, K, H, M, scale, out, t, v, tscale);
   }
 }
 
@@ -506,6 +508,35 @@ cudaError_t launch_combine(const void* y, const float* w, const int32_t* r2r, in
   }
   count_launch();
   return cudaGetLastError();
+}
+
+cudaError_t launch_permute_backward(const void* d_x, const int32_t* route_to_row, int T, int K,
+                                    int H, moe_dtype dt, void* d_hidden, cudaStream_t s) {
+  if (T == 0) return cudaSuccess;
+  const bool aligned = ((uintptr_t)d_x % 16 == 0) && ((uintptr_t)d_hidden % 16 == 0);
+  cudaError_t e = cudaSuccess;
+  auto go = [&](auto tag, auto vec) {
+    using B = decltype(tag);
+    constexpr int V = decltype(vec)::value;
+    const auto kern = combine_kernel<B, V, false>;
+    const long long items = (long long)T * (H / V);
+    const long long cap = (long long)num_sms() * resident_ctas((const void*)kern, 256);
+    e = launch_pdl(kern, dim3((unsigned)std::max<long long>(1, std::min(cap, (items + 255) / 256))),
+                   dim3(256), 0, s, static_cast<const B*>(d_x),
+                   static_cast<const float*>(nullptr), route_to_row, T, K, H, T * K, 1.0f,
+                   static_cast<B*>(d_hidden), static_cast<const float*>(nullptr));
+  };
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
+  using Eight = std::integral_constant<int, 8>;
+  if (dt == MOE_F32)
+    aligned && H % 4 == 0 ? go(float{}, Four{}) : go(float{}, One{});
+  else if (dt == MOE_F16)
+    aligned && H % 8 == 0 ? go(__half{}, Eight{}) : go(__half{}, One{});
+  else
+    aligned && H % 8 == 0 ? go(__nv_bfloat16{}, Eight{}) : go(__nv_bfloat16{}, One{});
+  count_launch();
+  return e;
 }
 
 }  // namespace moe

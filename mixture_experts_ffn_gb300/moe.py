@@ -90,6 +90,14 @@ _SIGNATURES = {
     "moe_ffn_forward_mx": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
                            _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
     "moe_workspace_size_mx": [_i, _i, _i, _i, _i],
+    "moe_combine_backward": [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp],
+    "moe_permute_backward": [_vp, _vp, _i, _i, _i, _i, _vp, _vp],
+    "moe_act_checkpoint": [_vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp],
+    "moe_act_backward": [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp],
+    "moe_grouped_gemm_dgrad": [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp],
+    "moe_grouped_gemm_wgrad": [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp],
+    "moe_grouped_gemm_wgrad_workspace_size": [_i, _i, _i, _i],
+    "moe_route_backward": [_vp, _vp, _vp, _i, _i, _vp, _vp, _vp],
     "moe_shared_expert_workspace_size": [_i, _i, _i, _i],
     "moe_ffn_forward_shared": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp,
                                _vp, _vp, _vp, _vp, _sz, _vp],
@@ -110,6 +118,7 @@ _RESTYPES = {"moe_workspace_size": _sz, "moe_permute_workspace_size": _sz,
              "moe_workspace_size_shared": _sz, "moe_permute_align_workspace_size": _sz,
              "moe_grouped_gemm_workspace_size": _sz, "moe_workspace_size_mx": _sz,
              "moe_grouped_gemm_mx_workspace_size": _sz,
+             "moe_grouped_gemm_wgrad_workspace_size": _sz,
              "moe_status_string": ctypes.c_char_p, "moe_launch_count": ctypes.c_uint64}
 
 _lib = None
@@ -208,6 +217,33 @@ def _cuda(*ts):
             _on_gpu(t)
             if not t.is_contiguous():
                 raise ValueError("libmoe takes contiguous tensors only")
+
+
+def _is_current(device) -> bool:
+    return device.index == torch._C._cuda_getDevice()
+
+
+def _together(first, *ts):
+    """first and those of ts that are given: contiguous CUDA tensors of the current device."""
+    _cuda(first, *ts)
+    dev = first.device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("the tensors of a call are on one device")
+    if not _is_current(dev):
+        raise ValueError("the tensors of a call are on the current device")
+
+
+def _asked(out, shape: tuple, dtype: torch.dtype, like, what: str):
+    """An output argument: True makes one, False is none, a tensor is checked."""
+    if out is True:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if out is False or out is None:
+        return None
+    _together(like, out)
+    _typed(out, dtype, what)
+    _fits(out, shape, out.element_size(), what)
+    return out
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -790,6 +826,188 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
                                   _ptr(topk_ids_out), ws.data_ptr(), ws.numel(),
                                   _stream_of(hidden)))
     return out
+
+
+def moe_combine_backward(d_out, expert_out, topk_weights, route_to_row, scale=1.0,
+                         d_expert_out=True, d_topk_weights=True):
+    """Gradient of moe_combine: (d_expert_out [T * K, H], d_topk_weights [T, K] float32).
+    Either is True (made), False (left out, None; expert_out may then be None for the
+    weights') or the tensor to write.  topk_weights [T, K]."""
+    lib = load_library()
+    _together(d_out, expert_out, topk_weights, route_to_row)
+    T, H = d_out.shape
+    _typed(topk_weights, torch.float32, "topk_weights")
+    _typed(route_to_row, torch.int32, "route_to_row")
+    _typed(expert_out, d_out.dtype, "expert_out")
+    if topk_weights.dim() != 2 or topk_weights.shape[0] != T:
+        raise ValueError("topk_weights is [T, K]")
+    K = topk_weights.shape[1]
+    if route_to_row.numel() != T * K or \
+            (expert_out is not None and expert_out.shape != (T * K, H)):
+        raise ValueError("route_to_row is [T * K] and expert_out [T * K, H]")
+    if expert_out is None and d_topk_weights is not False:
+        raise ValueError("the weights' gradient takes expert_out")
+    if K == 0:
+        raise ValueError("K is at least 1")
+    d_expert_out = _asked(d_expert_out, (T * K, H), d_out.dtype, d_out, "d_expert_out")
+    d_topk_weights = _asked(d_topk_weights, (T, K), torch.float32, d_out, "d_topk_weights")
+    _check("moe_combine_backward",
+           lib.moe_combine_backward(d_out.data_ptr(), _ptr(expert_out), topk_weights.data_ptr(),
+                                    route_to_row.data_ptr(), T, K, H, _dt(d_out), scale,
+                                    _ptr(d_expert_out), _ptr(d_topk_weights), _stream_of(d_out)))
+    return d_expert_out, d_topk_weights
+
+
+def moe_permute_backward(d_expert_input, route_to_row, K: int, d_hidden=True):
+    """Gradient of the permutation: d_hidden [T, H], the sum of a token's K rows of
+    d_expert_input [T * K, H]."""
+    lib = load_library()
+    _together(d_expert_input, route_to_row)
+    M, H = d_expert_input.shape
+    _typed(route_to_row, torch.int32, "route_to_row")
+    if K < 1 or M % K or route_to_row.numel() != M:
+        raise ValueError("d_expert_input is [T * K, H] and route_to_row [T * K]")
+    T = M // K
+    d_hidden = _asked(d_hidden, (T, H), d_expert_input.dtype, d_expert_input, "d_hidden")
+    if d_hidden is None:
+        raise ValueError("d_hidden is True or the tensor to write")
+    _check("moe_permute_backward",
+           lib.moe_permute_backward(d_expert_input.data_ptr(), route_to_row.data_ptr(), T, K, H,
+                                    _dt(d_expert_input), d_hidden.data_ptr(),
+                                    _stream_of(d_expert_input)))
+    return d_hidden
+
+
+def moe_act_checkpoint(p, act: ActParams, seg_end=None, out=True, codes=None, scales=None):
+    """The activation of a product's rows p [M, N1] and p as MX e4m3 rows: (out [M, F],
+    codes [M, N1p], scales [M, N1p / 32]); N1 = 2F for a gated act.  With seg_end, rows
+    at and past seg_end[-1] are left alone.  out: True, False, or the tensor to write."""
+    lib = load_library()
+    _together(p, seg_end, codes, scales)
+    _typed(seg_end, torch.int32, "seg_end")
+    M, N1 = p.shape
+    gated = act.kind in _GATED
+    if gated and N1 % 2:
+        raise ValueError("a gated activation takes pairs of columns")
+    F, Np = N1 // 2 if gated else N1, moe_mx_columns(N1)
+    out = _asked(out, (M, F), p.dtype, p, "out")
+    _coded(codes, _E4M3, "codes")
+    _coded(scales, _E8M0, "scales")
+    _fits(codes, (M, Np), 1, "codes")
+    _fits(scales, (M, Np // 32), 1, "scales")
+    if codes is None:
+        codes = torch.empty((M, Np), dtype=torch.float8_e4m3fn, device=p.device)
+    if scales is None:
+        scales = torch.empty((M, Np // 32), dtype=torch.float8_e8m0fnu, device=p.device)
+    _check("moe_act_checkpoint",
+           lib.moe_act_checkpoint(p.data_ptr(), _ptr(seg_end), M, F,
+                                  0 if seg_end is None else seg_end.numel(), _dt(p),
+                                  ctypes.byref(act), _ptr(out), codes.data_ptr(),
+                                  scales.data_ptr(), _stream_of(p)))
+    return out, codes, scales
+
+
+def moe_act_backward(p, d_out, act: ActParams, scales=None, seg_end=None, d_p=True, out=True):
+    """Gradient of the activation: (d_p [M, N1], out [M, F] = act(p) or None) from d_out
+    [M, F] and the checkpoint (p its codes, with scales) or p [M, N1] itself.  With
+    seg_end, rows at and past seg_end[-1] are left alone."""
+    lib = load_library()
+    _together(d_out, p, scales, seg_end)
+    _typed(seg_end, torch.int32, "seg_end")
+    M, F = d_out.shape
+    N1 = 2 * F if act.kind in _GATED else F
+    if scales is None:
+        _typed(p, d_out.dtype, "p")
+        if p.shape != (M, N1):
+            raise ValueError("p is [M, N1], N1 = 2F for a gated activation")
+    else:
+        Np = moe_mx_columns(N1)
+        _coded(p, _E4M3, "p")
+        _coded(scales, _E8M0, "scales")
+        _fits(p, (M, Np), 1, "p")
+        _fits(scales, (M, Np // 32), 1, "scales")
+    d_p = _asked(d_p, (M, N1), d_out.dtype, d_out, "d_p")
+    if d_p is None:
+        raise ValueError("d_p is True or the tensor to write")
+    out = _asked(out, (M, F), d_out.dtype, d_out, "out")
+    _check("moe_act_backward",
+           lib.moe_act_backward(p.data_ptr(), _ptr(scales), d_out.data_ptr(), _ptr(seg_end), M, F,
+                                0 if seg_end is None else seg_end.numel(), _dt(d_out),
+                                ctypes.byref(act), d_p.data_ptr(), _ptr(out), _stream_of(d_out)))
+    return d_p, out
+
+
+def moe_grouped_gemm_dgrad(d_out, w, seg_end, d_a=True, ws=None):
+    """Gradient of a grouped product's rows: d_a [M, K], d_a[m] = d_out[m] . w[e] for the
+    rows m of expert e; d_out [M, N], w [E, N, K]."""
+    lib = load_library()
+    _together(d_out, w, seg_end, ws)
+    M, N = d_out.shape
+    E, _, K = w.shape
+    _typed(w, d_out.dtype, "w")
+    _typed(seg_end, torch.int32, "seg_end")
+    if w.shape[1] != N or seg_end.numel() != E:
+        raise ValueError("d_out is [M, N], w [E, N, K] and seg_end [E]")
+    d_a = _asked(d_a, (M, K), d_out.dtype, d_out, "d_a")
+    if d_a is None:
+        raise ValueError("d_a is True or the tensor to write")
+    if ws is None:
+        ws = _ws(MOE_STATUS_BYTES, d_out.device)
+    _check("moe_grouped_gemm_dgrad",
+           lib.moe_grouped_gemm_dgrad(d_out.data_ptr(), w.data_ptr(), seg_end.data_ptr(), M, N, K,
+                                      E, _dt(d_out), d_a.data_ptr(), ws.data_ptr(),
+                                      ws.numel() * ws.element_size(), _stream_of(d_out)))
+    return d_a
+
+
+def moe_grouped_gemm_wgrad_workspace_size(M, N, K, E) -> int:
+    return load_library().moe_grouped_gemm_wgrad_workspace_size(M, N, K, E)
+
+
+def moe_grouped_gemm_wgrad(d_out, a, seg_end, bias=False, d_w=True, ws=None):
+    """Gradients of a grouped product's weights and bias: (d_w [E, N, K], d_bias [E, N] or
+    None), sums over each expert's rows of d_out [M, N] and a [M, K] (zeros for an expert
+    without rows).  bias: True, False, or the tensor to write."""
+    lib = load_library()
+    _together(d_out, a, seg_end, ws)
+    M, N = d_out.shape
+    K, E = a.shape[1], seg_end.numel()
+    _typed(a, d_out.dtype, "a")
+    _typed(seg_end, torch.int32, "seg_end")
+    if a.shape[0] != M or E == 0:
+        raise ValueError("d_out is [M, N], a [M, K] and seg_end [E]")
+    d_w = _asked(d_w, (E, N, K), d_out.dtype, d_out, "d_w")
+    if d_w is None:
+        raise ValueError("d_w is True or the tensor to write")
+    d_bias = _asked(bias, (E, N), d_out.dtype, d_out, "bias")
+    if ws is None:
+        ws = _ws(lib.moe_grouped_gemm_wgrad_workspace_size(M, N, K, E), d_out.device)
+    _check("moe_grouped_gemm_wgrad",
+           lib.moe_grouped_gemm_wgrad(d_out.data_ptr(), a.data_ptr(), seg_end.data_ptr(), M, N, K,
+                                      E, _dt(d_out), d_w.data_ptr(), _ptr(d_bias), ws.data_ptr(),
+                                      ws.numel() * ws.element_size(), _stream_of(d_out)))
+    return d_w, d_bias
+
+
+def moe_route_backward(logits, topk_ids, d_topk_weights, p: RouteParams, d_logits=True):
+    """Gradient of moe_route's topk_weights with respect to the logits, [T, E] in the
+    logits' type, for the ids that moe_route returned (or was given) under p."""
+    lib = load_library()
+    _together(logits, topk_ids, d_topk_weights)
+    T, E = logits.shape
+    _typed(topk_ids, torch.int32, "topk_ids")
+    _typed(d_topk_weights, torch.float32, "d_topk_weights")
+    _fits(topk_ids, (T, p.top_k), 4, "topk_ids")
+    _fits(d_topk_weights, (T, p.top_k), 4, "d_topk_weights")
+    d_logits = _asked(d_logits, (T, E), logits.dtype, logits, "d_logits")
+    if d_logits is None:
+        raise ValueError("d_logits is True or the tensor to write")
+    rp = p if p.dtype == _dt(logits) else _rp(p, logits)
+    _check("moe_route_backward",
+           lib.moe_route_backward(logits.data_ptr(), topk_ids.data_ptr(),
+                                  d_topk_weights.data_ptr(), T, E, ctypes.byref(rp),
+                                  d_logits.data_ptr(), _stream_of(logits)))
+    return d_logits
 
 
 def moe_shared_expert_workspace_size(T, H, S, dtype=MOE_BF16) -> int:
