@@ -1224,6 +1224,11 @@ moe_status moe_grouped_gemm_dgrad(const void* d_out, const void* w, const int32_
                 {seg_end, (size_t)E * 4}};
   if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
   if (M == 0) return MOE_OK;
+  if (dtype != MOE_F32 && num_sms() >= 2 && tc_ok(d_out, w, d_a, N, K, M))
+    return cuda_status(launch_gemm_sw(d_out, w, nullptr, seg_end, M, K, N, E, nullptr, d_a,
+                                      static_cast<int*>(ws), stream, nullptr, 1, 0, 0,
+                                      dtype == MOE_F16, N >= 2048 && (long long)M >= 128LL * E,
+                                      true));
   return cuda_status(launch_dgrad_simt(d_out, w, seg_end, M, N, K, E, dtype, d_a, stream));
 }
 
@@ -1249,6 +1254,9 @@ moe_status moe_grouped_gemm_wgrad(const void* d_out, const void* a, const int32_
     const cudaError_t e = launch_bias_grad(d_out, seg_end, M, N, E, dtype, d_bias, stream);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
   }
+  if (dtype != MOE_F32 && num_sms() >= 2 && M > 0 && tc_ok(d_out, a, d_w, N, K, M))
+    return cuda_status(launch_gemm_wgrad(d_out, a, seg_end, M, N, K, E, dtype == MOE_F16, d_w,
+                                         static_cast<int*>(ws), stream));
   return cuda_status(launch_wgrad_simt(d_out, a, seg_end, M, N, K, E, dtype, d_w, stream));
 }
 

@@ -87,16 +87,6 @@ struct Fp8Shared {
 constexpr size_t kSmemBytes = (size_t)STAGES * STAGE_BYTES + OUT_BYTES + sizeof(Fp8Shared) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-// A TMA load into this CTA's shared memory that completes on the leader's
-// barrier (shared::cluster address); coordinates innermost first.
-__device__ __forceinline__ void tma2_3d(void* dst, const CUtensorMap* m, uint32_t bar, int c0,
-                                        int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(su32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
 // The four K32 MMAs of one 128-wide K block into a fresh partial sum (M256
 // across the pair), then the commits that free the stage and publish the
 // partial sum in both CTAs.
@@ -116,12 +106,6 @@ __device__ __forceinline__ void umma2_fp8_block(uint32_t d_tmem, uint64_t ad, ui
       " [%11], %12;\n\t}" ::"r"(d_tmem),
       "l"(ad), "l"(bd), "r"(kIdescFp8), "l"(ad + 2), "l"(bd + 2), "l"(ad + 4), "l"(bd + 4),
       "l"(ad + 6), "l"(bd + 6), "r"(empty_bar), "r"(pfull_bar), "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ void umma2_commit_self(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          su32(bar))
       : "memory");
 }
 // 16 consecutive fp32 columns of this thread's TMEM lane.

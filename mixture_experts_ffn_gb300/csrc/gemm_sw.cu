@@ -172,24 +172,6 @@ __device__ __forceinline__ void publish_remote_u32(uint32_t addr_cluster, uint32
       : "memory");
 }
 
-// TMA loads into this CTA's shared memory that complete on the leader's
-// barrier (shared::cluster address); coordinates innermost first.
-__device__ __forceinline__ void tma2_2d(void* dst, const CUtensorMap* m, uint32_t bar, int c0,
-                                        int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(su32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1)
-      : "memory");
-}
-__device__ __forceinline__ void tma2_3d(void* dst, const CUtensorMap* m, uint32_t bar, int c0,
-                                        int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
-      "bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(su32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
 __device__ __forceinline__ void tma2_4d(void* dst, const CUtensorMap* m, uint32_t bar, int c0,
                                         int c1, int c2, int c3) {
   asm volatile(
@@ -207,8 +189,9 @@ __device__ __forceinline__ void tma2_5d(void* dst, const CUtensorMap* m, uint32_
       : "memory");
 }
 // The eight K16 MMAs of a stage (two K atoms; atom a of A at ad + a * 16 KB,
-// of B at bd + a * b_atom, descriptor units of 16 bytes) and the commit that
-// frees the stage in both CTAs.
+// of B at bd + a * b_atom, descriptor units of 16 bytes; AS such units from one
+// K16 step of A to the next) and the commit that frees the stage in both CTAs.
+template <uint32_t AS>
 __device__ __forceinline__ void umma2_stage(uint32_t d_tmem, uint64_t ad, uint64_t bd,
                                             uint32_t b_atom16, uint32_t idesc,
                                             uint32_t accumulate, uint32_t bar) {
@@ -227,14 +210,16 @@ __device__ __forceinline__ void umma2_stage(uint32_t d_tmem, uint64_t ad, uint64
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %18, %19, %3, t;\n\t"
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%5], %20;\n\t}" ::"r"(d_tmem),
-      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "l"(ad + 2), "l"(bd + 2),
-      "l"(ad + 4), "l"(bd + 4), "l"(ad + 6), "l"(bd + 6), "l"(ad1), "l"(bd1), "l"(ad1 + 2),
-      "l"(bd1 + 2), "l"(ad1 + 4), "l"(bd1 + 4), "l"(ad1 + 6), "l"(bd1 + 6), "h"((uint16_t)3)
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "l"(ad + AS), "l"(bd + 2),
+      "l"(ad + 2 * AS), "l"(bd + 4), "l"(ad + 3 * AS), "l"(bd + 6), "l"(ad1), "l"(bd1),
+      "l"(ad1 + AS),
+      "l"(bd1 + 2), "l"(ad1 + 2 * AS), "l"(bd1 + 4), "l"(ad1 + 3 * AS), "l"(bd1 + 6), "h"((uint16_t)3)
       : "memory");
 }
 // The eight K16 MMAs of a one-atom stage with two M halves per CTA: half h's
 // weight atom at ad + h * 16 KB accumulates into d0 + h * NMAX, both halves
 // reading the same token slice (bd); then the commit that frees the stage.
+template <uint32_t AS>
 __device__ __forceinline__ void umma2_stage_wide(uint32_t d0, uint64_t ad, uint64_t bd,
                                                  uint32_t idesc, uint32_t accumulate,
                                                  uint32_t bar) {
@@ -254,31 +239,11 @@ __device__ __forceinline__ void umma2_stage_wide(uint32_t d0, uint64_t ad, uint6
       "tcgen05.mma.cta_group::2.kind::f16 [%1], %16, %15, %4, t;\n\t"
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%6], %17;\n\t}" ::"r"(d0),
-      "r"(d1), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "l"(a1), "l"(ad + 2),
-      "l"(bd + 2), "l"(a1 + 2), "l"(ad + 4), "l"(bd + 4), "l"(a1 + 4), "l"(ad + 6), "l"(bd + 6),
-      "l"(a1 + 6), "h"((uint16_t)3)
+      "r"(d1), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "l"(a1), "l"(ad + AS),
+      "l"(bd + 2), "l"(a1 + AS), "l"(ad + 2 * AS), "l"(bd + 4), "l"(a1 + 2 * AS),
+      "l"(ad + 3 * AS), "l"(bd + 6), "l"(a1 + 3 * AS), "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ void umma2_commit_both(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(su32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ void umma2_commit_self(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          su32(bar))
-      : "memory");
-}
-// Instruction descriptor, kind::f16 with f32 accumulation, both operands
-// K-major: bf16 (or float16 when f16) A and B, M x N.
-__device__ __forceinline__ uint32_t idesc_sw(int M, int N, int f16) {
-  const uint32_t fmt = f16 ? 0u : ((1u << 7) | (1u << 10));
-  return (1u << 4) | fmt | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
 // One pair tile: expert e, weight-row tile nt (256 rows: 128 per CTA), and a
 // chunk of the expert's rows [m0, m0 + nv) as the N dimension (N columns,
 // nv <= N <= 256, N a multiple of 16 and at least 32).  nv == 0: an empty
@@ -533,7 +498,10 @@ __device__ __forceinline__ int tok_box_sel(int half) { return half <= 32 ? 0 : h
 // segmented row space is source row grows[r] / gdiv (the hidden states read
 // through the permutation; rows with an out-of-range entry read zeros) or,
 // without grows, row r of the source itself.
-template <int MODE, int ACT, bool F16, int TOK, int MH>
+// WT: the weights are [E][K][N1], N1 contiguous (the gradient of a product's rows
+// contracts over its weight rows): two boxes {64 of N1, 64 of K} make an atom's
+// 128 weight rows, and A is MN-major; all else is as with K contiguous.
+template <int MODE, int ACT, bool F16, int TOK, int MH, bool WT = false>
 __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
     gemm_sw_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ TokMaps tm_a,
                    const __grid_constant__ CUtensorMap tm_out, int tma_out,
@@ -668,9 +636,12 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
 #pragma unroll
             for (int h = 0; h < MH; ++h) {
               uint8_t* dst = a_dst + (a * MH + h) * ATOM_BYTES;
-              if constexpr (MODE == kSwPlain)
-                tma2_3d(dst, &tm_w, bar, k0,
-                        (st.nt * MH + h) * 2 * ROWS + ROWS * (int)rank, st.e);
+              const int row0 = (st.nt * MH + h) * 2 * ROWS + ROWS * (int)rank;
+              if constexpr (WT) {
+                tma2_3d(dst, &tm_w, bar, row0, k0, st.e);
+                tma2_3d(dst + ATOM_BYTES / 2, &tm_w, bar, row0 + ROWS / 2, k0, st.e);
+              } else if constexpr (MODE == kSwPlain)
+                tma2_3d(dst, &tm_w, bar, k0, row0, st.e);
               else if constexpr (MH == 2)  // half 0 the gate rows, half 1 the up rows
                 tma2_4d(dst, &tm_w, bar, k0, st.nt * 2 * ROWS + ROWS * (int)rank, h, st.e);
               else
@@ -703,15 +674,17 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, aphase = 0;
       bool ok = true, any = false;
-      const uint64_t adesc0 = sw128_desc(su32(smem));
+      const uint64_t adesc0 =
+          WT ? sw128_mn_desc(su32(smem), ATOM_BYTES / 2) : sw128_desc(su32(smem));
       const uint64_t bdesc0 = sw128_desc(su32(smem + A_BYTES));
+      constexpr uint32_t AS = WT ? kMnStep : 2;
       uint32_t empty_addr[STAGES];
       for (int s = 0; s < STAGES; ++s) empty_addr[s] = su32(&sh->empty[s]);
       for (int j = 0; ok; ++j) {
         const int tile = next_tile(j);
         if (tile >= total) break;
         const SwTile st = decode(tile);
-        const uint32_t idesc = idesc_sw(2 * ROWS, st.N, F16 ? 1 : 0);  // M256 per MMA
+        const uint32_t idesc = idesc_sw(2 * ROWS, st.N, F16 ? 1 : 0, WT);  // M256 per MMA
         // token atoms h rows apart (16-byte descriptor units)
         const uint32_t b_atom16 = (uint32_t)((32 << tok_box_sel(st.N >> 1)) * BK * 2) >> 4;
         if (!wait_pair_tmem(&sh->tempty[acc], aphase ^ 1u, abort_flag, status)) { ok = false; break; }
@@ -726,10 +699,10 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
           tc_fence_after();
           const uint64_t off = (uint64_t)((stage * STAGE_BYTES) >> 4);
           if constexpr (MH == 2)
-            umma2_stage_wide(d_tmem, adesc0 + off, bdesc0 + off, idesc, ks != 0 ? 1u : 0u,
-                             empty_addr[stage]);
+            umma2_stage_wide<AS>(d_tmem, adesc0 + off, bdesc0 + off, idesc, ks != 0 ? 1u : 0u,
+                                 empty_addr[stage]);
           else
-            umma2_stage(d_tmem, adesc0 + off, bdesc0 + off, b_atom16, idesc, ks != 0 ? 1u : 0u,
+            umma2_stage<AS>(d_tmem, adesc0 + off, bdesc0 + off, b_atom16, idesc, ks != 0 ? 1u : 0u,
                         empty_addr[stage]);
           any = true;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -926,13 +899,20 @@ const void* pick_sw_mh(bool f16, int tok, int mode, int kind) {
                                  : pick_sw<false, kTokCpAsync, MH>(mode, kind));
 }
 
+// the product with transposed weights (no bias, no activation, tiled rows)
+template <int MH>
+const void* pick_sw_wt(bool f16) {
+  return f16 ? (const void*)gemm_sw_kernel<kSwPlain, MOE_ACT_IDENTITY, true, kTokTiled, MH, true>
+             : (const void*)gemm_sw_kernel<kSwPlain, MOE_ACT_IDENTITY, false, kTokTiled, MH, true>;
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_sw(const void* a, const void* w, const void* bias, const int32_t* seg_end,
                            int M, int N, int K, int E, const moe_act_params* act, void* out,
                            int* status, cudaStream_t s, const int32_t* gather_rows,
                            int gather_div, int gather_src_rows, int seg_stride, bool f16,
-                           bool wide) {
+                           bool wide, bool w_transposed) {
   if (M == 0 || N == 0) return cudaSuccess;
   int mode = kSwPlain, kind = MOE_ACT_IDENTITY, N1 = N, inter = 0;
   float limit = 0.f, alpha = 1.f, beta = 0.f;
@@ -946,9 +926,16 @@ cudaError_t launch_gemm_sw(const void* a, const void* w, const void* bias, const
     beta = act->beta;
   }
   if (N % 8 != 0 || K % 8 != 0) return cudaErrorInvalidValue;
+  if (w_transposed && (act || bias || gather_rows)) return cudaErrorInvalidValue;
   CUtensorMap mw, mo;
   const uint64_t K2 = (uint64_t)K * 2;
-  if (mode == kSwPlain) {
+  if (w_transposed) {
+    cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)K, (cuuint64_t)E};
+    cuuint64_t str[2] = {(cuuint64_t)N * 2, (cuuint64_t)N * K2};
+    cuuint32_t box[3] = {ROWS / 2, BK, 1};
+    if (!tmap::encode_bf16(&mw, w, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, f16))
+      return cudaErrorInvalidValue;
+  } else if (mode == kSwPlain) {
     cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N1, (cuuint64_t)E};
     cuuint64_t str[2] = {K2, (cuuint64_t)N1 * K2};
     cuuint32_t box[3] = {BK, ROWS, 1};
@@ -1008,7 +995,9 @@ cudaError_t launch_gemm_sw(const void* a, const void* w, const void* bias, const
   }
   if (!tma_out) mo = mw;  // unused
   const int mh = wide ? 2 : 1;
-  const void* kern = wide ? pick_sw_mh<2>(f16, tok, mode, kind) : pick_sw_mh<1>(f16, tok, mode, kind);
+  const void* kern = w_transposed ? (wide ? pick_sw_wt<2>(f16) : pick_sw_wt<1>(f16))
+                     : wide       ? pick_sw_mh<2>(f16, tok, mode, kind)
+                                  : pick_sw_mh<1>(f16, tok, mode, kind);
   set_smem_limit(kern, (int)kSmemBytes);
   const int n_ftiles = mode == kSwPlain ? (N + 2 * ROWS * mh - 1) / (2 * ROWS * mh)
                                         : (N + ROWS * mh - 1) / (ROWS * mh);

@@ -193,11 +193,13 @@ cudaError_t launch_gemm_tc(const void* a, const void* w, const void* bias, const
 // The weights-as-M tcgen05 grouped GEMM on SM pairs (gemm_sw.cu): the same
 // contract as launch_gemm_tc without split weights; N and K multiples of 8.
 // wide: 256 weight rows per CTA (two M256 accumulators) instead of 128.
+// w_transposed: w is [E][K][N] (no act, bias or gather): the gradient of a
+// product's rows, with N its input and K its output columns.
 cudaError_t launch_gemm_sw(const void* a, const void* w, const void* bias, const int32_t* seg_end,
                            int M, int N, int K, int E, const moe_act_params* act, void* out,
                            int* status, cudaStream_t s, const int32_t* gather_rows,
                            int gather_div, int gather_src_rows, int seg_stride, bool f16,
-                           bool wide);
+                           bool wide, bool w_transposed = false);
 
 // block-scaled FP8 grouped GEMM over a masked slab (e4m3 operands, fp32
 // scales per row x 128 K of a and per 128 x 128 block of b, bf16 out)
@@ -251,6 +253,10 @@ cudaError_t launch_dgrad_simt(const void* d, const void* w, const int32_t* seg_e
                               int K, int E, moe_dtype dt, void* d_a, cudaStream_t s);
 cudaError_t launch_wgrad_simt(const void* d, const void* a, const int32_t* seg_end, int M, int N,
                               int K, int E, moe_dtype dt, void* d_w, cudaStream_t s);
+// tcgen05 weights' gradient of 16-bit operands (gemm_wgrad.cu); M >= 1, N and K
+// multiples of 8, all 16-byte aligned
+cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_end, int M, int N,
+                              int K, int E, bool f16, void* d_w, int* status, cudaStream_t s);
 cudaError_t launch_bias_grad(const void* d, const int32_t* seg_end, int M, int N, int E,
                              moe_dtype dt, void* d_bias, cudaStream_t s);
 cudaError_t launch_route_backward(const void* logits, const int32_t* ids, const float* d_w, int T,
