@@ -177,6 +177,262 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// ---------------------------------------------------------------- eight columns a thread
+// The shape of p and of the activation, known when compiled.
+enum Form { kSilu, kGelu, kSwigluHalves, kSwigluPairs, kPlain };
+
+// Eight consecutive elements as they sit in memory.
+template <typename T>
+struct Raw8 {
+  uint4 q[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {  // read once: first to leave the caches
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) q[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[sizeof(T) / 2 - 1].x,
+                           q[sizeof(T) / 2 - 1].y, q[sizeof(T) / 2 - 1].z, q[sizeof(T) / 2 - 1].w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+    } else {
+      constexpr bool F16 = std::is_same<T, __half>::value;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = lo16<F16>(u[i]);
+        v[2 * i + 1] = hi16<F16>(u[i]);
+      }
+    }
+  }
+};
+
+// Item i: output columns 8 (i % ipr) .. of row i / ipr; a thread's next item is a
+// grid's width on, so the loop divides nothing.
+struct Items {
+  uint32_t i, row, col, ipr, step, drow, dcol, count;
+  __device__ __forceinline__ Items(uint32_t ipr_, uint32_t rows) : ipr(ipr_), count(ipr_ * rows) {
+    i = blockIdx.x * kThreads + threadIdx.x;
+    step = gridDim.x * kThreads;
+    row = i / ipr;
+    col = i - row * ipr;
+    drow = step / ipr;
+    dcol = step - drow * ipr;
+  }
+  __device__ __forceinline__ bool more() const { return i < count; }
+  __device__ __forceinline__ void next() {
+    i += step;
+    row += drow;
+    col += dcol;
+    if (col >= ipr) {
+      col -= ipr;
+      ++row;
+    }
+  }
+};
+
+// The activation of eight columns, x (and y, the up values) its argument.
+template <int FORM, bool FAST>
+__device__ __forceinline__ void act8(const float (&x)[8], const float (&y)[8], const float (&d)[8],
+                                     const ActArgs& A, float (&a)[8], float (&dx)[8],
+                                     float (&dy)[8]) {
+  constexpr int KIND = FORM == kSilu   ? MOE_ACT_SILU_AND_MUL
+                       : FORM == kGelu ? MOE_ACT_GELU_AND_MUL
+                                       : MOE_ACT_SWIGLU;
+  if constexpr (FORM != kPlain) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gated_pair<FAST>(KIND, x[i], y[i], d[i], A, a[i], dx[i], dy[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) plain_value<FAST>(A.kind, x[i], d[i], a[i], dx[i]);
+  }
+}
+// (gate, up) pairs of sixteen consecutive columns
+__device__ __forceinline__ void unzip(const float (&lo)[8], const float (&hi)[8], float (&x)[8],
+                                      float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = lo[2 * i];
+    y[i] = lo[2 * i + 1];
+    x[4 + i] = hi[2 * i];
+    y[4 + i] = hi[2 * i + 1];
+  }
+}
+__device__ __forceinline__ void zip(const float (&x)[8], const float (&y)[8], float (&lo)[8],
+                                    float (&hi)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[2 * i] = x[i];
+    lo[2 * i + 1] = y[i];
+    hi[2 * i] = x[4 + i];
+    hi[2 * i + 1] = y[4 + i];
+  }
+}
+__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, mx::abs_bits(v[i]));
+  return m;
+}
+
+// F % 32 == 0, p and out 16-byte aligned.  A 32-column block of the checkpoint is
+// four lanes (two when gate and up are interleaved: 16 columns a lane), which
+// agree on its scale with shuffles; a block never straddles rows or halves.
+template <typename T, int FORM>
+__global__ void __launch_bounds__(kThreads)
+    act_checkpoint_vec(const T* __restrict__ p, const int32_t* __restrict__ seg_end, int E, int M,
+                       ActArgs A, T* __restrict__ out, uint8_t* __restrict__ codes,
+                       uint8_t* __restrict__ scales) {
+  pdl_launch();
+  pdl_wait();
+  constexpr bool FAST = sizeof(T) == 2, PAIRS = FORM == kSwigluPairs, ONE = FORM == kPlain;
+  const uint32_t mask = 0xfu << (threadIdx.x & 28);
+  Items w(A.F / 8, live_rows(seg_end, E, M));
+  Raw8<T> r0, r1;
+  auto fetch = [&]() {  // the next item's columns, in flight while this one is converted
+    if (!w.more()) return;
+    const T* src = p + (size_t)w.row * A.N1 + (PAIRS ? 16 : 8) * w.col;
+    r0.load(src);
+    if constexpr (!ONE) r1.load(src + (PAIRS ? 8 : A.F));
+  };
+  fetch();
+  while (w.more()) {
+    float u[8], v[8];
+    r0.get(u);
+    if constexpr (!ONE) r1.get(v);
+    const uint32_t row = w.row, col = w.col;
+    w.next();
+    fetch();
+    // blocks: u and v are one block's (pairs), or u and v of a block each
+    uint32_t mu = amax8(u), mv = ONE ? 0 : amax8(v);
+    if constexpr (PAIRS) mu = max(mu, mv);
+    mu = max(mu, __shfl_xor_sync(mask, mu, 1));
+    if constexpr (!PAIRS) mu = max(mu, __shfl_xor_sync(mask, mu, 2));
+    const uint32_t bu = mx::scale_byte<false>(mu);
+    uint8_t* crow = codes + (size_t)row * A.Np;
+    uint8_t* srow = scales + (size_t)row * (A.Np / 32);
+    float a[8], s[8], dx[8], dy[8];
+    const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if constexpr (PAIRS) {
+      float q[8], t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        q[i] = u[i];
+        t[i] = v[i];
+      }
+      mx::scale8(q, mx::inv_scale(bu));
+      mx::scale8(t, mx::inv_scale(bu));
+      const uint2 lo = mx::e4m3x8(q), hi = mx::e4m3x8(t);
+      *reinterpret_cast<uint4*>(crow + 16 * col) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      if ((threadIdx.x & 1) == 0) srow[col >> 1] = (uint8_t)bu;
+      float x[8], y[8];
+      unzip(u, v, x, y);
+      act8<FORM, FAST>(x, y, zero, A, a, dx, dy);
+    } else {
+      act8<FORM, FAST>(u, v, zero, A, a, dx, dy);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = u[i];
+      mx::scale8(s, mx::inv_scale(bu));
+      *reinterpret_cast<uint2*>(crow + 8 * col) = mx::e4m3x8(s);
+      if ((threadIdx.x & 3) == 0) srow[col >> 2] = (uint8_t)bu;
+      if constexpr (!ONE) {
+        mv = max(mv, __shfl_xor_sync(mask, mv, 1));
+        mv = max(mv, __shfl_xor_sync(mask, mv, 2));
+        const uint32_t bv = mx::scale_byte<false>(mv);
+        mx::scale8(v, mx::inv_scale(bv));
+        *reinterpret_cast<uint2*>(crow + A.F + 8 * col) = mx::e4m3x8(v);
+        if ((threadIdx.x & 3) == 0) srow[(A.F >> 5) + (col >> 2)] = (uint8_t)bv;
+      }
+    }
+    if (out) mx::store8<T, true>(out + (size_t)row * A.F, 8 * col, A.F, a);
+    // the blocks past N1, up to the next multiple of 128 columns
+    for (uint32_t q = col; q < (uint32_t)(A.Np - A.N1) / 8; q += w.ipr) {
+      *reinterpret_cast<uint2*>(crow + A.N1 + 8 * q) = make_uint2(0, 0);
+      if ((q & 3) == 0) srow[(A.N1 >> 5) + (q >> 2)] = 0;
+    }
+  }
+}
+
+__device__ __forceinline__ void e4m3_values(const uint2& c, float scale, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 h = __nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)((j < 2 ? c.x : c.y) >> (16 * (j & 1))), __NV_E4M3);
+    const float2 f = __half22float2(h);
+    v[2 * j] = f.x * scale;
+    v[2 * j + 1] = f.y * scale;
+  }
+}
+
+// F % 8 == 0, p, d_out, d_p and out 16-byte aligned: eight columns, or sixteen
+// interleaved ones, lie in one block of the checkpoint.
+template <typename T, int FORM, bool MX>
+__global__ void __launch_bounds__(kThreads)
+    act_backward_vec(const void* __restrict__ p, const uint8_t* __restrict__ scales,
+                     const T* __restrict__ d_out, const int32_t* __restrict__ seg_end, int E,
+                     int M, ActArgs A, T* __restrict__ d_p, T* __restrict__ out) {
+  pdl_launch();
+  pdl_wait();
+  constexpr bool FAST = sizeof(T) == 2, PAIRS = FORM == kSwigluPairs, ONE = FORM == kPlain;
+  Items w(A.F / 8, live_rows(seg_end, E, M));
+  Raw8<T> rd, r0, r1;      // d_out; p without a checkpoint
+  uint2 c0 = {}, c1 = {};  // codes
+  uint32_t s0 = 0, s1 = 0;
+  auto fetch = [&]() {  // the next item, in flight while this one is computed
+    if (!w.more()) return;
+    rd.load(d_out + (size_t)w.row * A.F + 8 * w.col);
+    const uint32_t at = (PAIRS ? 16 : 8) * w.col;
+    if constexpr (MX) {
+      const uint8_t* src = static_cast<const uint8_t*>(p) + (size_t)w.row * A.Np + at;
+      const uint8_t* sc = scales + (size_t)w.row * (A.Np / 32);
+      s0 = sc[at >> 5];
+      if constexpr (PAIRS) {
+        const uint4 c = __ldcs(reinterpret_cast<const uint4*>(src));
+        c0 = make_uint2(c.x, c.y);
+        c1 = make_uint2(c.z, c.w);
+      } else {
+        c0 = __ldcs(reinterpret_cast<const uint2*>(src));
+        if constexpr (!ONE) {
+          c1 = __ldcs(reinterpret_cast<const uint2*>(src + A.F));
+          s1 = sc[(at + A.F) >> 5];
+        }
+      }
+    } else {
+      const T* src = static_cast<const T*>(p) + (size_t)w.row * A.N1 + at;
+      r0.load(src);
+      if constexpr (!ONE) r1.load(src + (PAIRS ? 8 : A.F));
+    }
+  };
+  fetch();
+  while (w.more()) {
+    float u[8], v[8], d[8], x[8], y[8], a[8];
+    rd.get(d);
+    if constexpr (MX) {
+      e4m3_values(c0, mx::scale_value(s0), u);
+      if constexpr (!ONE) e4m3_values(c1, mx::scale_value(PAIRS ? s0 : s1), v);
+    } else {
+      r0.get(u);
+      if constexpr (!ONE) r1.get(v);
+    }
+    const uint32_t row = w.row, col = w.col;
+    w.next();
+    fetch();
+    T* dst = d_p + (size_t)row * A.N1;
+    float dx[8], dy[8];
+    if constexpr (PAIRS) {
+      unzip(u, v, x, y);
+      act8<FORM, FAST>(x, y, d, A, a, dx, dy);
+      zip(dx, dy, u, v);
+      mx::store8<T, true>(dst, 16 * col, A.N1, u);
+      mx::store8<T, true>(dst, 16 * col + 8, A.N1, v);
+    } else {
+      act8<FORM, FAST>(u, v, d, A, a, dx, dy);
+      mx::store8<T, true>(dst, 8 * col, A.N1, dx);
+      if constexpr (!ONE) mx::store8<T, true>(dst, A.F + 8 * col, A.N1, dy);
+    }
+    if (out) mx::store8<T, true>(out + (size_t)row * A.F, 8 * col, A.F, a);
+  }
+}
+
 ActArgs act_args(const moe_act_params& act, int F) {
   ActArgs A;
   A.kind = act.kind;
@@ -197,9 +453,50 @@ int rows_grid(const void* kernel, int rows) {
   return (int)std::min<long long>(want, (long long)num_sms() * resident_ctas(kernel, kThreads));
 }
 
+// CTAs for the items of M rows, at most a resident round
+int items_grid(const void* kernel, int M, int F) {
+  const long long want = ((long long)M * (F / 8) + kThreads - 1) / kThreads;
+  return (int)std::min<long long>(want, (long long)num_sms() * resident_ctas(kernel, kThreads));
+}
+bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename T, int FORM>
+cudaError_t checkpoint_form(const void* p, const int32_t* seg_end, int E, int M, const ActArgs& A,
+                            void* out, void* codes, void* scales, cudaStream_t s) {
+  const auto kern = act_checkpoint_vec<T, FORM>;
+  return launch_pdl(kern, dim3(items_grid((const void*)kern, M, A.F)), dim3(kThreads), 0, s,
+                    static_cast<const T*>(p), seg_end, E, M, A, static_cast<T*>(out),
+                    static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+}
+template <typename T, int FORM, bool MX>
+cudaError_t backward_form(const void* p, const void* scales, const void* d_out,
+                          const int32_t* seg_end, int E, int M, const ActArgs& A, void* d_p,
+                          void* out, cudaStream_t s) {
+  const auto kern = act_backward_vec<T, FORM, MX>;
+  return launch_pdl(kern, dim3(items_grid((const void*)kern, M, A.F)), dim3(kThreads), 0, s, p,
+                    static_cast<const uint8_t*>(scales), static_cast<const T*>(d_out), seg_end, E,
+                    M, A, static_cast<T*>(d_p), static_cast<T*>(out));
+}
+// f(form) with the form of A as a compile-time constant
+template <typename Fn>
+cudaError_t with_form(const ActArgs& A, Fn f) {
+  if (!A.gated) return f(std::integral_constant<int, kPlain>{});
+  if (A.kind == MOE_ACT_SILU_AND_MUL) return f(std::integral_constant<int, kSilu>{});
+  if (A.kind == MOE_ACT_GELU_AND_MUL) return f(std::integral_constant<int, kGelu>{});
+  if (A.inter) return f(std::integral_constant<int, kSwigluPairs>{});
+  return f(std::integral_constant<int, kSwigluHalves>{});
+}
+
 template <typename T>
 cudaError_t checkpoint_t(const void* p, const int32_t* seg_end, int E, int M, const ActArgs& A,
                          void* out, void* codes, void* scales, cudaStream_t s) {
+  if (A.F % 32 == 0 && a16(p) && a16(out)) {
+    const cudaError_t e = with_form(A, [&](auto form) {
+      return checkpoint_form<T, decltype(form)::value>(p, seg_end, E, M, A, out, codes, scales, s);
+    });
+    count_launch();
+    return e;
+  }
   const auto kern = act_checkpoint_any<T>;
   const cudaError_t e = launch_pdl(kern, dim3(rows_grid((const void*)kern, M)), dim3(kThreads), 0,
                                    s, static_cast<const T*>(p), seg_end, E, M, A,
@@ -212,6 +509,14 @@ template <typename T, bool MX>
 cudaError_t backward_t(const void* p, const void* scales, const void* d_out,
                        const int32_t* seg_end, int E, int M, const ActArgs& A, void* d_p,
                        void* out, cudaStream_t s) {
+  if (A.F % 8 == 0 && a16(p) && a16(d_out) && a16(d_p) && a16(out)) {
+    const cudaError_t e = with_form(A, [&](auto form) {
+      return backward_form<T, decltype(form)::value, MX>(p, scales, d_out, seg_end, E, M, A, d_p,
+                                                         out, s);
+    });
+    count_launch();
+    return e;
+  }
   const auto kern = act_backward_any<T, MX>;
   const cudaError_t e = launch_pdl(kern, dim3(rows_grid((const void*)kern, M)), dim3(kThreads), 0,
                                    s, p, static_cast<const uint8_t*>(scales),
