@@ -1250,13 +1250,14 @@ moe_status moe_grouped_gemm_wgrad(const void* d_out, const void* a, const int32_
   Span outs[] = {{d_w, (size_t)E * N * K * esz}, {d_bias, (size_t)E * N * esz}, {ws, need}};
   Span ins[] = {{d_out, (size_t)M * N * esz}, {a, (size_t)M * K * esz}, {seg_end, (size_t)E * 4}};
   if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
+  if (dtype != MOE_F32 && num_sms() >= 2 && M > 0 && tc_ok(d_out, a, d_w, N, K, M) &&
+      aligned16(d_bias))
+    return cuda_status(launch_gemm_wgrad(d_out, a, seg_end, M, N, K, E, dtype == MOE_F16, d_w,
+                                         d_bias, static_cast<int*>(ws), stream));
   if (d_bias) {
     const cudaError_t e = launch_bias_grad(d_out, seg_end, M, N, E, dtype, d_bias, stream);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
   }
-  if (dtype != MOE_F32 && num_sms() >= 2 && M > 0 && tc_ok(d_out, a, d_w, N, K, M))
-    return cuda_status(launch_gemm_wgrad(d_out, a, seg_end, M, N, K, E, dtype == MOE_F16, d_w,
-                                         static_cast<int*>(ws), stream));
   return cuda_status(launch_wgrad_simt(d_out, a, seg_end, M, N, K, E, dtype, d_w, stream));
 }
 

@@ -159,18 +159,6 @@ __device__ __noinline__ bool wait_cluster(uint64_t* b, uint32_t parity, volatile
   }
   return true;
 }
-// v to the peer's shared memory at addr_cluster, completing on the peer's
-// barrier bar_cluster (4 bytes of transaction, and the one arrival the phase
-// expects): no fence, the barrier's transaction count orders the data.
-__device__ __forceinline__ void publish_remote_u32(uint32_t addr_cluster, uint32_t bar_cluster,
-                                                   int v) {
-  asm volatile(
-      "mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 4;\n\t"
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%1], %2, [%0];" ::"r"(
-          bar_cluster),
-      "r"(addr_cluster), "r"(v)
-      : "memory");
-}
 
 __device__ __forceinline__ void tma2_4d(void* dst, const CUtensorMap* m, uint32_t bar, int c0,
                                         int c1, int c2, int c3) {

@@ -20,12 +20,31 @@
 //
 // Roles (384 threads per CTA)
 //   warp 0 lane 0 : producer
-//   warp 1        : TMEM allocation (pair); lane 0 of the leader issues the MMAs
+//   warp 1        : TMEM allocation (pair); lane 0 of the leader issues the MMAs,
+//                   the peer's hands out the tiles
 //   warp 2        : clears the rows past an expert's end
+//   warp 3        : the bias' gradient, d_bias[e, n] = the sum of d[m, n], beside the
+//                   products: 32 columns of an expert at a time, from global memory
+//                   (a launch of its own for it cost 8 us of 109 at 999 rows, 2880 x
+//                   2880, where d is a hundredth of what is written)
 //   warps 4..11   : epilogue of the CTA's 128 TMEM lanes, 64 columns at a time
-// Tiles go round-robin; an expert without rows gets zeros.  Every wait is bounded
-// (2 s); on a timeout the block latches the timeout bit, drains what it issued and
-// frees TMEM.
+// Tiles are as long as their expert has rows, and SMs write at unequal rates, so a
+// pair takes the next tile from a counter (in the workspace's status area; the
+// launch's last pair resets it): a warp of its own does, a tile ahead of the
+// producers, and sends it to every role of both CTAs through a ring of entries.
+// Against tiles in turn, 32 rows an expert (2880 x 2880, 32 experts) 89 us instead of
+// 102, 256 uneven ones (1536 x 2048, 128 experts) 207 instead of 219, 1024 (7168 x
+// 2048, 64 experts) 1148 instead of 1139; by the producer itself, which held up the
+// copies, 1200.  An expert without rows has no tiles; the epilogue warps write its
+// zeros at the end.  Every wait is bounded (2 s); on a timeout the block latches the
+// timeout bit, drains what it issued and frees TMEM.
+//
+// What bounds it: at 1024 rows an expert a stage takes 600 of the 512 cycles that its
+// MMAs need even without copies and stores, and 700 with them: 32 KB a stage into
+// each SM is most of what L2 delivers.  The ring's depth counts for that reason (4
+// stages 1328 us, 5 stages 1204, 6 stages 1165, uneven experts), more than a second
+// buffer for the stores (with 5 stages: 1223).  At 32 rows an expert writing d_w does
+// (5.9 TB/s).
 #include <cuda.h>
 
 #include <algorithm>
@@ -51,6 +70,18 @@ constexpr int EPI_WARPS = 8, EPI_WARP0 = 4;
 constexpr int NUM_THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
 constexpr int OUT_BYTES_WARP = 32 * 64 * 2;   // 32 rows of 64 columns
 
+// Schedule entries.  Entry j is sent when both producers have taken entry j - AHEAD,
+// and no role is further back than STAGES + 2 tiles from a producer: a stage is
+// loaded again after the MMAs of STAGES stages before, a tile has at least one, and
+// its MMAs wait for the drain of the tile before last.  So an entry is never
+// overwritten unread.
+constexpr int SCHED = 16, AHEAD = 1;
+static_assert(STAGES + 2 + AHEAD < SCHED, "schedule ring");
+// A clearing job holds its stage until it is done, so as many entries as stages,
+// and one for the job that ends the clearing warp.
+constexpr int JOBS = 8;
+static_assert(STAGES < JOBS, "clearing jobs");
+
 struct WgShared {
   uint64_t full[STAGES];   // leader: both CTAs' copies of a stage, or both clearing warps
   uint64_t own[STAGES];    // this CTA's copies of a stage whose rows are cleared
@@ -58,36 +89,60 @@ struct WgShared {
   uint64_t tfull[2];       // both: accumulator ready
   uint64_t tempty[2];      // leader: both CTAs drained the accumulator
   uint64_t drain;
+  uint64_t sfull[SCHED];   // both: schedule entry written
+  uint64_t staken[SCHED];  // peer: both producers have the entry
+  uint64_t jfull[JOBS];    // clearing job written
+  uint4 sched[SCHED];
+  int job[JOBS];           // stage, first row, boxes a byte each; -1 ends
   uint32_t tmem_base;
   int abort;
+  uint32_t live[kMaxExperts / 32];      // experts with rows
+  int live_before[kMaxExperts / 32 + 1];  // of the words before; all
 };
 constexpr size_t kSmemBytes =
     (size_t)STAGES * STAGE_BYTES + EPI_WARPS * OUT_BYTES_WARP + sizeof(WgShared) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-// Tile t: expert e with rows [lo, hi), n0 and k0 its corner, kw its columns (128 or
-// 256); `steps` stages.
+// A tile: expert e with rows [lo, hi), nt and kt its corner in tiles; none for
+// lo == hi.  In the schedule {e, lo, hi, nt << 16 | kt} (the launcher keeps both
+// below 2^16).
 struct WgTile {
-  int e, lo, hi, n0, k0, kw, steps;
+  int e, lo, hi, nt, kt;
+  __device__ __forceinline__ bool none() const { return lo == hi; }
+  __device__ __forceinline__ int steps() const { return (hi - lo + BR - 1) / BR; }
+  __device__ __forceinline__ int n0() const { return nt * TN; }
+  __device__ __forceinline__ int k0() const { return kt * TK; }
+  // columns of a: 128 or 256
+  __device__ __forceinline__ int kw(int K) const { return K - kt * TK > TK / 2 ? TK : TK / 2; }
+  // rows of the last K16 step past the end
+  __device__ __forceinline__ bool has_tail() const { return ((hi - lo) & 15) != 0; }
 };
-__device__ __forceinline__ WgTile wg_decode(int t, const int32_t* __restrict__ seg_end, int M,
-                                            int K, int tn, int tk) {
-  WgTile r;
-  const int per = tn * tk;
-  r.e = t / per;
-  const int in = t - r.e * per;
-  r.n0 = (in / tk) * TN;
-  r.k0 = (in % tk) * TK;
-  r.kw = K - r.k0 > TK / 2 ? TK : TK / 2;
+// Tile t of the list, by a whole warp: the per = tn * tk tiles of the experts with
+// rows follow one another; past the last, none.
+__device__ __forceinline__ WgTile wg_decode(int t, const WgShared* sh,
+                                            const int32_t* __restrict__ seg_end, int M, int per,
+                                            int tk) {
+  const int lane = threadIdx.x & 31;
+  WgTile r = {};
+  const int q = t / per, in = t - q * per;
+  if (q >= sh->live_before[kMaxExperts / 32]) return r;
+  // the word of live experts that holds the q-th, and in it the bit with the rest below
+  const int before = sh->live_before[lane];
+  const uint32_t word = sh->live[lane];
+  const int w = __ffs(__ballot_sync(0xffffffffu, before <= q && q < before + __popc(word))) - 1;
+  const uint32_t bits = __shfl_sync(0xffffffffu, word, w);
+  const int k = q - __shfl_sync(0xffffffffu, before, w);
+  r.e = w * 32 + __ffs(__ballot_sync(0xffffffffu, (bits >> lane & 1u) &&
+                                                      __popc(bits & ((1u << lane) - 1u)) == k)) - 1;
+  r.nt = in / tk;
+  r.kt = in - r.nt * tk;
   seg_bounds(seg_end, r.e, M, 0, r.lo, r.hi);
-  r.steps = (r.hi - r.lo + BR - 1) / BR;
   return r;
 }
-// K16 steps of stage s of a tile, and whether its last one has rows to clear
+// K16 steps of stage s of a tile
 __device__ __forceinline__ int k16_steps(const WgTile& t, int s) {
   return min(4, (t.hi - t.lo - s * BR + 15) >> 4);
 }
-__device__ __forceinline__ bool has_tail(const WgTile& t) { return ((t.hi - t.lo) & 15) != 0; }
 
 // `n16` (1..4) K16 MMAs of a stage and the commit that frees it in both CTAs.
 __device__ __forceinline__ void umma2_rows(uint32_t d_tmem, uint64_t ad, uint64_t bd,
@@ -112,6 +167,45 @@ __device__ __forceinline__ void umma2_rows(uint32_t d_tmem, uint64_t ad, uint64_
       "h"((uint16_t)3)
       : "memory");
 }
+// Sums of 32 columns n0 .. of d over the rows [lo, hi), by one warp: four lanes
+// read 64 bytes of a row, eight rows at once, eight such loads in flight.
+template <bool F16>
+__device__ __forceinline__ void bias_columns(const __nv_bfloat16* __restrict__ d, int lo, int hi,
+                                             int N, int n0, __nv_bfloat16* __restrict__ out) {
+  const int lane = threadIdx.x & 31, n = n0 + 8 * (lane & 3);
+  float sum[8] = {};
+  if (n < N) {  // N is a multiple of 8
+    for (int m = lo + (lane >> 2); m < hi; m += 64) {
+      uint4 q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        q[i] = m + 8 * i < hi
+                   ? __ldg(reinterpret_cast<const uint4*>(d + (size_t)(m + 8 * i) * N + n))
+                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[2 * j] += lo16<F16>(u[j]);
+          sum[2 * j + 1] += hi16<F16>(u[j]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+  if (lane < 4 && n < N) {
+    uint4 u;
+    u.x = pack2<F16>(sum[0], sum[1]);
+    u.y = pack2<F16>(sum[2], sum[3]);
+    u.z = pack2<F16>(sum[4], sum[5]);
+    u.w = pack2<F16>(sum[6], sum[7]);
+    *reinterpret_cast<uint4*>(out + n) = u;
+  }
+}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int c0, int c1,
                                              int c2) {
   asm volatile(
@@ -128,8 +222,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_wgrad_kernel(const __grid_constant__ CUtensorMap tm_d,
                       const __grid_constant__ CUtensorMap tm_a,
                       const __grid_constant__ CUtensorMap tm_out,
-                      const int32_t* __restrict__ seg_end, int M, int N, int K, int total, int tn,
-                      int tk, int* status) {
+                      const int32_t* __restrict__ seg_end, int M, int N, int K, int E, int tn,
+                      int tk, const __nv_bfloat16* __restrict__ d,
+                      __nv_bfloat16* __restrict__ d_bias, int* status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -148,9 +243,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&sh->tfull[a], 1);
-      mbar_init(&sh->tempty[a], 2 * 32 * EPI_WARPS);
+      mbar_init(&sh->tempty[a], 2 * EPI_WARPS);
     }
     mbar_init(&sh->drain, 1);
+    for (int i = 0; i < SCHED; ++i) {
+      mbar_init(&sh->sfull[i], 1);
+      mbar_init(&sh->staken[i], 2);
+    }
+    for (int i = 0; i < JOBS; ++i) mbar_init(&sh->jfull[i], 1);
     sh->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -169,12 +269,48 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // everything above overlaps the previous launch; seg_end and the operands are
   // read only after this
   pdl_wait();
+  for (int w = warp; w < kMaxExperts / 32; w += NUM_THREADS / 32) {
+    const int e = w * 32 + lane;
+    int lo = 0, hi = 0;
+    if (e < E) seg_bounds(seg_end, e, M, 0, lo, hi);
+    const uint32_t live = __ballot_sync(0xffffffffu, hi > lo);
+    if (lane == 0) sh->live[w] = live;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    static_assert(kMaxExperts / 32 == 32, "a word a lane");
+    const int n = __popc(sh->live[lane]);
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    sh->live_before[lane] = sum - n;
+    if (lane == 31) sh->live_before[32] = sum;
+  }
   tc_fence_before();
+  __syncthreads();
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated
   tc_fence_after();
   const uint32_t tmem_base = sh->tmem_base;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  auto decode = [&](int t) { return wg_decode(t, seg_end, M, K, tn, tk); };
+  const int per = tn * tk;
+  int* gctr = status + 8;  // tiles taken from the counter, pairs done
+  // tile j of the schedule (none at its end, or when the wait failed)
+  auto next_tile = [&](int j) -> WgTile {
+    WgTile r = {};
+    if (!wait_fast<kWaitShared>(&sh->sfull[j % SCHED], (uint32_t)(j / SCHED) & 1u, abort_flag, status)) return r;
+    const uint32_t addr = su32(&sh->sched[j % SCHED]);
+    uint32_t corner;
+    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.e), "=r"(r.lo), "=r"(r.hi), "=r"(corner)
+                 : "r"(addr)
+                 : "memory");
+    r.nt = (int)(corner >> 16);
+    r.kt = (int)(corner & 0xffffu);
+    return r;
+  };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -182,27 +318,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, own_used = 0, own_phase = 0, last_own = 0, used = 0, used_phase = 0;
       bool ok = true;
-      WgTile nx{};
-      if (pair < total) nx = decode(pair);
-      for (int t = pair; t < total && ok; t += npairs) {
-        const WgTile st = nx;  // the next tile's bounds arrive during this one
-        if (t + npairs < total) nx = decode(t + npairs);
-        const int half = st.kw >> 1;
-        const int nb = half / 64;
+      int jobs = 0;
+      const uint32_t staken0 = map_to_rank(su32(&sh->staken[0]), 1);
+      // (the arrival paces the schedule and orders nothing)
+      auto take = [&](int j) -> WgTile {
+        const WgTile t = next_tile(j);
+        mbar_arrive_cluster_tmem(staken0 + (uint32_t)(j % SCHED * sizeof(uint64_t)));
+        return t;
+      };
+      WgTile st = take(0), nx{};
+      for (int j = 0; ok && !st.none(); ++j) {
+        const int steps = st.steps(), half = st.kw(K) >> 1, nb = half / 64;
         const uint32_t tx = (uint32_t)(A_BYTES + nb * BOX_BYTES);
-        const int nc = st.n0 + 128 * (int)rank, kc = st.k0 + half * (int)rank;
-        for (int s = 0; s < st.steps; ++s) {
+        const int nc = st.n0() + 128 * (int)rank, kc = st.k0() + half * (int)rank;
+        for (int s = 0; s < steps; ++s) {
           if (!wait_pair(&sh->empty[stage], phase ^ 1u, abort_flag, status)) { ok = false; break; }
           uint8_t* a_dst = smem + (size_t)stage * STAGE_BYTES;
           uint8_t* b_dst = a_dst + A_BYTES;
           uint32_t bar;
           const uint32_t bit = 1u << stage;
-          if (s == st.steps - 1 && has_tail(st)) {
+          if (s == steps - 1 && st.has_tail()) {
             mbar_expect_tx(&sh->own[stage], tx);
             bar = map_to_rank(su32(&sh->own[stage]), rank);
             own_phase = (own_used & bit) ? own_phase ^ bit : own_phase & ~bit;
             own_used |= bit;
             last_own |= bit;
+            *reinterpret_cast<volatile int*>(&sh->job[jobs % JOBS]) =
+                stage | (st.hi - st.lo - s * BR) << 8 | (2 + nb) << 16;
+            mbar_arrive(&sh->jfull[jobs % JOBS]);
+            ++jobs;
           } else {
             if (leader) {
               mbar_expect_tx(&sh->full[stage], 2 * tx);
@@ -219,8 +363,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tma2_2d(b_dst, &tm_a, bar, kc, r0);
           if (nb == 2) tma2_2d(b_dst + BOX_BYTES, &tm_a, bar, kc + 64, r0);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (s == 0) nx = take(j + 1);
         }
+        st = nx;
       }
+      // no more jobs
+      *reinterpret_cast<volatile int*>(&sh->job[jobs % JOBS]) = -1;
+      mbar_arrive(&sh->jfull[jobs % JOBS]);
       if (!ok) {  // what is in flight lands before the block exits
         for (int s = 0; s < STAGES; ++s) {
           if (!((used >> s) & 1u)) continue;
@@ -237,66 +386,110 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true, any = false;
       const uint64_t adesc0 = sw128_mn_desc(su32(smem), BOX_BYTES);
       const uint64_t bdesc0 = sw128_mn_desc(su32(smem + A_BYTES), BOX_BYTES);
-      WgTile nx{};
-      if (pair < total) nx = decode(pair);
-      for (int t = pair; t < total && ok; t += npairs) {
-        const WgTile st = nx;
-        if (t + npairs < total) nx = decode(t + npairs);
-        if (st.steps == 0) continue;
-        const uint32_t idesc = idesc_sw(TN, st.kw, F16 ? 1 : 0, true, true);
+      WgTile st = next_tile(0), nx{};
+      for (int j = 0; ok && !st.none(); ++j) {
+        const int steps = st.steps();
+        const uint32_t idesc = idesc_sw(TN, st.kw(K), F16 ? 1 : 0, true, true);
         if (!wait_pair_tmem(&sh->tempty[acc], aphase ^ 1u, abort_flag, status)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * TK);
-        for (int s = 0; s < st.steps; ++s) {
-          if (!wait_pair(&sh->full[stage], phase, abort_flag, status)) { ok = false; break; }
-          // a clearing warp wrote through the generic proxy, the MMA reads
-          // through the async proxy
-          if (s == st.steps - 1) fence_proxy_async_smem();
+        for (int s = 0; s < steps; ++s) {
+          // copies alone complete a stage at this CTA's scope; after the clearing
+          // warps (which order their writes for the async proxy themselves) the
+          // peer's shared memory is acquired
+          if (!(s == steps - 1 && st.has_tail()
+                    ? wait_pair<true>(&sh->full[stage], phase, abort_flag, status)
+                    : wait_pair<false>(&sh->full[stage], phase, abort_flag, status))) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
           const uint64_t off = (uint64_t)((stage * STAGE_BYTES) >> 4);
           umma2_rows(d_tmem, adesc0 + off, bdesc0 + off, idesc, s != 0 ? 1u : 0u,
                      k16_steps(st, s), su32(&sh->empty[stage]));
           any = true;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (s == 0) nx = next_tile(j + 1);  // while the MMAs run
         }
         if (!ok) break;
         umma2_commit_both(&sh->tfull[acc]);
         if (++acc == 2) { acc = 0; aphase ^= 1u; }
+        st = nx;
       }
       if (!ok && any) {
         umma2_commit_self(&sh->drain);
         drain_wait(&sh->drain, 0);
       }
     }
+    if (!leader) {
+      // ---------------------------------------------- schedule (peer, whole warp)
+      int t = pair, grabbed = 0;  // the first tile is the pair's own
+      bool ok = true;
+      for (int j = 0;; ++j) {
+        const WgTile st = wg_decode(t, sh, seg_end, M, per, tk);
+        if (!st.none() && lane == 0) grabbed = npairs + atomicAdd(gctr, 1);
+        if (j >= AHEAD) {
+          const int i = j - AHEAD;
+          ok = wait_fast(&sh->staken[i % SCHED], (uint32_t)(i / SCHED) & 1u, abort_flag, status);
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        if (lane < 2)
+          publish_remote_v4(map_to_rank(su32(&sh->sched[j % SCHED]), lane),
+                            map_to_rank(su32(&sh->sfull[j % SCHED]), lane), (uint32_t)st.e,
+                            (uint32_t)st.lo, (uint32_t)st.hi, (uint32_t)(st.nt << 16 | st.kt));
+        if (st.none()) break;
+        t = __shfl_sync(0xffffffffu, grabbed, 0);
+      }
+      if (lane == 0 && !*abort_flag) {
+        __threadfence();  // this pair's last take before its done count
+        if (atomicAdd(gctr + 1, 1) == npairs - 1) {
+          __threadfence();  // every pair's takes before the reset
+          atomicExch(gctr, 0);
+          atomicExch(gctr + 1, 0);
+        }
+      }
+    }
   } else if (warp == 2) {
     // ------------------------------------------------ clearing (both CTAs)
-    int stage = 0;
     uint32_t own_phase = 0;  // bit s: parity of own[s]'s next phase
     const uint32_t full_remote0 = map_to_rank(su32(&sh->full[0]), 0);
-    WgTile nx{};
-    if (pair < total) nx = decode(pair);
-    for (int t = pair; t < total; t += npairs) {
-      const WgTile st = nx;
-      if (t + npairs < total) nx = decode(t + npairs);
-      if (st.steps == 0) continue;
-      const int last = (stage + st.steps - 1) % STAGES;
-      stage = (stage + st.steps) % STAGES;
-      if (!has_tail(st)) continue;
-      if (!wait_fast(&sh->own[last], (own_phase >> last) & 1u, abort_flag, status)) break;
-      own_phase ^= 1u << last;
+    for (int i = 0;; ++i) {
+      // there may be no job for as long as the launch takes; the producer, whose own
+      // waits are bounded, always sends the last one
+      bool ok = false;
+      for (int k = 0; k < 32 && !ok; ++k) {
+        drain_wait(&sh->jfull[i % JOBS], (uint32_t)(i / JOBS) & 1u);
+        ok = mbar_try_wait(su32(&sh->jfull[i % JOBS]), (uint32_t)(i / JOBS) & 1u);
+      }
+      const int job = *reinterpret_cast<volatile int*>(&sh->job[i % JOBS]);
+      // the lanes go on, or give up, together
+      if (!__all_sync(0xffffffffu, ok) || job < 0) break;
+      const int stage = job & 255, r0 = job >> 8 & 255, r1 = (r0 + 15) & ~15, boxes = job >> 16;
+      ok = wait_fast(&sh->own[stage], (own_phase >> stage) & 1u, abort_flag, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      own_phase ^= 1u << stage;
       // rows r0 .. r1 - 1 of every box, whole 128-byte rows (the swizzle stays
       // inside a row)
-      const int r0 = (st.hi - st.lo) - (st.steps - 1) * BR, r1 = (r0 + 15) & ~15;
-      const int boxes = 2 + st.kw / 128;
-      uint8_t* base = smem + (size_t)last * STAGE_BYTES;
+      uint8_t* base = smem + (size_t)stage * STAGE_BYTES;
       for (int b = 0; b < boxes; ++b)
         for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
           *reinterpret_cast<uint4*>(base + b * BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(full_remote0 + (uint32_t)(last * sizeof(uint64_t)));
+      if (lane == 0) mbar_arrive_cluster(full_remote0 + (uint32_t)(stage * sizeof(uint64_t)));
     }
-  } else if (warp >= EPI_WARP0) {
+  } else if (warp == 3) {
+    // ------------------------------------------------ bias (both CTAs)
+    if (d_bias) {
+      const int per = (N + 31) / 32;
+      for (int u = blockIdx.x; u < E * per; u += gridDim.x) {
+        const int e = u / per;
+        int lo, hi;
+        seg_bounds(seg_end, e, M, 0, lo, hi);
+        bias_columns<F16>(d, lo, hi, N, (u - e * per) * 32, d_bias + (size_t)e * N);
+      }
+    }
+  } else {
     // ------------------------------------------------ epilogue (both CTAs)
     const int quad = warp & 3, grp = (warp - EPI_WARP0) >> 2;
     int acc = 0;
@@ -304,30 +497,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t tempty_remote[2] = {map_to_rank(su32(&sh->tempty[0]), 0),
                                        map_to_rank(su32(&sh->tempty[1]), 0)};
     uint8_t* buf = out_stage + (warp - EPI_WARP0) * OUT_BYTES_WARP;
-    WgTile nx{};
-    if (pair < total) nx = decode(pair);
-    for (int t = pair; t < total; t += npairs) {
-      const WgTile st = nx;
-      if (t + npairs < total) nx = decode(t + npairs);
-      const bool zero = st.steps == 0;
-      if (!zero) {
-        if (!wait_pair_tmem(&sh->tfull[acc], aphase, abort_flag, status)) break;
-        tc_fence_after();
+    // 32 rows of 64 columns from the warp's buffer
+    auto store = [&](const WgTile& st, int c, int n) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d(&tm_out, buf, st.k0() + c, n, st.e);
+        bulk_commit();
       }
-      const int n = st.n0 + 128 * (int)rank + 32 * quad;
+    };
+    for (int j = 0;; ++j) {
+      const WgTile st = next_tile(j);
+      // the lanes go on, or give up, together
+      if (__any_sync(0xffffffffu, st.none())) break;
+      if (!__all_sync(0xffffffffu, wait_pair_tmem(&sh->tfull[acc], aphase, abort_flag, status)))
+        break;
+      tc_fence_after();
+      const int n = st.n0() + 128 * (int)rank + 32 * quad;
       const uint32_t tb = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * TK);
 #pragma unroll 1
-      for (int c = 64 * grp; c < st.kw; c += 128) {
-        if (n >= N || st.k0 + c >= K) break;  // warp-uniform
+      for (int c = 64 * grp; c < st.kw(K); c += 128) {
+        if (n >= N || st.k0() + c >= K) break;  // warp-uniform
         uint32_t r[2][32];
-        if (!zero) {
-          tmem_ld32(tb + (uint32_t)c, r[0]);
-          tmem_ld32(tb + (uint32_t)c + 32, r[1]);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[0][i] = r[1][i] = 0;
-        }
+        tmem_ld32(tb + (uint32_t)c, r[0]);
+        tmem_ld32(tb + (uint32_t)c + 32, r[1]);
+        tmem_wait_ld();
         if (lane == 0) bulk_wait_read<0>();  // the last store from this buffer
         __syncwarp();
         // row `lane` of the box, 16-byte chunk q at q ^ (lane & 7)
@@ -341,18 +535,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           u.w = pack2<F16>(__uint_as_float(v[6]), __uint_as_float(v[7]));
           *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) = u;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tm_out, buf, st.k0 + c, n, st.e);
-          bulk_commit();
-        }
+        store(st, c, n);
       }
-      if (!zero) {
-        tc_fence_before();
-        mbar_arrive_cluster_tmem(tempty_remote[acc]);
-        if (++acc == 2) { acc = 0; aphase ^= 1u; }
+      // one arrival a warp: those of all 512 threads took their time one by one
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_tmem(tempty_remote[acc]);
+      if (++acc == 2) { acc = 0; aphase ^= 1u; }
+    }
+    // the experts without rows: tile `in` of the i-th of them is pair
+    // (i * per + in) % npairs's
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+    for (int i = lane; i < OUT_BYTES_WARP / 16; i += 32)
+      reinterpret_cast<uint4*>(buf)[i] = make_uint4(0, 0, 0, 0);
+    long long before = 0;  // tiles of the empty experts before e
+    for (int e = 0; e < E; ++e) {
+      if ((sh->live[e >> 5] >> (e & 31)) & 1u) continue;
+      WgTile st = {e, 0, 0, 0, 0};
+      for (int in = (int)((npairs + pair - before % npairs) % npairs); in < per; in += npairs) {
+        st.nt = in / tk;
+        st.kt = in - st.nt * tk;
+        const int n = st.n0() + 128 * (int)rank + 32 * quad;
+        for (int c = 64 * grp; c < st.kw(K); c += 128)
+          if (n < N && st.k0() + c < K) store(st, c, n);
       }
+      before += per;
     }
     if (lane == 0) bulk_wait_all();  // every staged box written before the pair exits
   }
@@ -371,7 +579,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }  // namespace
 
 cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_end, int M, int N,
-                              int K, int E, bool f16, void* d_w, int* status, cudaStream_t s) {
+                              int K, int E, bool f16, void* d_w, void* d_bias, int* status,
+                              cudaStream_t s) {
   if (N % 8 != 0 || K % 8 != 0) return cudaErrorInvalidValue;
   CUtensorMap md, ma, mo;
   auto rows = [&](CUtensorMap* m, const void* p, int cols) {
@@ -387,8 +596,8 @@ cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_e
       !tmap::encode_bf16(&mo, d_w, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, f16))
     return cudaErrorInvalidValue;
   int tn = (N + TN - 1) / TN, tk = (K + TK - 1) / TK;
-  int total = E * tn * tk;
-  const int pairs = std::max(1, std::min(total, num_sms() / 2));
+  if (tn > 0xffff || tk > 0xffff) return cudaErrorInvalidValue;
+  const int pairs = std::max(1, std::min(E * tn * tk, num_sms() / 2));
   const void* kern = f16 ? (const void*)gemm_wgrad_kernel<true> : (const void*)gemm_wgrad_kernel<false>;
   cudaError_t e = set_smem_limit(kern, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -406,7 +615,9 @@ cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_e
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  void* args[] = {&md, &ma, &mo, &seg_end, &M, &N, &K, &total, &tn, &tk, &status};
+  const __nv_bfloat16* d_p = static_cast<const __nv_bfloat16*>(d);
+  __nv_bfloat16* bias_p = static_cast<__nv_bfloat16*>(d_bias);
+  void* args[] = {&md, &ma, &mo, &seg_end, &M, &N, &K, &E, &tn, &tk, &d_p, &bias_p, &status};
   e = cudaLaunchKernelExC(&cfg, kern, args);
   count_launch();
   return e;

@@ -13,7 +13,7 @@
 // gradient.  One warp a token; bound by writing the [T, E] gradients.
 #include <algorithm>
 
-#include "common.cuh"
+#include "mx_dev.cuh"
 
 namespace moe {
 namespace {
@@ -49,41 +49,56 @@ __device__ __forceinline__ void score_of(int scoring, float z, float& s, float& 
   }
 }
 
-// Lane j holds the routes j and j + 32 of the token (K <= 64).
+// The calling warp writes zeros over a row of the gradients.
+__device__ __forceinline__ void zero_row(void* row, int bytes) {
+  const int lane = threadIdx.x & 31;
+  if (((reinterpret_cast<uintptr_t>(row) | (uintptr_t)bytes) & 15) == 0) {
+    for (int i = lane; i < bytes / 16; i += 32) static_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+  } else {
+    for (int i = lane; i < bytes / 2; i += 32) static_cast<uint16_t*>(row)[i] = 0;
+  }
+}
+
+// Sum of x over the routes with the calling lane's id, in order (an id may come
+// twice): lane j holds the routes j and j + 32 of the token (K <= 64).
+__device__ __forceinline__ void same_id_sums(const int (&id)[2], const float (&x)[2], int K,
+                                             float (&sum)[2]) {
+  sum[0] = sum[1] = 0.f;
+  for (int k = 0; k < K; ++k) {
+    const int other = __shfl_sync(0xffffffffu, k < 32 ? id[0] : id[1], k & 31);
+    const float v = __shfl_sync(0xffffffffu, k < 32 ? x[0] : x[1], k & 31);
+    if (other == id[0]) sum[0] += v;
+    if (other == id[1]) sum[1] += v;
+  }
+}
+
+// The gradient is zero but at the chosen experts: all but a softmax whose weights
+// are as they are.  The zeros are written while the loads are under way.
 __global__ void __launch_bounds__(kThreads)
-    route_backward_kernel(const void* __restrict__ logits, const int32_t* __restrict__ ids,
+    route_backward_chosen(const void* __restrict__ logits, const int32_t* __restrict__ ids,
                           const float* __restrict__ d_w, int T, int E, int K, int scoring,
                           int renorm, float rsf, int dt, void* __restrict__ d_logits) {
+  pdl_launch();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, size = dt == MOE_F32 ? 4 : 2;
   const int warps = gridDim.x * (kThreads / 32);
-  const bool dense = scoring == MOE_SCORING_SOFTMAX && !renorm;
   for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < T; t += warps) {
     const size_t row = (size_t)t * E;
     int id[2];
-    float z[2], g[2], s[2], l[2];
+    float z[2], g[2], s[2] = {}, l[2] = {};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int k = lane + 32 * q;
       id[q] = k < K ? ids[(size_t)t * K + k] : -1;
-      if (id[q] >= E) id[q] = -1;  // an id outside [0, E) takes no part
-      const bool in = id[q] >= 0;
-      g[q] = in ? d_w[(size_t)t * K + k] : 0.f;
-      z[q] = in ? load_any(logits, row + id[q], dt) : -INFINITY;
-      s[q] = l[q] = 0.f;
+      g[q] = k < K ? d_w[(size_t)t * K + k] : 0.f;
     }
-    // scores (softmax: of the chosen experts, or with the whole row's sum)
-    float m = 0.f, sum = 0.f;
-    if (scoring == MOE_SCORING_SOFTMAX) {
-      m = fmaxf(z[0], z[1]);
-      if (dense)
-        for (int e = lane; e < E; e += 32) m = fmaxf(m, load_any(logits, row + e, dt));
-      m = warp_max(m);
-      if (dense) {
-        for (int e = lane; e < E; e += 32) sum += expf(load_any(logits, row + e, dt) - m);
-        sum = warp_sum(sum);
-      }
+    zero_row(static_cast<char*>(d_logits) + row * size, E * size);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (id[q] < 0 || id[q] >= E) id[q] = -1, g[q] = 0.f;  // no expert: takes no part
+      z[q] = id[q] >= 0 ? load_any(logits, row + id[q], dt) : -INFINITY;
     }
+    const float m = scoring == MOE_SCORING_SOFTMAX ? warp_max(fmaxf(z[0], z[1])) : 0.f;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (id[q] < 0) continue;
@@ -94,40 +109,81 @@ __global__ void __launch_bounds__(kThreads)
         score_of(scoring, z[q], s[q], l[q]);
       }
     }
-    if (!dense) sum = renorm ? warp_sum(s[0] + s[1]) : 1.f;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) s[q] = id[q] >= 0 ? s[q] / sum : 0.f;
     float mean = 0.f;  // sum_k g_k v_k
-    if (renorm || dense) {
-      mean = (id[0] >= 0 ? g[0] * s[0] : 0.f) + (id[1] >= 0 ? g[1] * s[1] : 0.f);
-      mean = warp_sum(mean);
-    }
-    // a chosen expert's value; the same id twice adds up
-    float v[2];
-    if (dense) {
-      v[0] = g[0];
-      v[1] = g[1];
-    } else {
+    if (renorm) {
+      const float sum = warp_sum(s[0] + s[1]);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) v[q] = id[q] >= 0 ? rsf * s[q] * l[q] * (g[q] - mean) : 0.f;
+      for (int q = 0; q < 2; ++q) s[q] = id[q] >= 0 ? s[q] / sum : 0.f;
+      mean = warp_sum(g[0] * s[0] + g[1] * s[1]);
     }
-    float add[2] = {0.f, 0.f};
-    for (int k = 0; k < K; ++k) {
-      const int q = k >> 5;
-      const int other = __shfl_sync(0xffffffffu, q ? id[1] : id[0], k & 31);
-      const float x = __shfl_sync(0xffffffffu, q ? v[1] : v[0], k & 31);
-      if (other == id[0]) add[0] += x;
-      if (other == id[1]) add[1] += x;
-    }
-    for (int e = lane; e < E; e += 32) {
-      const float o = dense ? rsf * (expf(load_any(logits, row + e, dt) - m) / sum) * -mean : 0.f;
-      store_any(d_logits, row + e, dt, o);
-    }
-    __syncwarp();  // the row's own values over the others
+    float x[2], v[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) x[q] = id[q] >= 0 ? rsf * s[q] * l[q] * (g[q] - mean) : 0.f;
+    same_id_sums(id, x, K, v);
+    __syncwarp();  // the chosen experts' values over the zeros
 #pragma unroll
     for (int q = 0; q < 2; ++q)
-      if (id[q] >= 0)
-        store_any(d_logits, row + id[q], dt, dense ? rsf * s[q] * (add[q] - mean) : add[q]);
+      if (id[q] >= 0) store_any(d_logits, row + id[q], dt, v[q]);
+  }
+}
+
+// Softmax, weights as they are: every expert has a part in the softmax's sum.
+// Expert lane + 32 i is in register i (E <= 32 NPL).
+template <int NPL>
+__global__ void __launch_bounds__(kThreads)
+    route_backward_softmax(const void* __restrict__ logits, const int32_t* __restrict__ ids,
+                           const float* __restrict__ d_w, int T, int E, int K, float rsf, int dt,
+                           void* __restrict__ d_logits) {
+  pdl_launch();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * (kThreads / 32);
+  for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < T; t += warps) {
+    const size_t row = (size_t)t * E;
+    int id[2];
+    float g[2], z[NPL];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int k = lane + 32 * q;
+      id[q] = k < K ? ids[(size_t)t * K + k] : -1;
+      g[q] = k < K ? d_w[(size_t)t * K + k] : 0.f;
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int e = lane + 32 * i;
+      z[i] = e < E ? load_any(logits, row + e, dt) : -INFINITY;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (id[q] < 0 || id[q] >= E) id[q] = -1, g[q] = 0.f;  // no expert: takes no part
+    // the chosen experts' logits again, now from the L1 cache
+    float s[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) s[q] = id[q] >= 0 ? load_any(logits, row + id[q], dt) : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) m = fmaxf(m, z[i]);
+    m = warp_max(m);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      z[i] = lane + 32 * i < E ? expf(z[i] - m) : 0.f;
+      sum += z[i];
+    }
+    sum = warp_sum(sum);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) s[q] = id[q] >= 0 ? expf(s[q] - m) / sum : 0.f;
+    const float mean = warp_sum(g[0] * s[0] + g[1] * s[1]);  // sum_k g_k s_k
+    float v[2];
+    same_id_sums(id, g, K, v);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (lane + 32 * i < E)
+        store_any(d_logits, row + lane + 32 * i, dt, rsf * (z[i] / sum) * -mean);
+    __syncwarp();  // the chosen experts' values over the others'
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (id[q] >= 0) store_any(d_logits, row + id[q], dt, rsf * s[q] * (v[q] - mean));
   }
 }
 
@@ -138,12 +194,23 @@ cudaError_t launch_route_backward(const void* logits, const int32_t* ids, const 
                                   cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   const long long want = ((long long)T + kThreads / 32 - 1) / (kThreads / 32);
-  const long long cap =
-      (long long)num_sms() * resident_ctas((const void*)route_backward_kernel, kThreads);
-  const cudaError_t e = launch_pdl(route_backward_kernel, dim3((unsigned)std::min(want, cap)),
-                                   dim3(kThreads), 0, s, logits, ids, d_w, T, E, (int)p.top_k,
-                                   (int)p.scoring, (int)(p.renormalize != 0),
-                                   p.routed_scaling_factor, (int)p.dtype, d_logits);
+  auto grid = [&](const void* kern) {
+    return dim3((unsigned)std::min(want, (long long)num_sms() * resident_ctas(kern, kThreads)));
+  };
+  cudaError_t e;
+  if (p.scoring == MOE_SCORING_SOFTMAX && !p.renormalize) {
+    auto go = [&](auto kern) {
+      return launch_pdl(kern, grid((const void*)kern), dim3(kThreads), 0, s, logits, ids, d_w, T, E,
+                        (int)p.top_k, p.routed_scaling_factor, (int)p.dtype, d_logits);
+    };
+    e = E <= 128   ? go(route_backward_softmax<4>)
+        : E <= 512 ? go(route_backward_softmax<16>)
+                   : go(route_backward_softmax<32>);
+  } else {
+    e = launch_pdl(route_backward_chosen, grid((const void*)route_backward_chosen), dim3(kThreads),
+                   0, s, logits, ids, d_w, T, E, (int)p.top_k, (int)p.scoring,
+                   (int)(p.renormalize != 0), p.routed_scaling_factor, (int)p.dtype, d_logits);
+  }
   count_launch();
   return e;
 }

@@ -210,6 +210,30 @@ __device__ __forceinline__ void umma2_commit_self(uint64_t* bar) {
       : "memory");
 }
 
+// v to the peer's shared memory at addr_cluster, completing on the peer's
+// barrier bar_cluster (4 bytes of transaction, and the one arrival the phase
+// expects): no fence, the barrier's transaction count orders the data.
+__device__ __forceinline__ void publish_remote_u32(uint32_t addr_cluster, uint32_t bar_cluster,
+                                                   int v) {
+  asm volatile(
+      "mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 4;\n\t"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%1], %2, [%0];" ::"r"(
+          bar_cluster),
+      "r"(addr_cluster), "r"(v)
+      : "memory");
+}
+
+// Four words likewise, 16 bytes of transaction; addr_cluster may be this CTA's own.
+__device__ __forceinline__ void publish_remote_v4(uint32_t addr_cluster, uint32_t bar_cluster,
+                                                  uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile(
+      "mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], 16;\n\t"
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%1], {%2, %3, %4, %5}, [%0];" ::
+          "r"(bar_cluster),
+      "r"(addr_cluster), "r"(a), "r"(b), "r"(c), "r"(d)
+      : "memory");
+}
+
 // TMA store of one box from shared memory (bulk async-group completion).
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(

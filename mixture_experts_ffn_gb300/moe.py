@@ -225,11 +225,13 @@ def _is_current(device) -> bool:
 
 def _together(first, *ts):
     """first and those of ts that are given: contiguous CUDA tensors of the current device."""
-    _cuda(first, *ts)
+    _on_gpu(first)
     dev = first.device
+    if not first.is_contiguous():
+        raise ValueError("libmoe takes contiguous tensors only")
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError("the tensors of a call are on one device")
+        if t is not None and not (t.is_contiguous() and t.device == dev):
+            raise ValueError("the tensors of a call are contiguous and on one CUDA device")
     if not _is_current(dev):
         raise ValueError("the tensors of a call are on the current device")
 
