@@ -4,10 +4,11 @@
 //   d_a[m, k] = sum_n d[m, n] w_e[n, k]           (m in expert e's segment)
 //   d_w_e[n, k] = sum_{m in e} d[m, n] a[m, k],   d_b_e[n] = sum_{m in e} d[m, n]
 // Both are C = X Y with Y read along its rows; X is read along its rows for d_a
-// and along its columns for d_w.  Tile 64 x 128 outputs, 16 terms of the sum a
-// step, 4 x 8 outputs a thread; the next step's operands are in registers while
-// a step is summed.  Bound by the float32 pipes (and, for d_w of few rows, by
-// writing d_w).
+// and along its columns for d_w.  256 threads a tile; the next step's operands are
+// in registers while a step is summed.  Bound by the float32 pipes where tiles are
+// many (38 TFLOP/s at 1024 rows an expert, 2048 x 2048, half the pipes' rate; the
+// library's product 52), by the latency of a tile's steps where they are few, hence
+// two tiles (pick_tile).
 #include <algorithm>
 
 #include "common.cuh"
@@ -15,113 +16,134 @@
 namespace moe {
 namespace {
 
-constexpr int GM = 64, GN = 128, GK = 16;
 constexpr int kThreads = 256;
+
+// BM x BN outputs, BM / 16 x BN / 16 of them a thread, BK terms of the sum a step.
+template <int BM_, int BN_, int BK_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, BK = BK_, TM = BM / 16, TN = BN / 16;
+  static constexpr int XR = BM * BK / kThreads, YR = BN * BK / kThreads;
+  struct Shared {
+    float x[BK][BM + 4], y[BK][BN + 4];
+  };
+};
+// T consecutive values (T = 2, 4), or two runs of four half a tile apart (T = 8)
+template <int T, int B>
+__device__ __forceinline__ void take(const float* row, int t, float (&v)[T]) {
+  if constexpr (T == 2) {
+    const float2 a = *reinterpret_cast<const float2*>(row + 2 * t);
+    v[0] = a.x; v[1] = a.y;
+  } else {
+#pragma unroll
+    for (int h = 0; h < T / 4; ++h) {
+      const float4 a = *reinterpret_cast<const float4*>(row + h * (B / 2) + 4 * t);
+      v[4 * h] = a.x; v[4 * h + 1] = a.y; v[4 * h + 2] = a.z; v[4 * h + 3] = a.w;
+    }
+  }
+}
+template <int T, int B>
+__device__ __forceinline__ int place(int t, int i) {
+  return T == 2 ? 2 * t + i : 4 * t + (i & 3) + (i >> 2) * (B / 2);
+}
 
 // X(i, q): output row i, term q.  Row i of the tile, i < mi valid, and terms
 // q < nq: element i * ldx + q (d_a) or q * ldx + i (d_w) of x.
-template <typename T, bool WGRAD>
+template <typename T, bool WGRAD, class G>
 __device__ __forceinline__ void grad_tile(const T* __restrict__ x, size_t ldx, int mi,
                                           const T* __restrict__ y, size_t ldy, int nj, int nq,
-                                          T* __restrict__ c, size_t ldc,
-                                          float (&Xs)[GK][GM + 4], float (&Ys)[GK][GN + 4]) {
+                                          T* __restrict__ c, size_t ldc, typename G::Shared& sh) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  float acc[4][8];
+  float acc[G::TM][G::TN];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < G::TM; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
-  float xr[4], yr[8];
+    for (int j = 0; j < G::TN; ++j) acc[i][j] = 0.0f;
+  float xr[G::XR], yr[G::YR];
+  auto xi = [&](int idx) { return WGRAD ? idx % G::BM : idx / G::BK; };
+  auto xq = [&](int idx) { return WGRAD ? idx / G::BM : idx % G::BK; };
   auto fetch = [&](int q0) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int idx = tid + r * kThreads;
-      const int i = WGRAD ? idx & 63 : idx >> 4, q = q0 + (WGRAD ? idx >> 6 : idx & 15);
+    for (int r = 0; r < G::XR; ++r) {
+      const int i = xi(tid + r * kThreads), q = q0 + xq(tid + r * kThreads);
       xr[r] = i < mi && q < nq ? Elem<T>::to_f(x[WGRAD ? q * ldx + i : i * ldx + q]) : 0.0f;
     }
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int idx = tid + r * kThreads;
-      const int j = idx & 127, q = q0 + (idx >> 7);
+    for (int r = 0; r < G::YR; ++r) {
+      const int idx = tid + r * kThreads, j = idx % G::BN, q = q0 + idx / G::BN;
       yr[r] = j < nj && q < nq ? Elem<T>::to_f(y[q * ldy + j]) : 0.0f;
     }
   };
   fetch(0);
-  for (int q0 = 0; q0 < nq; q0 += GK) {
+  for (int q0 = 0; q0 < nq; q0 += G::BK) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int idx = tid + r * kThreads;
-      if (WGRAD) Xs[idx >> 6][idx & 63] = xr[r];
-      else Xs[idx & 15][idx >> 4] = xr[r];
-    }
+    for (int r = 0; r < G::XR; ++r) sh.x[xq(tid + r * kThreads)][xi(tid + r * kThreads)] = xr[r];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
+    for (int r = 0; r < G::YR; ++r) {
       const int idx = tid + r * kThreads;
-      Ys[idx >> 7][idx & 127] = yr[r];
+      sh.y[idx / G::BN][idx % G::BN] = yr[r];
     }
     __syncthreads();
-    if (q0 + GK < nq) fetch(q0 + GK);
+    if (q0 + G::BK < nq) fetch(q0 + G::BK);
+#pragma unroll 16
+    for (int q = 0; q < G::BK; ++q) {
+      float xv[G::TM], yv[G::TN];
+      take<G::TM, G::BM>(sh.x[q], ty, xv);
+      take<G::TN, G::BN>(sh.y[q], tx, yv);
 #pragma unroll
-    for (int q = 0; q < GK; ++q) {
-      const float4 xv = *reinterpret_cast<const float4*>(&Xs[q][ty * 4]);
-      const float4 y0 = *reinterpret_cast<const float4*>(&Ys[q][tx * 4]);
-      const float4 y1 = *reinterpret_cast<const float4*>(&Ys[q][64 + tx * 4]);
-      const float xa[4] = {xv.x, xv.y, xv.z, xv.w};
-      const float ya[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+      for (int i = 0; i < G::TM; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(xa[i], ya[j], acc[i][j]);
+        for (int j = 0; j < G::TN; ++j) acc[i][j] = fmaf(xv[i], yv[j], acc[i][j]);
     }
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (ty * 4 + i >= mi) continue;
+  for (int i = 0; i < G::TM; ++i) {
+    const int row = place<G::TM, G::BM>(ty, i);
+    if (row >= mi) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = (j >> 2) * 64 + tx * 4 + (j & 3);
-      if (col < nj) c[(size_t)(ty * 4 + i) * ldc + col] = Elem<T>::from_f(acc[i][j]);
+    for (int j = 0; j < G::TN; ++j) {
+      const int col = place<G::TN, G::BN>(tx, j);
+      if (col < nj) c[(size_t)row * ldc + col] = Elem<T>::from_f(acc[i][j]);
     }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, class G>
+__global__ void __launch_bounds__(kThreads, 2)
     dgrad_simt_kernel(const T* __restrict__ d, const T* __restrict__ w,
                       const int32_t* __restrict__ seg_end, int M, int N, int K, int E,
                       T* __restrict__ d_a) {
-  __shared__ float Xs[GK][GM + 4], Ys[GK][GN + 4];
+  __shared__ __align__(16) typename G::Shared sh;
   __shared__ int prefix[kMaxExperts + 1];
   __shared__ int scan_tmp[33];
   pdl_wait();
-  const int n_tiles = (K + GN - 1) / GN;
-  const int total = build_tile_prefix(seg_end, E, M, GM, n_tiles, prefix, scan_tmp);
+  const int n_tiles = (K + G::BN - 1) / G::BN;
+  const int total = build_tile_prefix(seg_end, E, M, G::BM, n_tiles, prefix, scan_tmp);
   for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-    const SegTile st = decode_tile(tile, prefix, seg_end, E, M, GM, n_tiles);
-    const int k0 = st.n_idx * GN;
-    grad_tile<T, false>(d + (size_t)st.m0 * N, N, st.m_end - st.m0,
-                        w + (size_t)st.e * N * K + k0, K, K - k0, N,
-                        d_a + (size_t)st.m0 * K + k0, K, Xs, Ys);
+    const SegTile st = decode_tile(tile, prefix, seg_end, E, M, G::BM, n_tiles);
+    const int k0 = st.n_idx * G::BN;
+    grad_tile<T, false, G>(d + (size_t)st.m0 * N, N, st.m_end - st.m0,
+                           w + (size_t)st.e * N * K + k0, K, K - k0, N,
+                           d_a + (size_t)st.m0 * K + k0, K, sh);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, class G>
+__global__ void __launch_bounds__(kThreads, 2)
     wgrad_simt_kernel(const T* __restrict__ d, const T* __restrict__ a,
                       const int32_t* __restrict__ seg_end, int M, int N, int K, int E,
                       T* __restrict__ d_w) {
-  __shared__ float Xs[GK][GM + 4], Ys[GK][GN + 4];
+  __shared__ __align__(16) typename G::Shared sh;
   pdl_wait();
-  const long long tn = (N + GM - 1) / GM, tk = (K + GN - 1) / GN;
+  const long long tn = (N + G::BM - 1) / G::BM, tk = (K + G::BN - 1) / G::BN;
   for (long long tile = blockIdx.x; tile < tn * tk * E; tile += gridDim.x) {
     const int e = (int)(tile / (tn * tk));
     const long long in = tile - e * (tn * tk);
-    const int n0 = (int)(in / tk) * GM, k0 = (int)(in % tk) * GN;
+    const int n0 = (int)(in / tk) * G::BM, k0 = (int)(in % tk) * G::BN;
     int lo, hi;
     seg_bounds(seg_end, e, M, 0, lo, hi);
-    grad_tile<T, true>(d + (size_t)lo * N + n0, N, N - n0, a + (size_t)lo * K + k0, K, K - k0,
-                       hi - lo, d_w + ((size_t)e * N + n0) * K + k0, K, Xs, Ys);
+    grad_tile<T, true, G>(d + (size_t)lo * N + n0, N, N - n0, a + (size_t)lo * K + k0, K, K - k0,
+                          hi - lo, d_w + ((size_t)e * N + n0) * K + k0, K, sh);
   }
 }
 
@@ -138,8 +160,10 @@ __global__ void __launch_bounds__(kThreads)
   int lo, hi;
   seg_bounds(seg_end, e, M, 0, lo, hi);
   float sum = 0.0f;
-  if (n < N)
+  if (n < N) {
+#pragma unroll 8
     for (int m = lo + warp; m < hi; m += kThreads / 32) sum += Elem<T>::to_f(d[(size_t)m * N + n]);
+  }
   part[warp][lane] = sum;
   __syncthreads();
   if (warp == 0 && n < N) {
@@ -148,29 +172,51 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// 64 x 128 outputs a tile where that gives every SM one; where it does not, 32 x 32
+// with four times the terms a step, whose latency then bounds.  3 experts of 100 rows,
+// 1000 x 1000, d_a: 75 us with the wide tile, 54 with the small one; d_w of 2000 rows,
+// 50 x 1000: 143 and 39; 32 experts of 20 rows, 100 x 1000, d_a: 18 and 23.  (128 x 128
+// gains 5 to 12% at 1024 rows an expert and loses as much at 64.)
+using Wide = Tile<64, 128, 16>;
+using Small = Tile<32, 32, 64>;
+template <typename Fn>
+cudaError_t pick_tile(long long row_tiles, long long cols, Fn f) {
+  if (row_tiles * ((cols + Wide::BN - 1) / Wide::BN) >= num_sms()) return f(Wide{});
+  return f(Small{});
+}
+
 template <typename T>
 cudaError_t dgrad_t(const void* d, const void* w, const int32_t* seg_end, int M, int N, int K,
                     int E, void* d_a, cudaStream_t s) {
-  const long long tiles = (long long)((M + GM - 1) / GM + E) * ((K + GN - 1) / GN);
-  const auto kern = dgrad_simt_kernel<T>;
-  const long long cap = (long long)num_sms() * resident_ctas((const void*)kern, kThreads);
-  const cudaError_t e = launch_pdl(kern, dim3((unsigned)std::min(tiles, cap)), dim3(kThreads), 0,
-                                   s, static_cast<const T*>(d), static_cast<const T*>(w), seg_end,
-                                   M, N, K, E, static_cast<T*>(d_a));
-  count_launch();
-  return e;
+  // an expert with rows has a tile at least
+  const int row_tiles = std::max((M + Wide::BM - 1) / Wide::BM, std::min(E, M));
+  return pick_tile(row_tiles, K, [&](auto tile) {
+    using G = decltype(tile);
+    const long long tiles = ((long long)(M + G::BM - 1) / G::BM + E) * ((K + G::BN - 1) / G::BN);
+    const auto kern = dgrad_simt_kernel<T, G>;
+    const long long cap = (long long)num_sms() * resident_ctas((const void*)kern, kThreads);
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)std::min(tiles, cap)), dim3(kThreads), 0,
+                                     s, static_cast<const T*>(d), static_cast<const T*>(w),
+                                     seg_end, M, N, K, E, static_cast<T*>(d_a));
+    count_launch();
+    return e;
+  });
 }
 template <typename T>
 cudaError_t wgrad_t(const void* d, const void* a, const int32_t* seg_end, int M, int N, int K,
                     int E, void* d_w, cudaStream_t s) {
-  const long long tiles = (long long)((N + GM - 1) / GM) * ((K + GN - 1) / GN) * E;
-  const auto kern = wgrad_simt_kernel<T>;
-  const long long cap = (long long)num_sms() * resident_ctas((const void*)kern, kThreads);
-  const cudaError_t e = launch_pdl(kern, dim3((unsigned)std::min(tiles, cap)), dim3(kThreads), 0,
-                                   s, static_cast<const T*>(d), static_cast<const T*>(a), seg_end,
-                                   M, N, K, E, static_cast<T*>(d_w));
-  count_launch();
-  return e;
+  return pick_tile((long long)((N + Wide::BM - 1) / Wide::BM) * E, K, [&](auto tile) {
+    using G = decltype(tile);
+    const long long tiles =
+        (long long)((N + G::BM - 1) / G::BM) * ((K + G::BN - 1) / G::BN) * E;
+    const auto kern = wgrad_simt_kernel<T, G>;
+    const long long cap = (long long)num_sms() * resident_ctas((const void*)kern, kThreads);
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)std::min(tiles, cap)), dim3(kThreads), 0,
+                                     s, static_cast<const T*>(d), static_cast<const T*>(a),
+                                     seg_end, M, N, K, E, static_cast<T*>(d_w));
+    count_launch();
+    return e;
+  });
 }
 template <typename T>
 cudaError_t bias_t(const void* d, const int32_t* seg_end, int M, int N, int E, void* d_bias,

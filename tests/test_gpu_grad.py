@@ -381,6 +381,74 @@ def test_wgrad(moe, counts, N, K, dtype):
     assert none is None and torch.equal(again, dw)
 
 
+@pytest.mark.parametrize("dtype", DTYPES[:2])
+@pytest.mark.parametrize("counts", [[1], [16, 48, 0, 64], [300, 2], [0, 7] * 20])
+@pytest.mark.parametrize("N,K", [(1032, 8), (1032, 520), (2056, 1032)])
+def test_dgrad_long_sums(moe, counts, N, K, dtype):
+    g = gen(sum(counts) + N + K)
+    M, E = sum(counts), len(counts)
+    d, w = randn(g, M, N, dtype=dtype), randn(g, E, N, K, dtype=dtype, std=0.03)
+    ref, slack = R.dgrad(d, w, segments(counts))
+    R.close(moe.moe_grouped_gemm_dgrad(d, w, segments(counts)), ref, slack, "d_a")
+
+
+@pytest.mark.parametrize("dtype", DTYPES[:2])
+@pytest.mark.parametrize("counts", [[33, 0, 5] * 14, [0] * 500 + [3, 0, 64] * 8 + [0] * 500,
+                                    [1] * 1024, [130] * 40])
+@pytest.mark.parametrize("N,K", [(520, 776), (264, 136)])
+def test_wgrad_many_tiles(moe, counts, N, K, dtype):
+    """Several tiles a CTA, up to 1024 experts, most of them empty or none: the same workspace
+    twice, the second time with its counters as the first left them."""
+    g = gen(len(counts) + N)
+    M, E = sum(counts), len(counts)
+    d, a = randn(g, M, N, dtype=dtype, std=0.1), randn(g, M, K, dtype=dtype)
+    ws = torch.zeros(moe.moe_grouped_gemm_wgrad_workspace_size(M, N, K, E), dtype=torch.uint8,
+                     device="cuda")
+    rw, sw, rb, sb = R.wgrad(d, a, segments(counts))
+    for _ in range(2):
+        dw, db = moe.moe_grouped_gemm_wgrad(d, a, segments(counts), bias=True, ws=ws)
+        R.close(dw, rw, sw, "d_w")
+        R.close(db, rb, sb, "d_bias")
+    assert moe.moe_sync_status(ws) == moe.MOE_OK and (ws[:256] == 0).all()
+
+
+def test_wgrad_on_two_streams(moe):
+    """Calls that run at the same time, with workspaces of their own."""
+    g = gen(20)
+    counts = [200, 0, 77, 300, 1]
+    M, N, K = sum(counts), 1024, 768
+    seg = segments(counts)
+    sets = [(randn(g, M, N, dtype=torch.bfloat16, std=0.1), randn(g, M, K, dtype=torch.bfloat16),
+             torch.zeros(4096, dtype=torch.uint8, device="cuda")) for _ in range(2)]
+    want = [moe.moe_grouped_gemm_wgrad(d, a, seg, bias=True, ws=ws) for d, a, ws in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (d, a, ws) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(moe.moe_grouped_gemm_wgrad(d, a, seg, bias=True, ws=ws))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for dw, db in got[i]:
+            assert torch.equal(dw, want[i][0]) and torch.equal(db, want[i][1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N", [(1, 8), (5000, 40), (70000, 72), (333, 33)])
+def test_bias_of_long_columns(moe, M, N, dtype):
+    """Column sums over many rows, also into a bias that starts between 16-byte lines."""
+    g = gen(M)
+    d, a = randn(g, M, N, dtype=dtype), randn(g, M, 8, dtype=dtype)
+    seg = segments([M - M // 3, 0, M // 3])
+    _, _, rb, sb = R.wgrad(d, a, seg)
+    # a chain of at most M / 8 + 64 additions and a tree: the bound's M terms hold
+    R.close(moe.moe_grouped_gemm_wgrad(d, a, seg, bias=True)[1], rb, sb)
+    odd = torch.empty(3 * N + 1, dtype=dtype, device="cuda")[1:].view(3, N)
+    moe.moe_grouped_gemm_wgrad(d, a, seg, bias=odd)
+    R.close(odd, rb, sb)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N,K", [(64, 64), (264, 328), (45, 30)])
 def test_products_keep_to_their_rows(moe, N, K, dtype):
