@@ -1253,7 +1253,8 @@ moe_status moe_grouped_gemm_wgrad(const void* d_out, const void* a, const int32_
   Span outs[] = {{d_w, (size_t)E * N * K * esz}, {d_bias, (size_t)E * N * esz}, {ws, need}};
   Span ins[] = {{d_out, (size_t)M * N * esz}, {a, (size_t)M * K * esz}, {seg_end, (size_t)E * 4}};
   if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
-  const bool tc = dtype != MOE_F32 && num_sms() >= 2 && M > 0 && tc_ok(d_out, a, d_w, N, K, M);
+  const bool tc = dtype != MOE_F32 && num_sms() >= 2 && M > 0 &&
+                  tc_ok(d_out, a, d_w, N, K, M) && gemm_wgrad_ok(N, K);
   const bool with_bias = tc && aligned16(d_bias);  // the bias' sums beside the products
   if (d_bias && !with_bias) {
     const cudaError_t e = launch_bias_grad(d_out, seg_end, M, N, E, dtype, d_bias, stream);

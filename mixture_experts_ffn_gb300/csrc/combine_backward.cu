@@ -22,13 +22,13 @@ __global__ void __launch_bounds__(kThreads)
                             float* __restrict__ d_w) {
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (kThreads / 32);
-  for (int r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < M; r += warps) {
+  const long long warps = gridDim.x * (kThreads / 32);
+  for (long long r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < M; r += warps) {
     const int row = route_to_row[r];
     const bool ok = row >= 0 && row < M;
     float dot = 0.0f;
     if (ok) {
-      const T* d = d_out + (size_t)(r / K) * H;
+      const T* d = d_out + (size_t)((int)r / K) * H;
       const size_t at = (size_t)row * H;
       const float f = d_y ? scale * w[r] : 0.0f;
       for (int h = lane; h < H; h += 32) {
@@ -88,12 +88,12 @@ __global__ void __launch_bounds__(kThreads)
   pdl_launch();
   pdl_wait();
   const int lane = threadIdx.x % LANES;
-  const int groups = gridDim.x * (kThreads / LANES);
-  for (int r = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES; r < M; r += groups) {
+  const long long groups = gridDim.x * (kThreads / LANES);
+  for (long long r = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES; r < M; r += groups) {
     const int row = route_to_row[r];
     float dot[U] = {};
     if (row >= 0 && row < M) {
-      const uint4* d = d_out + (size_t)(r / K) * n;
+      const uint4* d = d_out + (size_t)((int)r / K) * n;
       const uint4* src = y + (size_t)row * n;
       uint4* dst = d_y + (size_t)row * n;
       const float f = d_y ? scale * w[r] : 0.0f;

@@ -104,8 +104,7 @@ constexpr size_t kSmemBytes =
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
 // A tile: expert e with rows [lo, hi), nt and kt its corner in tiles; none for
-// lo == hi.  In the schedule {e, lo, hi, nt << 16 | kt} (the launcher keeps both
-// below 2^16).
+// lo == hi.  In the schedule {e, lo, hi, nt << 16 | kt}.
 struct WgTile {
   int e, lo, hi, nt, kt;
   __device__ __forceinline__ bool none() const { return lo == hi; }
@@ -125,7 +124,8 @@ __device__ __forceinline__ WgTile wg_decode(int t, const WgShared* sh,
   const int lane = threadIdx.x & 31;
   WgTile r = {};
   const int q = t / per, in = t - q * per;
-  if (q >= sh->live_before[kMaxExperts / 32]) return r;
+  // (a counter that was not cleared gives no tile, and no fault)
+  if (t < 0 || q >= sh->live_before[kMaxExperts / 32]) return r;
   // the word of live experts that holds the q-th, and in it the bit with the rest below
   const int before = sh->live_before[lane];
   const uint32_t word = sh->live[lane];
@@ -578,10 +578,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 }  // namespace
 
+// a schedule entry has 16 bits for each coordinate of a tile
+bool gemm_wgrad_ok(int N, int K) {
+  return N % 8 == 0 && K % 8 == 0 && N <= 0xffff * TN && K <= 0xffff * TK;
+}
+
 cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_end, int M, int N,
                               int K, int E, bool f16, void* d_w, void* d_bias, int* status,
                               cudaStream_t s) {
-  if (N % 8 != 0 || K % 8 != 0) return cudaErrorInvalidValue;
+  if (!gemm_wgrad_ok(N, K)) return cudaErrorInvalidValue;
   CUtensorMap md, ma, mo;
   auto rows = [&](CUtensorMap* m, const void* p, int cols) {
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)M};
@@ -596,7 +601,6 @@ cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_e
       !tmap::encode_bf16(&mo, d_w, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, f16))
     return cudaErrorInvalidValue;
   int tn = (N + TN - 1) / TN, tk = (K + TK - 1) / TK;
-  if (tn > 0xffff || tk > 0xffff) return cudaErrorInvalidValue;
   const int pairs = std::max(1, std::min(E * tn * tk, num_sms() / 2));
   const void* kern = f16 ? (const void*)gemm_wgrad_kernel<true> : (const void*)gemm_wgrad_kernel<false>;
   cudaError_t e = set_smem_limit(kern, (int)kSmemBytes);

@@ -254,7 +254,8 @@ cudaError_t launch_dgrad_simt(const void* d, const void* w, const int32_t* seg_e
 cudaError_t launch_wgrad_simt(const void* d, const void* a, const int32_t* seg_end, int M, int N,
                               int K, int E, moe_dtype dt, void* d_w, cudaStream_t s);
 // tcgen05 gradients of 16-bit weights and bias (d_bias may be null; gemm_wgrad.cu);
-// M >= 1, N and K multiples of 8, all 16-byte aligned
+// M >= 1, all 16-byte aligned, extents for which gemm_wgrad_ok
+bool gemm_wgrad_ok(int N, int K);
 cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_end, int M, int N,
                               int K, int E, bool f16, void* d_w, void* d_bias, int* status,
                               cudaStream_t s);

@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(kThreads)
   pdl_launch();
   pdl_wait();
   const int lane = threadIdx.x & 31, size = dt == MOE_F32 ? 4 : 2;
-  const int warps = gridDim.x * (kThreads / 32);
-  for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < T; t += warps) {
+  const long long warps = gridDim.x * (kThreads / 32);
+  for (long long t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < T; t += warps) {
     const size_t row = (size_t)t * E;
     int id[2];
     float z[2], g[2], s[2] = {}, l[2] = {};
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kThreads)
   pdl_launch();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (kThreads / 32);
-  for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < T; t += warps) {
+  const long long warps = gridDim.x * (kThreads / 32);
+  for (long long t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < T; t += warps) {
     const size_t row = (size_t)t * E;
     int id[2];
     float g[2], z[NPL];

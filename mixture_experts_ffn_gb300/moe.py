@@ -248,6 +248,23 @@ def _asked(out, shape: tuple, dtype: torch.dtype, like, what: str):
     return out
 
 
+def _segments(seg_end):
+    """Segment ends of at least one expert, or None."""
+    if seg_end is not None:
+        _typed(seg_end, torch.int32, "seg_end")
+        if seg_end.numel() == 0:  # to the library an empty tensor is none
+            raise ValueError("seg_end is [E]")
+
+
+def _made(out, shape: tuple, dtype: torch.dtype, like, what: str):
+    """An output that every call has: True makes one, a tensor is checked."""
+    if out is True:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if out is False or out is None:
+        raise ValueError(f"{what} is True or the tensor to write")
+    return _asked(out, shape, dtype, like, what)
+
+
 def _ws(nbytes: int, device) -> torch.Tensor:
     """A fresh workspace with a cleared status word (torch's caching allocator
     returns 512-byte aligned blocks)."""
@@ -837,25 +854,23 @@ def moe_combine_backward(d_out, expert_out, topk_weights, route_to_row, scale=1.
     weights') or the tensor to write.  topk_weights [T, K]."""
     lib = load_library()
     _together(d_out, expert_out, topk_weights, route_to_row)
+    dtype = d_out.dtype
     T, H = d_out.shape
-    _typed(topk_weights, torch.float32, "topk_weights")
-    _typed(route_to_row, torch.int32, "route_to_row")
-    _typed(expert_out, d_out.dtype, "expert_out")
-    if topk_weights.dim() != 2 or topk_weights.shape[0] != T:
-        raise ValueError("topk_weights is [T, K]")
-    K = topk_weights.shape[1]
-    if route_to_row.numel() != T * K or \
-            (expert_out is not None and expert_out.shape != (T * K, H)):
-        raise ValueError("route_to_row is [T * K] and expert_out [T * K, H]")
+    Tw, K = topk_weights.shape
+    M = T * K
+    if topk_weights.dtype is not torch.float32 or route_to_row.dtype is not torch.int32 or \
+            (expert_out is not None and expert_out.dtype is not dtype):
+        raise TypeError("topk_weights is float32, route_to_row int32, expert_out as d_out")
+    if Tw != T or K == 0 or route_to_row.numel() != M or \
+            (expert_out is not None and expert_out.shape != (M, H)):
+        raise ValueError("topk_weights is [T, K], route_to_row [T * K], expert_out [T * K, H]")
     if expert_out is None and d_topk_weights is not False:
         raise ValueError("the weights' gradient takes expert_out")
-    if K == 0:
-        raise ValueError("K is at least 1")
-    d_expert_out = _asked(d_expert_out, (T * K, H), d_out.dtype, d_out, "d_expert_out")
+    d_expert_out = _asked(d_expert_out, (M, H), dtype, d_out, "d_expert_out")
     d_topk_weights = _asked(d_topk_weights, (T, K), torch.float32, d_out, "d_topk_weights")
     _check("moe_combine_backward",
            lib.moe_combine_backward(d_out.data_ptr(), _ptr(expert_out), topk_weights.data_ptr(),
-                                    route_to_row.data_ptr(), T, K, H, _dt(d_out), scale,
+                                    route_to_row.data_ptr(), T, K, H, _dtype(dtype), scale,
                                     _ptr(d_expert_out), _ptr(d_topk_weights), _stream_of(d_out)))
     return d_expert_out, d_topk_weights
 
@@ -865,17 +880,17 @@ def moe_permute_backward(d_expert_input, route_to_row, K: int, d_hidden=True):
     d_expert_input [T * K, H]."""
     lib = load_library()
     _together(d_expert_input, route_to_row)
+    dtype = d_expert_input.dtype
     M, H = d_expert_input.shape
-    _typed(route_to_row, torch.int32, "route_to_row")
+    if route_to_row.dtype is not torch.int32:
+        raise TypeError("route_to_row is int32")
     if K < 1 or M % K or route_to_row.numel() != M:
         raise ValueError("d_expert_input is [T * K, H] and route_to_row [T * K]")
     T = M // K
-    d_hidden = _asked(d_hidden, (T, H), d_expert_input.dtype, d_expert_input, "d_hidden")
-    if d_hidden is None:
-        raise ValueError("d_hidden is True or the tensor to write")
+    d_hidden = _made(d_hidden, (T, H), dtype, d_expert_input, "d_hidden")
     _check("moe_permute_backward",
            lib.moe_permute_backward(d_expert_input.data_ptr(), route_to_row.data_ptr(), T, K, H,
-                                    _dt(d_expert_input), d_hidden.data_ptr(),
+                                    _dtype(dtype), d_hidden.data_ptr(),
                                     _stream_of(d_expert_input)))
     return d_hidden
 
@@ -886,24 +901,27 @@ def moe_act_checkpoint(p, act: ActParams, seg_end=None, out=True, codes=None, sc
     at and past seg_end[-1] are left alone.  out: True, False, or the tensor to write."""
     lib = load_library()
     _together(p, seg_end, codes, scales)
-    _typed(seg_end, torch.int32, "seg_end")
+    dtype = p.dtype
     M, N1 = p.shape
+    _segments(seg_end)
     gated = act.kind in _GATED
     if gated and N1 % 2:
         raise ValueError("a gated activation takes pairs of columns")
     F, Np = N1 // 2 if gated else N1, moe_mx_columns(N1)
-    out = _asked(out, (M, F), p.dtype, p, "out")
-    _coded(codes, _E4M3, "codes")
-    _coded(scales, _E8M0, "scales")
-    _fits(codes, (M, Np), 1, "codes")
-    _fits(scales, (M, Np // 32), 1, "scales")
+    out = _asked(out, (M, F), dtype, p, "out")
     if codes is None:
         codes = torch.empty((M, Np), dtype=torch.float8_e4m3fn, device=p.device)
+    else:
+        _coded(codes, _E4M3, "codes")
+        _fits(codes, (M, Np), 1, "codes")
     if scales is None:
         scales = torch.empty((M, Np // 32), dtype=torch.float8_e8m0fnu, device=p.device)
+    else:
+        _coded(scales, _E8M0, "scales")
+        _fits(scales, (M, Np // 32), 1, "scales")
     _check("moe_act_checkpoint",
            lib.moe_act_checkpoint(p.data_ptr(), _ptr(seg_end), M, F,
-                                  0 if seg_end is None else seg_end.numel(), _dt(p),
+                                  0 if seg_end is None else seg_end.numel(), _dtype(dtype),
                                   ctypes.byref(act), _ptr(out), codes.data_ptr(),
                                   scales.data_ptr(), _stream_of(p)))
     return out, codes, scales
@@ -915,26 +933,25 @@ def moe_act_backward(p, d_out, act: ActParams, scales=None, seg_end=None, d_p=Tr
     seg_end, rows at and past seg_end[-1] are left alone."""
     lib = load_library()
     _together(d_out, p, scales, seg_end)
-    _typed(seg_end, torch.int32, "seg_end")
+    dtype = d_out.dtype
     M, F = d_out.shape
     N1 = 2 * F if act.kind in _GATED else F
+    _segments(seg_end)
     if scales is None:
-        _typed(p, d_out.dtype, "p")
+        _typed(p, dtype, "p")
         if p.shape != (M, N1):
             raise ValueError("p is [M, N1], N1 = 2F for a gated activation")
     else:
         Np = moe_mx_columns(N1)
         _coded(p, _E4M3, "p")
         _coded(scales, _E8M0, "scales")
-        _fits(p, (M, Np), 1, "p")
-        _fits(scales, (M, Np // 32), 1, "scales")
-    d_p = _asked(d_p, (M, N1), d_out.dtype, d_out, "d_p")
-    if d_p is None:
-        raise ValueError("d_p is True or the tensor to write")
-    out = _asked(out, (M, F), d_out.dtype, d_out, "out")
+        if p.shape != (M, Np) or scales.shape != (M, Np // 32):
+            raise ValueError("p and scales are [M, N1p] codes and [M, N1p / 32] scales")
+    d_p = _made(d_p, (M, N1), dtype, d_out, "d_p")
+    out = _asked(out, (M, F), dtype, d_out, "out")
     _check("moe_act_backward",
            lib.moe_act_backward(p.data_ptr(), _ptr(scales), d_out.data_ptr(), _ptr(seg_end), M, F,
-                                0 if seg_end is None else seg_end.numel(), _dt(d_out),
+                                0 if seg_end is None else seg_end.numel(), _dtype(dtype),
                                 ctypes.byref(act), d_p.data_ptr(), _ptr(out), _stream_of(d_out)))
     return d_p, out
 
@@ -944,20 +961,19 @@ def moe_grouped_gemm_dgrad(d_out, w, seg_end, d_a=True, ws=None):
     rows m of expert e; d_out [M, N], w [E, N, K]."""
     lib = load_library()
     _together(d_out, w, seg_end, ws)
+    dtype = d_out.dtype
     M, N = d_out.shape
-    E, _, K = w.shape
-    _typed(w, d_out.dtype, "w")
-    _typed(seg_end, torch.int32, "seg_end")
-    if w.shape[1] != N or seg_end.numel() != E:
+    E, Nw, K = w.shape
+    if w.dtype is not dtype or seg_end.dtype is not torch.int32:
+        raise TypeError("w is of d_out's type and seg_end int32")
+    if Nw != N or seg_end.numel() != E:
         raise ValueError("d_out is [M, N], w [E, N, K] and seg_end [E]")
-    d_a = _asked(d_a, (M, K), d_out.dtype, d_out, "d_a")
-    if d_a is None:
-        raise ValueError("d_a is True or the tensor to write")
+    d_a = _made(d_a, (M, K), dtype, d_out, "d_a")
     if ws is None:
         ws = _ws(MOE_STATUS_BYTES, d_out.device)
     _check("moe_grouped_gemm_dgrad",
            lib.moe_grouped_gemm_dgrad(d_out.data_ptr(), w.data_ptr(), seg_end.data_ptr(), M, N, K,
-                                      E, _dt(d_out), d_a.data_ptr(), ws.data_ptr(),
+                                      E, _dtype(dtype), d_a.data_ptr(), ws.data_ptr(),
                                       ws.numel() * ws.element_size(), _stream_of(d_out)))
     return d_a
 
@@ -972,22 +988,23 @@ def moe_grouped_gemm_wgrad(d_out, a, seg_end, bias=False, d_w=True, ws=None):
     without rows).  bias: True, False, or the tensor to write."""
     lib = load_library()
     _together(d_out, a, seg_end, ws)
+    dtype = d_out.dtype
     M, N = d_out.shape
-    K, E = a.shape[1], seg_end.numel()
-    _typed(a, d_out.dtype, "a")
-    _typed(seg_end, torch.int32, "seg_end")
-    if a.shape[0] != M or E == 0:
+    Ma, K = a.shape
+    E = seg_end.numel()
+    if a.dtype is not dtype or seg_end.dtype is not torch.int32:
+        raise TypeError("a is of d_out's type and seg_end int32")
+    if Ma != M or E == 0:
         raise ValueError("d_out is [M, N], a [M, K] and seg_end [E]")
-    d_w = _asked(d_w, (E, N, K), d_out.dtype, d_out, "d_w")
-    if d_w is None:
-        raise ValueError("d_w is True or the tensor to write")
-    d_bias = _asked(bias, (E, N), d_out.dtype, d_out, "bias")
+    d_w = _made(d_w, (E, N, K), dtype, d_out, "d_w")
+    d_bias = _asked(bias, (E, N), dtype, d_out, "bias")
     if ws is None:
         ws = _ws(lib.moe_grouped_gemm_wgrad_workspace_size(M, N, K, E), d_out.device)
     _check("moe_grouped_gemm_wgrad",
            lib.moe_grouped_gemm_wgrad(d_out.data_ptr(), a.data_ptr(), seg_end.data_ptr(), M, N, K,
-                                      E, _dt(d_out), d_w.data_ptr(), _ptr(d_bias), ws.data_ptr(),
-                                      ws.numel() * ws.element_size(), _stream_of(d_out)))
+                                      E, _dtype(dtype), d_w.data_ptr(), _ptr(d_bias),
+                                      ws.data_ptr(), ws.numel() * ws.element_size(),
+                                      _stream_of(d_out)))
     return d_w, d_bias
 
 
@@ -996,15 +1013,14 @@ def moe_route_backward(logits, topk_ids, d_topk_weights, p: RouteParams, d_logit
     logits' type, for the ids that moe_route returned (or was given) under p."""
     lib = load_library()
     _together(logits, topk_ids, d_topk_weights)
+    dtype = logits.dtype
     T, E = logits.shape
-    _typed(topk_ids, torch.int32, "topk_ids")
-    _typed(d_topk_weights, torch.float32, "d_topk_weights")
-    _fits(topk_ids, (T, p.top_k), 4, "topk_ids")
-    _fits(d_topk_weights, (T, p.top_k), 4, "d_topk_weights")
-    d_logits = _asked(d_logits, (T, E), logits.dtype, logits, "d_logits")
-    if d_logits is None:
-        raise ValueError("d_logits is True or the tensor to write")
-    rp = p if p.dtype == _dt(logits) else _rp(p, logits)
+    if topk_ids.dtype is not torch.int32 or d_topk_weights.dtype is not torch.float32:
+        raise TypeError("topk_ids is int32 and d_topk_weights float32")
+    if topk_ids.shape != (T, p.top_k) or d_topk_weights.shape != (T, p.top_k):
+        raise ValueError("topk_ids and d_topk_weights are [T, K]")
+    d_logits = _made(d_logits, (T, E), dtype, logits, "d_logits")
+    rp = p if p.dtype == _dtype(dtype) else _rp(p, logits)
     _check("moe_route_backward",
            lib.moe_route_backward(logits.data_ptr(), topk_ids.data_ptr(),
                                   d_topk_weights.data_ptr(), T, E, ctypes.byref(rp),

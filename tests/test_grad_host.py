@@ -249,6 +249,7 @@ def test_binding_refuses_other_mistakes(moe):
     refused(moe, f, {**kw, "d_hidden": False}, "no output")
     f, kw, _ = c["checkpoint"]
     refused(moe, f, {**kw, "p": z(M, 2 * F + 1)}, "odd gated width")
+    refused(moe, f, {**kw, "seg_end": i32(0)}, "no experts")
     f, kw, _ = c["act"]
     refused(moe, f, {**kw, "d_p": False}, "no output")
     refused(moe, f, {**kw, "scales": None}, "codes without scales")
