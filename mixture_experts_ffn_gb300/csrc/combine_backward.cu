@@ -2,7 +2,9 @@
 // row = route_to_row[r] and out[t] = c sum_k w[r] y[row],
 //   d_y[row] = c w[r] d_out[t],   d_w[r] = c <d_out[t], y[row]>.
 // One pass over y and d_out: a route's products with d_out[t] and its scaled
-// copy come from the same registers.  Bound by HBM: y read, d_y written.
+// copy come from the same registers.  Bound by HBM: y read, d_y written (8192 tokens,
+// top-8, 7168 columns, bf16: 311 us, 6.4 TB/s; the sum of the rows in permute.cu 166 us,
+// 6.4 TB/s; a plain copy of as much as y here 276 us, 6.8 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -143,8 +145,10 @@ cudaError_t launch_t(const void* d_out, const void* y, const float* w, const int
                      int K, int H, float scale, void* d_y, float* d_w, cudaStream_t s) {
   const auto a16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   if ((size_t)H * sizeof(T) % 16 == 0 && a16(d_out) && a16(y) && a16(d_y)) {
-    // few routes: a CTA each, so that a row's latency is shared by eight warps
-    const bool few = M < 4 * num_sms();
+    // a CTA each for few routes, so that eight warps share a row's latency: 24 routes of
+    // 7168 columns 2.2 us against 5.5 with a warp each, 1024 of them 5.5 and 8.6; 2048 of
+    // 2880 columns 7.5 and 6.0
+    const bool few = M < 8 * num_sms();
     const auto kern = few ? combine_backward_vec<T, kThreads> : combine_backward_vec<T, 32>;
     const long long want = few ? M : ((long long)M + kThreads / 32 - 1) / (kThreads / 32);
     const long long cap = (long long)num_sms() * resident_ctas((const void*)kern, kThreads);
