@@ -1,6 +1,6 @@
 /*
  * moe.h -- C ABI of libmoe.so, a GB300 (sm_103a) routed Mixture-of-Experts FFN
- * forward.
+ * forward, and the gradients of its stages.
  *
  * The layer computes, per token t with hidden row h[t] and router logits z[t]:
  *
