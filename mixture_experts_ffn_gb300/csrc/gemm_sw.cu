@@ -159,7 +159,7 @@ __device__ __noinline__ bool wait_cluster(uint64_t* b, uint32_t parity, volatile
   }
   return true;
 }
-
+// TMA loads as tma2_2d and tma2_3d (tc_ptx.cuh)
 __device__ __forceinline__ void tma2_4d(void* dst, const CUtensorMap* m, uint32_t bar, int c0,
                                         int c1, int c2, int c3) {
   asm volatile(
@@ -200,8 +200,8 @@ __device__ __forceinline__ void umma2_stage(uint32_t d_tmem, uint64_t ad, uint64
       " [%5], %20;\n\t}" ::"r"(d_tmem),
       "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(bar), "l"(ad + AS), "l"(bd + 2),
       "l"(ad + 2 * AS), "l"(bd + 4), "l"(ad + 3 * AS), "l"(bd + 6), "l"(ad1), "l"(bd1),
-      "l"(ad1 + AS),
-      "l"(bd1 + 2), "l"(ad1 + 2 * AS), "l"(bd1 + 4), "l"(ad1 + 3 * AS), "l"(bd1 + 6), "h"((uint16_t)3)
+      "l"(ad1 + AS), "l"(bd1 + 2), "l"(ad1 + 2 * AS), "l"(bd1 + 4), "l"(ad1 + 3 * AS),
+      "l"(bd1 + 6), "h"((uint16_t)3)
       : "memory");
 }
 // The eight K16 MMAs of a one-atom stage with two M halves per CTA: half h's
@@ -232,6 +232,7 @@ __device__ __forceinline__ void umma2_stage_wide(uint32_t d0, uint64_t ad, uint6
       "l"(ad + 3 * AS), "l"(bd + 6), "l"(a1 + 3 * AS), "h"((uint16_t)3)
       : "memory");
 }
+
 // One pair tile: expert e, weight-row tile nt (256 rows: 128 per CTA), and a
 // chunk of the expert's rows [m0, m0 + nv) as the N dimension (N columns,
 // nv <= N <= 256, N a multiple of 16 and at least 32).  nv == 0: an empty
@@ -690,8 +691,8 @@ __global__ void __launch_bounds__(SwRoles<TOK, MH>::THREADS, 1)
             umma2_stage_wide<AS>(d_tmem, adesc0 + off, bdesc0 + off, idesc, ks != 0 ? 1u : 0u,
                                  empty_addr[stage]);
           else
-            umma2_stage<AS>(d_tmem, adesc0 + off, bdesc0 + off, b_atom16, idesc, ks != 0 ? 1u : 0u,
-                        empty_addr[stage]);
+            umma2_stage<AS>(d_tmem, adesc0 + off, bdesc0 + off, b_atom16, idesc,
+                            ks != 0 ? 1u : 0u, empty_addr[stage]);
           any = true;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }

@@ -36,7 +36,8 @@
 // 102, 256 uneven ones (1536 x 2048, 128 experts) 207 instead of 219, 1024 (7168 x
 // 2048, 64 experts) 1148 instead of 1139; by the producer itself, which held up the
 // copies, 1200.  An expert without rows has no tiles; the epilogue warps write its
-// zeros at the end.  Every wait is bounded (2 s); on a timeout the block latches the
+// zeros at the end (found by words of 32 experts; a step an expert cost 2 of the 89 us
+// and 9 of the 207).  Every wait is bounded (2 s); on a timeout the block latches the
 // timeout bit, drains what it issued and frees TMEM.
 //
 // What bounds it: at 1024 rows an expert a stage takes 600 of the 512 cycles that its
@@ -300,7 +301,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // tile j of the schedule (none at its end, or when the wait failed)
   auto next_tile = [&](int j) -> WgTile {
     WgTile r = {};
-    if (!wait_fast<kWaitShared>(&sh->sfull[j % SCHED], (uint32_t)(j / SCHED) & 1u, abort_flag, status)) return r;
+    if (!wait_fast<kWaitShared>(&sh->sfull[j % SCHED], (uint32_t)(j / SCHED) & 1u, abort_flag,
+                                status))
+      return r;
     const uint32_t addr = su32(&sh->sched[j % SCHED]);
     uint32_t corner;
     asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -550,17 +553,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int i = lane; i < OUT_BYTES_WARP / 16; i += 32)
       reinterpret_cast<uint4*>(buf)[i] = make_uint4(0, 0, 0, 0);
     long long before = 0;  // tiles of the empty experts before e
-    for (int e = 0; e < E; ++e) {
-      if ((sh->live[e >> 5] >> (e & 31)) & 1u) continue;
-      WgTile st = {e, 0, 0, 0, 0};
-      for (int in = (int)((npairs + pair - before % npairs) % npairs); in < per; in += npairs) {
-        st.nt = in / tk;
-        st.kt = in - st.nt * tk;
-        const int n = st.n0() + 128 * (int)rank + 32 * quad;
-        for (int c = 64 * grp; c < st.kw(K); c += 128)
-          if (n < N && st.k0() + c < K) store(st, c, n);
+    for (int w = 0; w * 32 < E; ++w) {
+      uint32_t empty = ~sh->live[w];
+      if (E - w * 32 < 32) empty &= (1u << (E - w * 32)) - 1u;
+      for (; empty; empty &= empty - 1u, before += per) {
+        WgTile st = {w * 32 + __ffs(empty) - 1, 0, 0, 0, 0};
+        for (int in = (int)((npairs + pair - before % npairs) % npairs); in < per; in += npairs) {
+          st.nt = in / tk;
+          st.kt = in - st.nt * tk;
+          const int n = st.n0() + 128 * (int)rank + 32 * quad;
+          for (int c = 64 * grp; c < st.kw(K); c += 128)
+            if (n < N && st.k0() + c < K) store(st, c, n);
+        }
       }
-      before += per;
     }
     if (lane == 0) bulk_wait_all();  // every staged box written before the pair exits
   }
@@ -602,7 +607,8 @@ cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_e
     return cudaErrorInvalidValue;
   int tn = (N + TN - 1) / TN, tk = (K + TK - 1) / TK;
   const int pairs = std::max(1, std::min(E * tn * tk, num_sms() / 2));
-  const void* kern = f16 ? (const void*)gemm_wgrad_kernel<true> : (const void*)gemm_wgrad_kernel<false>;
+  const void* kern =
+      f16 ? (const void*)gemm_wgrad_kernel<true> : (const void*)gemm_wgrad_kernel<false>;
   cudaError_t e = set_smem_limit(kern, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -776,6 +776,4 @@ def test_training_step_without_some_routes(moe):
     d_w2, d_b2 = moe.moe_grouped_gemm_wgrad(dy, a, seg, bias=True)
     assert torch.isfinite(d_w2).all() and torch.isfinite(d_b2).all()
     assert torch.isfinite(d_p[:live]).all()
-    d_h = moe.moe_permute_backward(torch.where(torch.arange(T * K, device="cuda")[:, None] < live,
-                                               y, y), rows, K)
-    assert torch.isfinite(d_h).all()
+    assert torch.isfinite(moe.moe_permute_backward(y, rows, K)).all()
