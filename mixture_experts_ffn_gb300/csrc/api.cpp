@@ -1134,6 +1134,22 @@ moe_status moe_ffn_forward_mx(const void* hidden, const void* hidden_scale, cons
 }
 
 // ---------------------------------------------------------------- gradients
+namespace {
+// Columns of a pair's tile of the rows' gradient: 512, or 256.  Sums of at most 1024
+// terms are faster with 256 (1024 terms, 8 experts of 2048 rows, K = 4096: 97 us against
+// 105).  Above, a tile of 512 takes 1.9 times one of 256, so whichever rounds of tiles
+// over the SM pairs come to less: 1536 terms, 128 experts of 256 rows, K = 2048, 183 us
+// with 512 and 198 with 256; 64 of 64, 2048 terms, K = 600, 43 and 42; one of 2048 rows,
+// 2048 x 2048, where only one round is filled in part, 27 and 19.
+bool dgrad_wide(int M, int N, int K, int E) {
+  if (N <= 1024) return false;
+  const long long experts = std::min(E, M), chunks = experts * ((M / experts + 255) / 256);
+  const long long pairs = std::max(1, num_sms() / 2);
+  auto rounds = [&](int cols) { return ((K + cols - 1LL) / cols * chunks + pairs - 1) / pairs; };
+  return rounds(512) * 19 < rounds(256) * 10;
+}
+}  // namespace
+
 moe_status moe_combine_backward(const void* d_out, const void* expert_out,
                                 const float* topk_weights, const int32_t* route_to_row, int T,
                                 int K, int H, moe_dtype dtype, float scale, void* d_expert_out,
@@ -1224,20 +1240,16 @@ moe_status moe_grouped_gemm_dgrad(const void* d_out, const void* w, const int32_
                 {seg_end, (size_t)E * 4}};
   if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
   if (M == 0) return MOE_OK;
-  // 256 output columns a CTA for sums longer than 1024: 4096 terms, 64 experts of 1024
-  // rows, K = 7168, 2191 us against 2273 with 128; 1536 terms, 128 of 21, K = 2048, 125
-  // and 134; 1024 terms, 8 of 2048, K = 4096, 105 and 97; 512, 32 of 512, 46.4 and 45.8
-  const bool wide = N > 1024;
   if (dtype != MOE_F32 && num_sms() >= 2 && tc_ok(d_out, w, d_a, N, K, M))
     return cuda_status(launch_gemm_sw(d_out, w, nullptr, seg_end, M, K, N, E, nullptr, d_a,
                                       static_cast<int*>(ws), stream, nullptr, 1, 0, 0,
-                                      dtype == MOE_F16, wide, true));
+                                      dtype == MOE_F16, dgrad_wide(M, N, K, E), true));
   return cuda_status(launch_dgrad_simt(d_out, w, seg_end, M, N, K, E, dtype, d_a, stream));
 }
 
 size_t moe_grouped_gemm_wgrad_workspace_size(int M, int N, int K, int E) {
   if (!mx_gemm_extent_ok(M, N, K, E)) return 0;
-  return MOE_STATUS_BYTES;
+  return MOE_STATUS_BYTES + gemm_wgrad_partial_bytes(M, N, K, E);
 }
 
 moe_status moe_grouped_gemm_wgrad(const void* d_out, const void* a, const int32_t* seg_end, int M,
@@ -1263,6 +1275,8 @@ moe_status moe_grouped_gemm_wgrad(const void* d_out, const void* a, const int32_
   if (tc)
     return cuda_status(launch_gemm_wgrad(d_out, a, seg_end, M, N, K, E, dtype == MOE_F16, d_w,
                                          with_bias ? d_bias : nullptr, static_cast<int*>(ws),
+                                         reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                                                  MOE_STATUS_BYTES),
                                          stream));
   return cuda_status(launch_wgrad_simt(d_out, a, seg_end, M, N, K, E, dtype, d_w, stream));
 }

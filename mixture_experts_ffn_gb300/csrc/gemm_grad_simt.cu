@@ -172,16 +172,16 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// 64 x 128 outputs a tile where that gives every SM one; where it does not, 32 x 32
-// with four times the terms a step, whose latency then bounds.  3 experts of 100 rows,
-// 1000 x 1000, d_a: 75 us with the wide tile, 54 with the small one; d_w of 2000 rows,
-// 50 x 1000: 143 and 39; 32 experts of 20 rows, 100 x 1000, d_a: 18 and 23.  (128 x 128
-// gains 5 to 12% at 1024 rows an expert and loses as much at 64.)
+// 64 x 128 outputs a tile where that gives two SMs of five one; where it does not, 32 x
+// 32 with four times the terms a step, whose latency then bounds.  2000 rows, 50 x 1000,
+// d_w (8 wide tiles): 143 us with the wide tile, 39 with the small one; 3 experts of 100
+// rows, 1000 x 1000, d_a (48): 75 and 54; 32 of 64 rows, 2048 x 300 (96): 175 and 213.
+// (128 x 128 gains 5 to 12% at 1024 rows an expert and loses as much at 64.)
 using Wide = Tile<64, 128, 16>;
 using Small = Tile<32, 32, 64>;
 template <typename Fn>
 cudaError_t pick_tile(long long row_tiles, long long cols, Fn f) {
-  if (row_tiles * ((cols + Wide::BN - 1) / Wide::BN) >= num_sms()) return f(Wide{});
+  if (row_tiles * ((cols + Wide::BN - 1) / Wide::BN) * 5 >= 2 * num_sms()) return f(Wide{});
   return f(Small{});
 }
 

@@ -40,6 +40,10 @@
 // and 9 of the 207).  Every wait is bounded (2 s); on a timeout the block latches the
 // timeout bit, drains what it issued and frees TMEM.
 //
+// Few tiles (SPLIT): where experts have many rows and their tiles leave SM pairs idle,
+// the rows are cut into `parts` equal pieces, each a tile of its own whose float32 sums
+// go to the workspace, and a second launch adds them up in order (wgrad_parts).
+//
 // What bounds it: at 1024 rows an expert a stage takes 600 of the 512 cycles that its
 // MMAs need even without copies and stores, and 700 with them: 32 KB a stage into
 // each SM is most of what L2 delivers.  The ring's depth counts for that reason (4
@@ -104,8 +108,9 @@ constexpr size_t kSmemBytes =
     (size_t)STAGES * STAGE_BYTES + EPI_WARPS * OUT_BYTES_WARP + sizeof(WgShared) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 
-// A tile: expert e with rows [lo, hi), nt and kt its corner in tiles; none for
-// lo == hi.  In the schedule {e, lo, hi, nt << 16 | kt}.
+// A tile: rows [lo, hi) of an expert, e its place in the result (with SPLIT, part * E +
+// expert in the partial sums), nt and kt its corner in tiles; none for lo == hi.  In the
+// schedule {e, lo, hi, nt << 16 | kt}.
 struct WgTile {
   int e, lo, hi, nt, kt;
   __device__ __forceinline__ bool none() const { return lo == hi; }
@@ -117,16 +122,24 @@ struct WgTile {
   // rows of the last K16 step past the end
   __device__ __forceinline__ bool has_tail() const { return ((hi - lo) & 15) != 0; }
 };
+// Rows of each of an expert's `parts` pieces (the last ones may be shorter, or empty).
+__device__ __forceinline__ int part_rows(int n, int parts) {
+  return ((n + parts - 1) / parts + BR - 1) / BR * BR;
+}
 // Tile t of the list, by a whole warp: the per = tn * tk tiles of the experts with
-// rows follow one another; past the last, none.
+// rows, times `parts`, follow one another; `end`: t is past the last.  A piece without
+// rows is none.
+template <bool SPLIT>
 __device__ __forceinline__ WgTile wg_decode(int t, const WgShared* sh,
                                             const int32_t* __restrict__ seg_end, int M, int per,
-                                            int tk) {
+                                            int tk, int parts, int E, bool& end) {
   const int lane = threadIdx.x & 31;
   WgTile r = {};
-  const int q = t / per, in = t - q * per;
+  const int q = t / (SPLIT ? per * parts : per);
+  int in = t - q * (SPLIT ? per * parts : per);
   // (a counter that was not cleared gives no tile, and no fault)
-  if (t < 0 || q >= sh->live_before[kMaxExperts / 32]) return r;
+  end = t < 0 || q >= sh->live_before[kMaxExperts / 32];
+  if (end) return r;
   // the word of live experts that holds the q-th, and in it the bit with the rest below
   const int before = sh->live_before[lane];
   const uint32_t word = sh->live[lane];
@@ -135,9 +148,16 @@ __device__ __forceinline__ WgTile wg_decode(int t, const WgShared* sh,
   const int k = q - __shfl_sync(0xffffffffu, before, w);
   r.e = w * 32 + __ffs(__ballot_sync(0xffffffffu, (bits >> lane & 1u) &&
                                                       __popc(bits & ((1u << lane) - 1u)) == k)) - 1;
+  seg_bounds(seg_end, r.e, M, 0, r.lo, r.hi);
+  if constexpr (SPLIT) {
+    const int part = in / per, rows = part_rows(r.hi - r.lo, parts);
+    in -= part * per;
+    r.lo = min(r.lo + part * rows, r.hi);
+    r.hi = min(r.lo + rows, r.hi);
+    r.e += part * E;
+  }
   r.nt = in / tk;
   r.kt = in - r.nt * tk;
-  seg_bounds(seg_end, r.e, M, 0, r.lo, r.hi);
   return r;
 }
 // K16 steps of stage s of a tile
@@ -217,14 +237,15 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* s
 }
 
 // tm_d: d [M][N], tm_a: a [M][K], boxes {64, 64}; tm_out: d_w [E][N][K], box
-// {64, 32, 1}; all with 128-byte swizzle, zeros read and nothing written outside.
-template <bool F16>
+// {64, 32, 1}, or with SPLIT the partial sums [parts * E][N][K] in float32, box {32, 32,
+// 1}; all with 128-byte swizzle, zeros read and nothing written outside.
+template <bool F16, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_wgrad_kernel(const __grid_constant__ CUtensorMap tm_d,
                       const __grid_constant__ CUtensorMap tm_a,
                       const __grid_constant__ CUtensorMap tm_out,
                       const int32_t* __restrict__ seg_end, int M, int N, int K, int E, int tn,
-                      int tk, const __nv_bfloat16* __restrict__ d,
+                      int tk, int parts, const __nv_bfloat16* __restrict__ d,
                       __nv_bfloat16* __restrict__ d_bias, int* status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -426,11 +447,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     if (!leader) {
       // ---------------------------------------------- schedule (peer, whole warp)
-      int t = pair, grabbed = 0;  // the first tile is the pair's own
+      int t = pair;  // the first tile is the pair's own
       bool ok = true;
       for (int j = 0;; ++j) {
-        const WgTile st = wg_decode(t, sh, seg_end, M, per, tk);
-        if (!st.none() && lane == 0) grabbed = npairs + atomicAdd(gctr, 1);
+        WgTile st;
+        for (bool end = false;;) {
+          st = wg_decode<SPLIT>(t, sh, seg_end, M, per, tk, parts, E, end);
+          if (end) break;
+          int grabbed = 0;
+          if (lane == 0) grabbed = npairs + atomicAdd(gctr, 1);
+          t = __shfl_sync(0xffffffffu, grabbed, 0);
+          if (!st.none()) break;  // (a piece without rows is passed over)
+        }
         if (j >= AHEAD) {
           const int i = j - AHEAD;
           ok = wait_fast(&sh->staken[i % SCHED], (uint32_t)(i / SCHED) & 1u, abort_flag, status);
@@ -441,7 +469,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             map_to_rank(su32(&sh->sfull[j % SCHED]), lane), (uint32_t)st.e,
                             (uint32_t)st.lo, (uint32_t)st.hi, (uint32_t)(st.nt << 16 | st.kt));
         if (st.none()) break;
-        t = __shfl_sync(0xffffffffu, grabbed, 0);
       }
       if (lane == 0 && !*abort_flag) {
         __threadfence();  // this pair's last take before its done count
@@ -525,20 +552,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_ld32(tb + (uint32_t)c, r[0]);
         tmem_ld32(tb + (uint32_t)c + 32, r[1]);
         tmem_wait_ld();
-        if (lane == 0) bulk_wait_read<0>();  // the last store from this buffer
-        __syncwarp();
-        // row `lane` of the box, 16-byte chunk q at q ^ (lane & 7)
+        // boxes of 128-byte rows: 64 results, or twice 32 partial sums
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t* v = &r[q >> 2][(q & 3) * 8];
-          uint4 u;
-          u.x = pack2<F16>(__uint_as_float(v[0]), __uint_as_float(v[1]));
-          u.y = pack2<F16>(__uint_as_float(v[2]), __uint_as_float(v[3]));
-          u.z = pack2<F16>(__uint_as_float(v[4]), __uint_as_float(v[5]));
-          u.w = pack2<F16>(__uint_as_float(v[6]), __uint_as_float(v[7]));
-          *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) = u;
+        for (int h = 0; h < (SPLIT ? 2 : 1); ++h) {
+          if (SPLIT && st.k0() + c + 32 * h >= K) break;  // warp-uniform
+          if (lane == 0) bulk_wait_read<0>();  // the last store from this buffer
+          __syncwarp();
+          // row `lane` of the box, 16-byte chunk q at q ^ (lane & 7)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint4 u;
+            if constexpr (SPLIT) {
+              u = make_uint4(r[h][4 * q], r[h][4 * q + 1], r[h][4 * q + 2], r[h][4 * q + 3]);
+            } else {
+              const uint32_t* v = &r[q >> 2][(q & 3) * 8];
+              u.x = pack2<F16>(__uint_as_float(v[0]), __uint_as_float(v[1]));
+              u.y = pack2<F16>(__uint_as_float(v[2]), __uint_as_float(v[3]));
+              u.z = pack2<F16>(__uint_as_float(v[4]), __uint_as_float(v[5]));
+              u.w = pack2<F16>(__uint_as_float(v[6]), __uint_as_float(v[7]));
+            }
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) = u;
+          }
+          store(st, c + 32 * h, n);
         }
-        store(st, c, n);
       }
       // one arrival a warp: those of all 512 threads took their time one by one
       tc_fence_before();
@@ -546,25 +582,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) mbar_arrive_cluster_tmem(tempty_remote[acc]);
       if (++acc == 2) { acc = 0; aphase ^= 1u; }
     }
-    // the experts without rows: tile `in` of the i-th of them is pair
-    // (i * per + in) % npairs's
+    // the experts without rows: their tiles follow one another and go to the pairs in
+    // turn; `first` is the pair's next one in the expert at hand
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
     for (int i = lane; i < OUT_BYTES_WARP / 16; i += 32)
       reinterpret_cast<uint4*>(buf)[i] = make_uint4(0, 0, 0, 0);
-    long long before = 0;  // tiles of the empty experts before e
-    for (int w = 0; w * 32 < E; ++w) {
+    const int shift = per % npairs;
+    int first = pair;
+    for (int w = 0; !SPLIT && w * 32 < E; ++w) {  // (adding up the parts writes them too)
       uint32_t empty = ~sh->live[w];
       if (E - w * 32 < 32) empty &= (1u << (E - w * 32)) - 1u;
-      for (; empty; empty &= empty - 1u, before += per) {
+      for (; empty; empty &= empty - 1u) {
         WgTile st = {w * 32 + __ffs(empty) - 1, 0, 0, 0, 0};
-        for (int in = (int)((npairs + pair - before % npairs) % npairs); in < per; in += npairs) {
+        for (int in = first; in < per; in += npairs) {
           st.nt = in / tk;
           st.kt = in - st.nt * tk;
           const int n = st.n0() + 128 * (int)rank + 32 * quad;
           for (int c = 64 * grp; c < st.kw(K); c += 128)
             if (n < N && st.k0() + c < K) store(st, c, n);
         }
+        first -= shift;
+        if (first < 0) first += npairs;
       }
     }
     if (lane == 0) bulk_wait_all();  // every staged box written before the pair exits
@@ -583,6 +622,53 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 }  // namespace
 
+namespace {
+
+// d_w[e] = the sum of its parts' partial sums in order, rounded once; zeros for an
+// expert without rows.  Eight results a thread.
+template <bool F16>
+__global__ void __launch_bounds__(256)
+    wgrad_join_kernel(const float4* __restrict__ partial, const int32_t* __restrict__ seg_end,
+                      int M, long long per_expert, int E, int parts, uint4* __restrict__ d_w) {
+  pdl_wait();
+  const long long count = per_expert * E;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < count; i += gridDim.x * 256LL) {
+    int lo, hi;
+    seg_bounds(seg_end, (int)(i / per_expert), M, 0, lo, hi);
+    const int rows = part_rows(hi - lo, parts), n = hi > lo ? (hi - lo + rows - 1) / rows : 0;
+    float v[8] = {};
+#pragma unroll 4
+    for (int p = 0; p < n; ++p) {
+      const float4 a = __ldcs(partial + (p * count + i) * 2);
+      const float4 b = __ldcs(partial + (p * count + i) * 2 + 1);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+      v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    }
+    d_w[i] = make_uint4(pack2<F16>(v[0], v[1]), pack2<F16>(v[2], v[3]), pack2<F16>(v[4], v[5]),
+                        pack2<F16>(v[6], v[7]));
+  }
+}
+
+// Pieces that an expert's rows are cut into: as many as there are SM pairs for the
+// tiles of all experts, of 256 rows at least (on average), and one where that shortens a
+// tile by less than 1200 rows, since the partial sums and the second launch cost 3 us or
+// more: 2 experts of 6639 rows, 544 x 288, 17.7 us in 6 pieces, 38.5 in one; one of 8192,
+// 1024 x 1024, 22 in 4 and 46; but one of 1024, 13.1 in 4 and 12.3, and 4 of 1024, 512 x
+// 1024, 14.9 in 2 and 12.4.
+int wgrad_parts(int M, int N, int K, int E) {
+  const long long experts = std::max(1, std::min(E, M)), rows = M / experts;
+  const long long tiles = ((N + TN - 1LL) / TN) * ((K + TK - 1LL) / TK) * experts;
+  const long long parts = std::min<long long>(num_sms() / 2 / tiles, rows / 256);
+  return parts >= 2 && rows - rows / parts >= 1200 ? (int)parts : 1;
+}
+
+}  // namespace
+
+size_t gemm_wgrad_partial_bytes(int M, int N, int K, int E) {
+  const int parts = wgrad_parts(M, N, K, E);
+  return parts > 1 ? (size_t)parts * E * N * K * sizeof(float) : 0;
+}
+
 // a schedule entry has 16 bits for each coordinate of a tile
 bool gemm_wgrad_ok(int N, int K) {
   return N % 8 == 0 && K % 8 == 0 && N <= 0xffff * TN && K <= 0xffff * TK;
@@ -590,8 +676,10 @@ bool gemm_wgrad_ok(int N, int K) {
 
 cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_end, int M, int N,
                               int K, int E, bool f16, void* d_w, void* d_bias, int* status,
-                              cudaStream_t s) {
+                              float* partial, cudaStream_t s) {
   if (!gemm_wgrad_ok(N, K)) return cudaErrorInvalidValue;
+  int parts = wgrad_parts(M, N, K, E);
+  const bool split = parts > 1;
   CUtensorMap md, ma, mo;
   auto rows = [&](CUtensorMap* m, const void* p, int cols) {
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)M};
@@ -599,16 +687,20 @@ cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_e
     cuuint32_t box[2] = {64, BR};
     return tmap::encode_bf16(m, p, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, f16);
   };
-  cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)E};
-  cuuint64_t str[2] = {(cuuint64_t)K * 2, (cuuint64_t)N * K * 2};
-  cuuint32_t box[3] = {64, 32, 1};
+  const cuuint64_t size = split ? 4 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)E * parts};
+  cuuint64_t str[2] = {(cuuint64_t)K * size, (cuuint64_t)N * K * size};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / size), 32, 1};
   if (!rows(&md, d, N) || !rows(&ma, a, K) ||
-      !tmap::encode_bf16(&mo, d_w, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, f16))
+      !(split ? tmap::encode_f32(&mo, partial, 3, dims, str, box)
+              : tmap::encode_bf16(&mo, d_w, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, f16)))
     return cudaErrorInvalidValue;
   int tn = (N + TN - 1) / TN, tk = (K + TK - 1) / TK;
-  const int pairs = std::max(1, std::min(E * tn * tk, num_sms() / 2));
-  const void* kern =
-      f16 ? (const void*)gemm_wgrad_kernel<true> : (const void*)gemm_wgrad_kernel<false>;
+  const int pairs = std::max(1, std::min(E * tn * tk * parts, num_sms() / 2));
+  const void* kern = split ? (f16 ? (const void*)gemm_wgrad_kernel<true, true>
+                                  : (const void*)gemm_wgrad_kernel<false, true>)
+                           : (f16 ? (const void*)gemm_wgrad_kernel<true, false>
+                                  : (const void*)gemm_wgrad_kernel<false, false>);
   cudaError_t e = set_smem_limit(kern, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -627,8 +719,19 @@ cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_e
   cfg.numAttrs = 2;
   const __nv_bfloat16* d_p = static_cast<const __nv_bfloat16*>(d);
   __nv_bfloat16* bias_p = static_cast<__nv_bfloat16*>(d_bias);
-  void* args[] = {&md, &ma, &mo, &seg_end, &M, &N, &K, &E, &tn, &tk, &d_p, &bias_p, &status};
+  void* args[] = {&md, &ma,    &mo,  &seg_end, &M,     &N, &K, &E,
+                  &tn, &tk, &parts, &d_p,     &bias_p, &status};
   e = cudaLaunchKernelExC(&cfg, kern, args);
+  count_launch();
+  if (e != cudaSuccess || !split) return e;
+  const long long per_expert = (long long)N * K / 8, count = per_expert * E;
+  auto join = [&](auto k) {
+    const long long cap = (long long)num_sms() * resident_ctas((const void*)k, 256);
+    return launch_pdl(k, dim3((unsigned)std::min((count + 255) / 256, cap)), dim3(256), 0, s,
+                      reinterpret_cast<const float4*>(partial), seg_end, M, per_expert, E, parts,
+                      static_cast<uint4*>(d_w));
+  };
+  e = f16 ? join(wgrad_join_kernel<true>) : join(wgrad_join_kernel<false>);
   count_launch();
   return e;
 }

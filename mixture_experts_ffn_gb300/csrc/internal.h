@@ -254,11 +254,13 @@ cudaError_t launch_dgrad_simt(const void* d, const void* w, const int32_t* seg_e
 cudaError_t launch_wgrad_simt(const void* d, const void* a, const int32_t* seg_end, int M, int N,
                               int K, int E, moe_dtype dt, void* d_w, cudaStream_t s);
 // tcgen05 gradients of 16-bit weights and bias (d_bias may be null; gemm_wgrad.cu);
-// M >= 1, all 16-byte aligned, extents for which gemm_wgrad_ok
+// M >= 1, all 16-byte aligned, extents for which gemm_wgrad_ok; partial holds
+// gemm_wgrad_partial_bytes (none where an expert's rows are not cut into parts)
 bool gemm_wgrad_ok(int N, int K);
+size_t gemm_wgrad_partial_bytes(int M, int N, int K, int E);
 cudaError_t launch_gemm_wgrad(const void* d, const void* a, const int32_t* seg_end, int M, int N,
                               int K, int E, bool f16, void* d_w, void* d_bias, int* status,
-                              cudaStream_t s);
+                              float* partial, cudaStream_t s);
 cudaError_t launch_bias_grad(const void* d, const int32_t* seg_end, int M, int N, int E,
                              moe_dtype dt, void* d_bias, cudaStream_t s);
 cudaError_t launch_route_backward(const void* logits, const int32_t* ids, const float* d_w, int T,

@@ -412,6 +412,34 @@ def test_wgrad_many_tiles(moe, counts, N, K, dtype):
     assert moe.moe_sync_status(ws) == moe.MOE_OK and (ws[:256] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES[:2])
+@pytest.mark.parametrize("counts", [[2600], [7000, 0, 901], [5000, 3], [0, 1, 9000, 0],
+                                    [4097, 2047]])
+@pytest.mark.parametrize("N,K", [(8, 8), (72, 200), (256, 264), (264, 136), (520, 40)])
+def test_wgrad_in_parts(moe, counts, N, K, dtype):
+    """Few tiles and many rows: the rows in parts, added up in order.  Experts without rows, with
+    fewer than a part, and with NaN next door; every element written."""
+    g = gen(sum(counts) + N * K)
+    M, E = sum(counts) + 5, len(counts)
+    seg = segments(counts)
+    need = moe.moe_grouped_gemm_wgrad_workspace_size(M, N, K, E)
+    assert need > moe.MOE_STATUS_BYTES
+    d, a = randn(g, M, N, dtype=dtype, std=0.1), randn(g, M, K, dtype=dtype)
+    d[M - 5:], a[M - 5:] = float("nan"), float("inf")
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    ws[moe.MOE_STATUS_BYTES:] = 255  # partial sums that no part writes are NaN
+    dw = torch.full((E, N, K), float("nan"), dtype=dtype, device="cuda")
+    db = torch.full((E, N), float("nan"), dtype=dtype, device="cuda")
+    moe.moe_grouped_gemm_wgrad(d, a, seg, bias=db, d_w=dw, ws=ws)
+    rw, sw, rb, sb = R.wgrad(d, a, seg)
+    R.close(dw, rw, sw, "d_w")
+    R.close(db, rb, sb, "d_bias")
+    assert moe.moe_sync_status(ws) == moe.MOE_OK and (ws[:moe.MOE_STATUS_BYTES] == 0).all()
+    assert torch.equal(moe.moe_grouped_gemm_wgrad(d, a, seg, ws=ws)[0], dw)
+    with pytest.raises(moe.MoEError):
+        moe.moe_grouped_gemm_wgrad(d, a, seg, ws=ws[:need - 256])
+
+
 def test_wgrad_on_two_streams(moe):
     """Calls that run at the same time, with workspaces of their own."""
     g = gen(20)
