@@ -109,13 +109,16 @@ def act_backward(p, d, kind, inter=False, limit=0.0, alpha=1.0, beta=0.0, fast=F
 
     These are relative and hold for normal numbers only.  A factor (sigmoid, Phi, a product
     of two factors) below 2^-126 is a multiple of 2^-149, off by a few of these (erfc's four
-    units in the last place, and one rounding a product: 2^-146), or is zero where the fast
-    quotient gives zero for results below 2^-126 (off by 2^-126); the other factors, at most
+    units in the last place, and one rounding a product: 2^-146).  The fast quotient gives
+    zero for results below 2^-126, and the exact sigmoid 1 / (1 + exp(-x)) below 2^-128, where
+    the exponential overflows: off by 2^-126 at most.  The other factors, at most
     (1 + |d|) (1 + |g|) (1 + |u|), multiply that."""
     p, d = p.double(), d.double()
     g, u = split(p, kind, inter)
     one = torch.ones_like(g)
-    low = (2.0 ** -125 if fast else 2.0 ** -146) * (1 + g.abs()) * (1 + (0 if u is None else u.abs()))
+    sigmoid = kind in ("silu", "silu1", "swiglu")
+    low = 2.0 ** -125 if fast or sigmoid else 2.0 ** -146
+    low = low * (1 + g.abs()) * (1 + (0 if u is None else u.abs()))
     low_d = low * (1 + d.abs())
     a = act_forward(p, kind, inter, limit, alpha, beta)
     if kind == "identity":
@@ -128,7 +131,8 @@ def act_backward(p, d, kind, inter=False, limit=0.0, alpha=1.0, beta=0.0, fast=F
         # the exponent and erfc's argument are rounded: a relative 2 u g^2 of pdf, g pdf u of cdf
         dc = 8 * U * c + 4 * U * g.abs() * f
         df = f * (8 + 2 * g * g) * U
-        if fast:  # exp(-x^2 / 2) to (2 + 1.2 x^2 / 2) 2^-23, its cofactor of the lower tail to 2^-19
+        # fast: exp(-x^2 / 2) to (2 + 1.2 x^2 / 2) 2^-23, its cofactor of the lower tail to 2^-19
+        if fast:
             df = df + f * (2 + 0.6 * g * g) * 2 * U
             tail = torch.minimum(c, cdf(-g))
             dc = tail * (2.0 ** -19 + (2 + 0.6 * g * g) * 2 * U + (12 + g * g) * U) + U
@@ -207,7 +211,7 @@ def route_weights(z, ids, scoring, renorm, rsf):
     elif scoring == "sigmoid":
         s = torch.sigmoid(z)
     else:
-        s = torch.sqrt(torch.clamp(z, min=0) + torch.log1p(torch.exp(-z.abs())))
+        s = torch.sqrt(torch.nn.functional.softplus(z, threshold=700.0))  # (smooth at zero)
     ok = (ids >= 0) & (ids < z.shape[1])
     s = torch.where(ok, s.gather(1, torch.where(ok, ids, 0).long()), 0.0)
     return rsf * (s / s.sum(1, keepdim=True) if renorm else s)
