@@ -44,12 +44,15 @@
 // the rows are cut into `parts` equal pieces, each a tile of its own whose float32 sums
 // go to the workspace, and a second launch adds them up in order (wgrad_parts).
 //
-// What bounds it: at 1024 rows an expert a stage takes 600 of the 512 cycles that its
-// MMAs need even without copies and stores, and 700 with them: 32 KB a stage into
-// each SM is most of what L2 delivers.  The ring's depth counts for that reason (4
-// stages 1328 us, 5 stages 1204, 6 stages 1165, uneven experts), more than a second
-// buffer for the stores (with 5 stages: 1223).  At 32 rows an expert writing d_w does
-// (5.9 TB/s).
+// What bounds it: with many rows an expert a stage takes 590 to 620 cycles for MMAs of
+// 512, with or without the copies: shared memory carries 32 KB in and 48 KB out to the
+// MMAs, 640 cycles at 128 bytes each.  (The issuing lane itself waits 98 cycles a stage
+// and issues for 342; one elected lane of a converged warp issues in 251, waits longer,
+// and the whole gains 1% or nothing.  Stages of 32 rows take it 600 cycles as well: 252
+// us instead of 149 on 8 experts of 1024 rows, 7168 x 2048.)  The ring's depth counts,
+// since 32 KB a stage into each SM is most of what L2 delivers (4 stages 1328 us, 5
+// stages 1204, 6 stages 1165, 64 uneven experts), more than a second buffer for the
+// stores (with 5 stages: 1223).  At 32 rows an expert writing d_w bounds (6 TB/s).
 #include <cuda.h>
 
 #include <algorithm>
