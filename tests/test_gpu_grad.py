@@ -599,6 +599,51 @@ def test_route_backward_masked_and_far_logits(moe, scoring, renorm):
     assert torch.isnan(out2[2, 0]) and torch.equal(out2[3:], out[3:]) and torch.equal(out2[:2], out[:2])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid", "sqrt_softplus"])
+def test_route_backward_far_choices(moe, scoring, dtype):
+    """Every chosen logit so low that its float32 score is zero: the weights' ratios remain.
+    Chosen experts masked with -inf weigh nothing, and a choice of these alone has no gradient."""
+    g = gen(13)
+    E, K, low, inf = 16, 4, torch.finfo(dtype).min, float("-inf")
+    rows = [(-100, -100, -100, -100), (-100, -120, -95, -110), (low,) * 4, (low, low, inf, inf),
+            (inf,) * 4, (inf, -96, inf, inf)]
+    T = len(rows)
+    z = randn(g, T, E, dtype=dtype)
+    z[:, :K] = torch.tensor(rows, device="cuda")
+    ids = torch.arange(K, dtype=torch.int32, device="cuda").repeat(T, 1)
+    dw = randn(g, T, K)
+    p = moe.route_params(K, scoring, True, routed_scaling_factor=2.5)
+    out = moe.moe_route_backward(z, ids, dw, p)
+    ref, slack = R.route_backward(z[:2], ids[:2], dw[:2], scoring, True, 2.5)
+    R.close(out[:2], ref, slack, "far")
+    # equal scores: weights of 1/4 and 1/2, exact; dlog score / dz is 1, of sqrt_softplus 1/2
+    l = 0.5 if scoring == "sqrt_softplus" else 1.0
+    for t, n in ((2, 4), (3, 2)):
+        h = dw[t, :n].double()
+        want = torch.zeros(E, dtype=torch.float64, device="cuda")
+        want[:n] = 2.5 / n * l * (h - h.mean())
+        mag = torch.zeros_like(want)
+        mag[:n] = 2.5 / n * l * (h.abs() + h.abs().mean())
+        # three additions of the sum, the difference and three products, of R.U each
+        R.close(out[t], want, 8 * R.U * mag, ("lowest", n))
+    assert (out[4:] == 0).all()
+    # a NaN among the masks is kept
+    z[4, 1] = float("nan")
+    assert torch.isnan(moe.moe_route_backward(z, ids, dw, p)[4, :K]).all()
+
+
+@pytest.mark.parametrize("z", [0.5, -30.0, -100.0, -1e30, float("-inf")])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid", "sqrt_softplus"])
+def test_route_backward_single_weight(moe, scoring, z):
+    """One renormalised weight is 1 whatever its logit."""
+    logits = torch.full((3, 8), z, device="cuda")
+    ids = torch.tensor([[0], [7], [3]], dtype=torch.int32, device="cuda")
+    out = moe.moe_route_backward(logits, ids, torch.full((3, 1), 1.7, device="cuda"),
+                                 moe.route_params(1, scoring, True))
+    assert (out == 0).all()
+
+
 def test_route_against_differences(moe):
     g = gen(10)
     T, E, K = 4, 9, 3
