@@ -751,7 +751,8 @@ size_t moe_grouped_gemm_wgrad_workspace_size(int M, int N, int K, int E);
  *   part in a sum.  An id outside [0, E) takes no part.
  * Renormalised weights are ratios of the chosen scores, also where these are so far
  * down that each is zero in float32 (and moe_route's weights are 0 / 0); a chosen
- * logit of -inf weighs nothing, and where every one is -inf the gradient is zero. */
+ * logit of -inf weighs nothing, and where every one is -inf the gradient is zero.
+ * So is that of a softmax without renormalisation whose E logits are all -inf. */
 moe_status moe_route_backward(const void* logits, const int32_t* topk_ids,
                               const float* d_topk_weights, int T, int E,
                               const moe_route_params* p, void* d_logits, cudaStream_t stream);

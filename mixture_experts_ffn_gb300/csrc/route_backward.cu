@@ -171,12 +171,13 @@ __global__ void __launch_bounds__(kThreads)
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      z[i] = lane + 32 * i < E ? expf(z[i] - m) : 0.f;
+      z[i] = z[i] != -INFINITY ? expf(z[i] - m) : 0.f;  // (past E, or masked)
       sum += z[i];
     }
     sum = warp_sum(sum);
+    if (sum == 0.f) sum = 1.f;  // every expert is masked: weights and gradients of zero
 #pragma unroll
-    for (int q = 0; q < 2; ++q) s[q] = id[q] >= 0 ? expf(s[q] - m) / sum : 0.f;
+    for (int q = 0; q < 2; ++q) s[q] = s[q] != -INFINITY ? expf(s[q] - m) / sum : 0.f;
     const float mean = warp_sum(g[0] * s[0] + g[1] * s[1]);  // sum_k g_k s_k
     float v[2];
     same_id_sums(id, g, K, v);

@@ -644,6 +644,24 @@ def test_route_backward_single_weight(moe, scoring, z):
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("E", [5, 200, 600, 1000])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_route_backward_softmax_without_a_logit(moe, E, dtype):
+    """Softmax weights as they are: a row whose mask leaves no expert has a zero gradient, its
+    neighbours theirs; a NaN makes its row NaN."""
+    g = gen(E)
+    K = 3
+    z, dw = randn(g, 4, E, dtype=dtype), randn(g, 4, K)
+    ids = torch.arange(K, dtype=torch.int32, device="cuda").repeat(4, 1)
+    p = moe.route_params(K, "softmax", False)
+    ref = moe.moe_route_backward(z, ids, dw, p)
+    z[1], z[2] = float("-inf"), float("-inf")
+    z[2, E - 1] = float("nan")
+    out = moe.moe_route_backward(z, ids, dw, p)
+    assert (out[1] == 0).all() and torch.isnan(out[2]).all()
+    assert torch.equal(out[::3], ref[::3])
+
+
 def test_route_against_differences(moe):
     g = gen(10)
     T, E, K = 4, 9, 3
