@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kThreads)
     sum = warp_sum(sum);
     if (sum == 0.f) sum = 1.f;  // every expert is masked: weights and gradients of zero
 #pragma unroll
-    for (int q = 0; q < 2; ++q) s[q] = s[q] != -INFINITY ? expf(s[q] - m) / sum : 0.f;
+    for (int q = 0; q < 2; ++q)  // (divided also where masked: a NaN of the row is kept)
+      s[q] = (s[q] != -INFINITY ? expf(s[q] - m) : 0.f) / sum;
     const float mean = warp_sum(g[0] * s[0] + g[1] * s[1]);  // sum_k g_k s_k
     float v[2];
     same_id_sums(id, g, K, v);
