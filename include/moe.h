@@ -729,7 +729,8 @@ moe_status moe_act_backward(const void* p, const void* scales, const void* d_out
  *          over the rows m of expert e; zeros for an expert without rows
  *   d_out [M, N] dtype;  a, d_a [M, K] dtype;  w, d_w [E, N, K] dtype;
  *   d_bias [E, N] dtype or NULL;  seg_end [E] i32 as moe_grouped_gemm_act;
- *   ws >= MOE_STATUS_BYTES bytes (dgrad), moe_grouped_gemm_wgrad_workspace_size (wgrad).
+ *   ws >= MOE_STATUS_BYTES bytes (dgrad; wgrad in float32 FMA),
+ *   moe_grouped_gemm_wgrad_workspace_size (wgrad on the tensor cores).
  * Rows past seg_end[E-1] have no part in the results and are not written.  Every
  * element of d_w and d_bias is written.  16-bit operands run on the tensor cores when N % 8 == 0,
  * K % 8 == 0 and the operands and results are 16-byte aligned; float32 and other

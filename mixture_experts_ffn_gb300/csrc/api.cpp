@@ -1249,7 +1249,7 @@ moe_status moe_grouped_gemm_dgrad(const void* d_out, const void* w, const int32_
 
 size_t moe_grouped_gemm_wgrad_workspace_size(int M, int N, int K, int E) {
   if (!mx_gemm_extent_ok(M, N, K, E)) return 0;
-  return MOE_STATUS_BYTES + gemm_wgrad_partial_bytes(M, N, K, E);
+  return MOE_STATUS_BYTES + (gemm_wgrad_ok(N, K) ? gemm_wgrad_partial_bytes(M, N, K, E) : 0);
 }
 
 moe_status moe_grouped_gemm_wgrad(const void* d_out, const void* a, const int32_t* seg_end, int M,
@@ -1260,13 +1260,13 @@ moe_status moe_grouped_gemm_wgrad(const void* d_out, const void* a, const int32_
   if (!seg_end || !d_w || (M > 0 && (!d_out || !a))) return MOE_ERR_INVALID_ARG;
   for (const void* ptr : {d_out, a, (const void*)d_w, (const void*)d_bias})
     if (!aligned(ptr, esz)) return MOE_ERR_INVALID_ARG;
-  const size_t need = moe_grouped_gemm_wgrad_workspace_size(M, N, K, E);
+  const bool tc = dtype != MOE_F32 && num_sms() >= 2 && M > 0 &&
+                  tc_ok(d_out, a, d_w, N, K, M) && gemm_wgrad_ok(N, K);
+  const size_t need = MOE_STATUS_BYTES + (tc ? gemm_wgrad_partial_bytes(M, N, K, E) : 0);
   if (!ws_ok(ws, ws_bytes, need)) return MOE_ERR_WORKSPACE;
   Span outs[] = {{d_w, (size_t)E * N * K * esz}, {d_bias, (size_t)E * N * esz}, {ws, need}};
   Span ins[] = {{d_out, (size_t)M * N * esz}, {a, (size_t)M * K * esz}, {seg_end, (size_t)E * 4}};
   if (any_overlap(outs, ins)) return MOE_ERR_OVERLAP;
-  const bool tc = dtype != MOE_F32 && num_sms() >= 2 && M > 0 &&
-                  tc_ok(d_out, a, d_w, N, K, M) && gemm_wgrad_ok(N, K);
   const bool with_bias = tc && aligned16(d_bias);  // the bias' sums beside the products
   if (d_bias && !with_bias) {
     const cudaError_t e = launch_bias_grad(d_out, seg_end, M, N, E, dtype, d_bias, stream);

@@ -999,8 +999,9 @@ def moe_grouped_gemm_wgrad(d_out, a, seg_end, bias=False, d_w=True, ws=None):
         raise ValueError("d_out is [M, N], a [M, K] and seg_end [E]")
     d_w = _made(d_w, (E, N, K), dtype, d_out, "d_w")
     d_bias = _asked(bias, (E, N), dtype, d_out, "bias")
-    if ws is None:
-        ws = _ws(lib.moe_grouped_gemm_wgrad_workspace_size(M, N, K, E), d_out.device)
+    if ws is None:  # (float32 sums have no parts)
+        ws = _ws(MOE_STATUS_BYTES if dtype is torch.float32 else
+                 lib.moe_grouped_gemm_wgrad_workspace_size(M, N, K, E), d_out.device)
     _check("moe_grouped_gemm_wgrad",
            lib.moe_grouped_gemm_wgrad(d_out.data_ptr(), a.data_ptr(), seg_end.data_ptr(), M, N, K,
                                       E, _dtype(dtype), d_w.data_ptr(), _ptr(d_bias),

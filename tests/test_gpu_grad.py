@@ -440,6 +440,27 @@ def test_wgrad_in_parts(moe, counts, N, K, dtype):
         moe.moe_grouped_gemm_wgrad(d, a, seg, ws=ws[:need - 256])
 
 
+@pytest.mark.parametrize("dtype,N,K,off", [(torch.float32, 40, 64, 0), (torch.float32, 7, 33, 0),
+                                           (torch.bfloat16, 42, 64, 0), (torch.float16, 40, 64, 1)])
+def test_wgrad_in_the_status_bytes(moe, dtype, N, K, off):
+    """Sums in float32 FMA over an expert of many rows take a workspace of the status alone."""
+    g = gen(17)
+    M, seg = 5000, segments([5000])
+    d = randn(g, M * N + off, dtype=dtype)[off:].view(M, N)
+    a = randn(g, M, K, dtype=dtype)
+    ws = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    ws[moe.MOE_STATUS_BYTES:] = 77
+    dw, db = moe.moe_grouped_gemm_wgrad(d, a, seg, bias=True, ws=ws[:moe.MOE_STATUS_BYTES])
+    rw, sw, rb, sb = R.wgrad(d, a, seg)
+    R.close(dw, rw, sw)
+    R.close(db, rb, sb)
+    assert (ws[moe.MOE_STATUS_BYTES:] == 77).all()
+    with pytest.raises(moe.MoEError):
+        moe.moe_grouped_gemm_wgrad(randn(g, M, 40, dtype=torch.bfloat16),
+                                   randn(g, M, 64, dtype=torch.bfloat16), seg,
+                                   ws=ws[:moe.MOE_STATUS_BYTES])
+
+
 def test_wgrad_on_two_streams(moe):
     """Calls that run at the same time, with workspaces of their own."""
     g = gen(20)

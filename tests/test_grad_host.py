@@ -130,6 +130,25 @@ def test_route_backward_refuses(lib):
         assert call(**kw) == OVERLAP, kw
 
 
+@nogpu
+def test_wgrad_takes_the_space_it_uses(lib):
+    """One expert of many rows: the tensor-core kernel sums in parts and needs room for these,
+    the float32 FMA one (float32, other widths, unaligned operands) the status alone."""
+    M, N, K = 16384, 512, 512
+    size = lib.moe_grouped_gemm_wgrad_workspace_size
+    need = size(M, N, K, 1)
+    assert need > 256 and size(M, N + 1, K, 1) == 256 and size(M, N, K - 4, 1) == 256
+
+    def call(d=A(0), a=A(1), N=N, K=K, dt=BF, n=256, dw=A(3)):  # dw == ws: never launched
+        return lib.moe_grouped_gemm_wgrad(d, a, A(2), M, N, K, 1, dt, dw, None, A(3), n, None)
+
+    assert call() == SPACE and call(n=need - 1) == SPACE and call(n=need) == OVERLAP
+    for kw in (dict(dt=F32), dict(N=N + 1), dict(K=K - 4), dict(d=A(0, 2)), dict(a=A(1, 8)),
+               dict(dw=A(3, 2))):
+        assert call(**kw) == OVERLAP, kw
+        assert call(**kw, n=255) == SPACE, kw
+
+
 # ------------------------------------------------------------------ the binding
 class Recorder:
     def __init__(self):
@@ -236,6 +255,15 @@ def test_binding_refuses_another_device(moe, name, monkeypatch):
     f, kw, _ = calls(moe)[name]
     monkeypatch.setattr(moe, "_is_current", lambda device: False)
     refused(moe, f, kw, "current device")
+
+
+def test_binding_asks_for_parts_where_they_are_used(moe):
+    f, kw, _ = calls(moe)["wgrad"]
+    f(**{**kw, "d_out": f32(M, N), "a": f32(M, H)})
+    assert moe.recorder.calls == ["moe_grouped_gemm_wgrad"]
+    f(**kw)
+    assert moe.recorder.calls[1:] == ["moe_grouped_gemm_wgrad_workspace_size",
+                                      "moe_grouped_gemm_wgrad"]
 
 
 def test_binding_refuses_other_mistakes(moe):
