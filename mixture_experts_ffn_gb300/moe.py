@@ -238,7 +238,7 @@ def _together(first, *ts):
 
 def _asked(out, shape: tuple, dtype: torch.dtype, like, what: str, twin=None):
     """An output argument: True makes one (like twin, an input of this shape and type, where
-    there is one: a fifth less time), False is none, a tensor is checked."""
+    there is one: a fifth less time), False or None is none, a tensor is checked."""
     if out is True:
         return torch.empty(shape, dtype=dtype, device=like.device) if twin is None else \
             torch.empty_like(twin)
@@ -850,7 +850,7 @@ def moe_ffn_forward_mx(hidden, hidden_scale, logits, w_gate_up, w_gate_up_scale,
 def moe_combine_backward(d_out, expert_out, topk_weights, route_to_row, scale=1.0,
                          d_expert_out=True, d_topk_weights=True):
     """Gradient of moe_combine: (d_expert_out [T * K, H], d_topk_weights [T, K] float32).
-    Either is True (made), False (left out, None; expert_out may then be None for the
+    Either is True (made), False or None (left out; expert_out may then be None for the
     weights') or the tensor to write.  topk_weights [T, K]."""
     lib = load_library()
     _together(d_out, expert_out, topk_weights, route_to_row)
@@ -864,7 +864,7 @@ def moe_combine_backward(d_out, expert_out, topk_weights, route_to_row, scale=1.
     if Tw != T or K == 0 or route_to_row.numel() != M or \
             (expert_out is not None and expert_out.shape != (M, H)):
         raise ValueError("topk_weights is [T, K], route_to_row [T * K], expert_out [T * K, H]")
-    if expert_out is None and d_topk_weights is not False:
+    if expert_out is None and not (d_topk_weights is False or d_topk_weights is None):
         raise ValueError("the weights' gradient takes expert_out")
     d_expert_out = _asked(d_expert_out, (M, H), dtype, d_out, "d_expert_out", expert_out)
     d_topk_weights = _asked(d_topk_weights, (T, K), torch.float32, d_out, "d_topk_weights",

@@ -257,6 +257,23 @@ def test_binding_refuses_another_device(moe, name, monkeypatch):
     refused(moe, f, kw, "current device")
 
 
+@pytest.mark.parametrize("none", [False, None])
+def test_outputs_left_out(moe, none):
+    """False and None leave an output out; the weights' gradient left out takes no expert_out."""
+    c = calls(moe)
+    f, kw, _ = c["combine"]
+    d_y, d_w = f(**{**kw, "expert_out": None}, d_topk_weights=none)
+    assert d_w is None and d_y.shape == (M, H)
+    d_y, d_w = f(**kw, d_expert_out=none)
+    assert d_y is None and d_w.shape == (T, K)
+    f, kw, _ = c["checkpoint"]
+    assert f(**kw, out=none)[0] is None
+    f, kw, _ = c["act"]
+    assert f(**kw, out=none)[1] is None
+    f, kw, _ = c["wgrad"]
+    assert f(**kw, bias=none)[1] is None
+
+
 def test_binding_asks_for_parts_where_they_are_used(moe):
     f, kw, _ = calls(moe)["wgrad"]
     f(**{**kw, "d_out": f32(M, N), "a": f32(M, H)})
