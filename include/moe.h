@@ -715,7 +715,9 @@ moe_status moe_act_checkpoint(const void* p, const int32_t* seg_end, int M, int 
  * given: p holds e4m3 codes) or as it was (scales NULL: p [M, N1] dtype):
  *   d_p[m] = d_out[m] * act'(p[m]);  out[m] = act(p[m])
  * A clamp passes the gradient up to and at its bound and stops it past it; relu
- * passes it for p > 0.  A NaN of p gives NaN.
+ * passes it for p > 0.  A NaN of p is a NaN of out, and of d_p where the derivative
+ * takes its value: not in identity's, not in that of the up value by itself, not
+ * past a clamp.  In the checkpoint it makes its 32 columns NaN.
  *   d_out [M, F] dtype;  d_p [M, N1] dtype out;  out [M, F] dtype or NULL;
  *   p, scales, seg_end, alignment and extents as moe_act_checkpoint. */
 moe_status moe_act_backward(const void* p, const void* scales, const void* d_out,

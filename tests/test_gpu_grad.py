@@ -280,6 +280,35 @@ def test_act_keeps_nan_in_its_block(moe, kind, inter, F, dtype):
     assert torch.isfinite(dp[0]).all() and torch.isfinite(dp[3]).all()
 
 
+@pytest.mark.parametrize("kind,inter", ACTS)
+@pytest.mark.parametrize("F", [31, 64])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_act_nan_of_the_argument(moe, kind, inter, F, dtype):
+    """Without a checkpoint a NaN reaches what the formula takes it for: the activation always,
+    the gradients of a gate or a single value but identity's, of a NaN up value the gate's alone
+    and not past the gate's clamp."""
+    g = gen(15)
+    gated = kind in GATED
+    p, d = randn(g, 4, 2 * F if gated else F, dtype=dtype), randn(g, 4, F, dtype=dtype)
+    at, up = (2 * 5, 2 * 5 + 1) if inter else (5, F + 5)
+    nan = float("nan")
+    p[1, at] = nan
+    if gated:
+        p[2, up], p[3, up] = nan, nan
+        p[3, at] = 9.0  # past SwiGLU's clamp of 7
+    dp, out = moe.moe_act_backward(p, d, act_params(moe, kind, inter))
+    want_out = torch.zeros((4, F), dtype=torch.bool, device="cuda")
+    want = torch.zeros(p.shape, dtype=torch.bool, device="cuda")
+    want_out[1, 5], want[1, at] = True, kind != "identity"
+    if gated:
+        want_out[2:, 5], want[1, up], want[2, at] = True, True, True
+        want[3, at] = kind != "swiglu"
+        if kind == "swiglu":
+            assert dp[3, at] == 0
+    assert torch.equal(torch.isnan(out), want_out)
+    assert torch.equal(torch.isnan(dp), want)
+
+
 @pytest.mark.parametrize("F", [20, 64])
 @pytest.mark.parametrize("end,live", [(3, 3), (0, 0), (-4, 0), (99, 8)])
 def test_act_rows_behind_the_last_segment(moe, F, end, live):
