@@ -37,8 +37,9 @@
 // 2048, 64 experts) 1148 instead of 1139; by the producer itself, which held up the
 // copies, 1200.  An expert without rows has no tiles; the epilogue warps write its
 // zeros at the end (found by words of 32 experts; a step an expert cost 2 of the 89 us
-// and 9 of the 207).  Every wait is bounded (2 s); on a timeout the block latches the
-// timeout bit, drains what it issued and frees TMEM.
+// and 9 of the 207).  Every wait is bounded (2 s; the clearing warp's for its next job,
+// which the producer always ends, 64 s); on a timeout the block latches the timeout bit,
+// drains what it issued and frees TMEM.
 //
 // Few tiles (SPLIT): where experts have many rows and their tiles leave SM pairs idle,
 // the rows are cut into `parts` equal pieces, each a tile of its own whose float32 sums
@@ -658,11 +659,15 @@ __global__ void __launch_bounds__(256)
 // more: 2 experts of 6639 rows, 544 x 288, 17.7 us in 6 pieces, 38.5 in one; one of 8192,
 // 1024 x 1024, 22 in 4 and 46; but one of 1024, 13.1 in 4 and 12.3, and 4 of 1024, 512 x
 // 1024, 14.9 in 2 and 12.4.
+// One expert may have nearly all of the rows, whatever their average: a piece is cut to
+// 2^26 of them at most, a million stages of 0.3 us, since the drain waits for a piece's
+// sum and a wait ends after 2 s (2^30 rows in one piece would take 5).
 int wgrad_parts(int M, int N, int K, int E) {
+  const int least = (int)std::max(1LL, ((M - 1LL) >> 26) + 1);
   const long long experts = std::max(1, std::min(E, M)), rows = M / experts;
   const long long tiles = ((N + TN - 1LL) / TN) * ((K + TK - 1LL) / TK) * experts;
   const long long parts = std::min<long long>(num_sms() / 2 / tiles, rows / 256);
-  return parts >= 2 && rows - rows / parts >= 1200 ? (int)parts : 1;
+  return std::max(parts >= 2 && rows - rows / parts >= 1200 ? (int)parts : 1, least);
 }
 
 }  // namespace

@@ -469,6 +469,25 @@ def test_wgrad_in_parts(moe, counts, N, K, dtype):
         moe.moe_grouped_gemm_wgrad(d, a, seg, ws=ws[:need - 256])
 
 
+def test_wgrad_of_one_among_many(moe):
+    """All of more than 2^26 rows on one of 100 experts: cut by the rows themselves, where the
+    average would not be.  Whole numbers whose sums float32 holds: exact but for the rounding."""
+    M, N, K, E = (1 << 26) + 12345, 8, 8, 100
+    g = gen(23)
+    d, a = (torch.randint(-1, 2, (M, N), generator=g, device="cuda", dtype=torch.int8
+                          ).to(torch.bfloat16) for _ in range(2))
+    counts = [0] * E
+    counts[41], counts[77] = M - 3, 3
+    dw, _ = moe.moe_grouped_gemm_wgrad(d, a, segments(counts))
+    ref = torch.zeros((E, N, K), dtype=torch.float64, device="cuda")
+    for lo in range(0, M - 3, 1 << 22):
+        x, y = (t[lo:min(lo + (1 << 22), M - 3)].float() for t in (d, a))
+        ref[41] += (x.t() @ y).double()  # partial sums below 2^22: exact
+    ref[77] = d[-3:].double().t() @ a[-3:].double()
+    assert ref.abs().max() < 2 ** 24
+    assert torch.equal(dw, ref.to(torch.bfloat16))
+
+
 @pytest.mark.parametrize("dtype,N,K,off", [(torch.float32, 40, 64, 0), (torch.float32, 7, 33, 0),
                                            (torch.bfloat16, 42, 64, 0), (torch.float16, 40, 64, 1)])
 def test_wgrad_in_the_status_bytes(moe, dtype, N, K, off):

@@ -149,6 +149,18 @@ def test_wgrad_takes_the_space_it_uses(lib):
         assert call(**kw, n=255) == SPACE, kw
 
 
+@nogpu
+def test_wgrad_cuts_rows_without_end(lib):
+    """An expert may have all of the rows, however many experts there are: past 2^26 rows there
+    are parts, one for each 2^26, so that no tile takes as long as the kernel waits for it."""
+    def parts(m, n=8, k=8, e=1024):
+        return (lib.moe_grouped_gemm_wgrad_workspace_size(m, n, k, e) - 256) // (4 * e * n * k)
+
+    assert parts(1 << 26) == 0
+    assert parts((1 << 26) + 1) == 2 and parts(1 << 28) == 4 and parts((1 << 30) - 1) == 16
+    assert parts((1 << 30) - 1, e=1) > 16
+
+
 # ------------------------------------------------------------------ the binding
 class Recorder:
     def __init__(self):
