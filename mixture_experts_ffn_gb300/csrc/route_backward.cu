@@ -31,22 +31,19 @@ __device__ __forceinline__ void store_any(void* p, size_t i, int dt, float v) {
   else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
-// The score s of z times a factor that all of a token's weights share (1 for c = 0;
-// exp(-c), for sqrt_softplus exp(-c / 2)), and its log-derivative l = dlog s / dz, both
-// from exponentials of -|z| or of differences:
+// log of the score's square for sqrt_softplus and of the score for sigmoid are
+// never taken: both scores and their log-derivatives come from e = exp(-|z|).
 //   sigmoid:        s = 1 / (1 + exp(-z)),          l = sigmoid(-z)
 //   sqrt_softplus:  s = sqrt(max(z, 0) + log1p(e)), l = sigmoid(z) / (2 s^2);
 // below z = -80 softplus(z) and sigmoid(z) are both exp(z) to the last bit, so
-// l = 1/2 (and exp(z) may underflow).  c, at most 0, is the highest chosen logit where
-// that is negative: the largest of the scaled scores is then 1/2 at least, however far
-// down it lies (a score itself underflows from -89, and -207, on: 0 / 0).
-__device__ __forceinline__ void score_of(int scoring, float z, float c, float& s, float& l) {
+// l = 1/2 (and exp(z) may underflow).
+__device__ __forceinline__ void score_of(int scoring, float z, float& s, float& l) {
   if (scoring == MOE_SCORING_SIGMOID) {
-    s = 1.f / (expf(c) + expf(c - z));
+    s = sigmoidf_(z);
     l = sigmoidf_(-z);
   } else {
     const float sp = fmaxf(z, 0.f) + log1pf(expf(-fabsf(z)));
-    s = z < -80.f ? expf(0.5f * (z - c)) : sqrtf(sp) * expf(-0.5f * c);
+    s = z < -80.f ? expf(0.5f * z) : sqrtf(sp);
     l = z < -80.f ? 0.5f : sigmoidf_(z) / (2.f * sp);
     if (z != z) s = l = z;  // fmaxf drops a NaN
   }
@@ -101,7 +98,7 @@ __global__ void __launch_bounds__(kThreads)
       if (id[q] < 0 || id[q] >= E) id[q] = -1, g[q] = 0.f;  // no expert: takes no part
       z[q] = id[q] >= 0 ? load_any(logits, row + id[q], dt) : -INFINITY;
     }
-    const float m = renorm ? warp_max(fmaxf(z[0], z[1])) : 0.f;
+    const float m = scoring == MOE_SCORING_SOFTMAX ? warp_max(fmaxf(z[0], z[1])) : 0.f;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       if (id[q] < 0 || z[q] == -INFINITY) continue;  // a masked expert's score is zero
@@ -109,12 +106,22 @@ __global__ void __launch_bounds__(kThreads)
         s[q] = expf(z[q] - m);
         l[q] = 1.f;
       } else {
-        score_of(scoring, z[q], fminf(m, 0.f), s[q], l[q]);
+        score_of(scoring, z[q], s[q], l[q]);
       }
     }
     float mean = 0.f;  // sum_k g_k v_k
     if (renorm) {
-      const float sum = warp_sum(s[0] + s[1]);
+      float sum = warp_sum(s[0] + s[1]);
+      if (sum < 1e-15f && scoring != MOE_SCORING_SOFTMAX) {
+        // Every chosen logit is below -34 (sqrt_softplus -69), where the scores are exp(z)
+        // and exp(z / 2) to the last bit and underflow from -89 and -207 on: the same
+        // ratios from the differences to the highest.
+        const float top = warp_max(fmaxf(z[0], z[1]));
+        const float h = scoring == MOE_SCORING_SIGMOID ? 1.f : 0.5f;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) s[q] = z[q] == -INFINITY ? 0.f : expf(h * (z[q] - top));
+        sum = warp_sum(s[0] + s[1]);
+      }
 #pragma unroll
       for (int q = 0; q < 2; ++q)  // (no weight where every chosen expert is masked)
         s[q] = id[q] >= 0 && sum != 0.f ? s[q] / sum : 0.f;
