@@ -706,7 +706,8 @@ moe_status moe_permute_backward(const void* d_expert_input, const int32_t* route
  *   seg_end [E] i32 or NULL (then E is ignored).
  * With seg_end, rows at and past seg_end[E-1] are neither read nor written.
  * codes and scales 16-byte aligned (MOE_ERR_UNSUPPORTED otherwise);
- * M * N1p < 2^34. */
+ * M * N1p < 2^34.  Any F; multiples of 32 with p and out 16-byte aligned take the
+ * kernel of whole blocks, the others one that is three to four times slower. */
 moe_status moe_act_checkpoint(const void* p, const int32_t* seg_end, int M, int F, int E,
                               moe_dtype dtype, const moe_act_params* act, void* out, void* codes,
                               void* scales, cudaStream_t stream);

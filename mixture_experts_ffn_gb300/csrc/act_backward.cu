@@ -298,9 +298,11 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
   return m;
 }
 
-// F % 32 == 0, p and out 16-byte aligned.  A 32-column block of the checkpoint is
-// four lanes (two when gate and up are interleaved: 16 columns a lane), which
-// agree on its scale with shuffles; a block never straddles rows or halves.
+// F % 32 == 0, p and out 16-byte aligned (other widths, and other starts, go a lane a
+// column through act_checkpoint_any: 65536 x 720 silu bf16 218 us, 65536 x 704 here 65;
+// 65536 x 360 120, its floor 29).  A 32-column block of the checkpoint is four lanes
+// (two when gate and up are interleaved: 16 columns a lane), which agree on its scale
+// with shuffles; a block never straddles rows or halves.
 template <typename T, int FORM>
 __global__ void __launch_bounds__(kThreads)
     act_checkpoint_vec(const T* __restrict__ p, const int32_t* __restrict__ seg_end, int E, int M,

@@ -26,7 +26,12 @@
 //   warp 3        : the bias' gradient, d_bias[e, n] = the sum of d[m, n], beside the
 //                   products: 32 columns of an expert at a time, from global memory
 //                   (a launch of its own for it cost 8 us of 109 at 999 rows, 2880 x
-//                   2880, where d is a hundredth of what is written)
+//                   2880, where d is a hundredth of what is written).  One warp walks
+//                   all rows of its columns, 64 a round, also where the products are
+//                   cut into parts: free at 31 rows an expert (90 us with and without),
+//                   not where they are many (256 on each of 32, 2048 x 1024, 39 us
+//                   without and 87 with; 1024 on each of 8, 7168 x 2048, 160 and 249;
+//                   16384 of one expert, 512 x 512, 23 and 134)
 //   warps 4..11   : epilogue of the CTA's 128 TMEM lanes, 64 columns at a time
 // Tiles are as long as their expert has rows, and SMs write at unequal rates, so a
 // pair takes the next tile from a counter (in the workspace's status area; the
@@ -45,15 +50,15 @@
 // the rows are cut into `parts` equal pieces, each a tile of its own whose float32 sums
 // go to the workspace, and a second launch adds them up in order (wgrad_parts).
 //
-// What bounds it: with many rows an expert a stage takes 590 to 620 cycles for MMAs of
-// 512, with or without the copies: shared memory carries 32 KB in and 48 KB out to the
-// MMAs, 640 cycles at 128 bytes each.  (The issuing lane itself waits 98 cycles a stage
-// and issues for 342; one elected lane of a converged warp issues in 251, waits longer,
-// and the whole gains 1% or nothing.  Stages of 32 rows take it 600 cycles as well: 252
-// us instead of 149 on 8 experts of 1024 rows, 7168 x 2048.)  The ring's depth counts,
-// since 32 KB a stage into each SM is most of what L2 delivers (4 stages 1328 us, 5
-// stages 1204, 6 stages 1165, 64 uneven experts), more than a second buffer for the
-// stores (with 5 stages: 1223).  At 32 rows an expert writing d_w bounds (6 TB/s).
+// What was measured of it: with many rows an expert a stage takes 590 to 620 cycles for
+// MMAs of 512, with or without the copies into shared memory, so these are not what
+// holds it up; what does was not established.  (The issuing lane itself waits 98 cycles
+// a stage and issues for 342; one elected lane of a converged warp issues in 251, waits
+// longer, and the whole gains 1% or nothing.  Stages of 32 rows take it 600 cycles as
+// well: 252 us instead of 149 on 8 experts of 1024 rows, 7168 x 2048.)  The ring's depth
+// counts, since 32 KB a stage into each SM is most of what L2 delivers (4 stages 1328
+// us, 5 stages 1204, 6 stages 1165, 64 uneven experts), more than a second buffer for
+// the stores (with 5 stages: 1223).  At 32 rows an expert writing d_w bounds (6 TB/s).
 #include <cuda.h>
 
 #include <algorithm>
@@ -656,9 +661,9 @@ __global__ void __launch_bounds__(256)
 // Pieces that an expert's rows are cut into: as many as there are SM pairs for the
 // tiles of all experts, of 256 rows at least (on average), and one where that shortens a
 // tile by less than 1200 rows, since the partial sums and the second launch cost 3 us or
-// more: 2 experts of 6639 rows, 544 x 288, 17.7 us in 6 pieces, 38.5 in one; one of 8192,
-// 1024 x 1024, 22 in 4 and 46; but one of 1024, 13.1 in 4 and 12.3, and 4 of 1024, 512 x
-// 1024, 14.9 in 2 and 12.4.
+// more (all without a bias): 2 experts of 6639 rows, 544 x 288, 17.7 us in 6 pieces,
+// 38.5 in one; one of 8192, 1024 x 1024, 22 in 4 and 46; but one of 1024, 13.1 in 4 and
+// 12.3, and 4 of 1024, 512 x 1024, 14.9 in 2 and 12.4.
 // One expert may have nearly all of the rows, whatever their average: a piece is cut to
 // 2^26 of them at most, a million stages of 0.3 us, since the drain waits for a piece's
 // sum and a wait ends after 2 s (2^30 rows in one piece would take 5).
